@@ -347,6 +347,100 @@ W8A8_API w8a8_status moe_layer(const void* x, const float* x_scale, const int64_
 W8A8_API int64_t moe_layer_workspace_offset(int64_t T, int64_t k, int64_t H, int64_t I, int64_t E, int which);
 
 /* ------------------------------------------------------------------------ */
+/* Expert router: router logits -> topk_ids and topk_weights, as moe_layer   */
+/* and moe_fp8_layer take them.  Per token, over E experts:                  */
+/*   live    an expert whose logit is above -inf (-inf or NaN masks it)      */
+/*   s       sigmoid: 1 / (1 + exp(-l)); softmax: exp(l - m) / S over the    */
+/*           live experts (m their largest logit, S the sum)                 */
+/*   key     s + bias[e] where a bias is given, else s; masked experts (and  */
+/*           keys of -inf or NaN) rank below all others                      */
+/*   groups  n_group runs of E / n_group experts; a group's score is its     */
+/*           largest key, or with W8A8_GATE_GROUP_TOP2 the sum of its two    */
+/*           largest (a masked second counts 0); the topk_group best stay    */
+/*   choice  the k largest keys of the groups that stay, in falling order;   */
+/*           equal keys and equal groups by the lowest index (softmax        */
+/*           without a bias compares exp(l - m)); when only masked experts   */
+/*           are left they are taken by index with weight 0, so the ids of a */
+/*           token are always k distinct experts                             */
+/*   weight  s of the choice, with W8A8_GATE_RENORM divided by the token's   */
+/*           sum (0 where the sum is 0), times routed_scale                  */
+/* ------------------------------------------------------------------------ */
+
+#define W8A8_GATE_SIGMOID 1u     /* sigmoid scores (else softmax) */
+#define W8A8_GATE_GROUP_TOP2 2u  /* a group's score is the sum of its two largest keys (else the largest) */
+#define W8A8_GATE_RENORM 4u      /* weights divided by their sum */
+#define W8A8_GATE_BF16 8u        /* logits are bf16 (else fp32) */
+#define W8A8_GATE_MAX_K 32
+#define W8A8_GATE_MAX_GROUPS 32
+
+/* logits [T,E] fp32 (or bf16), bias [E] fp32 or NULL -> topk_ids int64 [T,k],
+ * topk_weights fp32 [T,k].  1 <= E <= W8A8_MAX_EXPERTS, E % n_group == 0,
+ * n_group <= W8A8_GATE_MAX_GROUPS, 1 <= topk_group <= n_group, 1 <= k <=
+ * min(W8A8_GATE_MAX_K, topk_group * E / n_group), T * max(E, k) <= INT32_MAX.
+ * No alignment beyond the element's. */
+W8A8_API w8a8_status moe_gate_topk(const void* logits, int64_t T, int64_t E, const float* bias, int64_t n_group,
+                                   int64_t topk_group, int64_t k, float routed_scale, uint32_t flags,
+                                   int64_t* topk_ids, float* topk_weights, w8a8_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Block-scaled FP8: E4M3 codes with one fp32 scale per 128 values of an     */
+/* activation row and per 128 x 128 block of a weight (rows of a weight are  */
+/* output channels).  The last block of a row or of a weight's channels may  */
+/* be shorter: ceil(K/128) scales a row, ceil(N/128) x ceil(K/128) a weight. */
+/* Weights are used as they lie in a checkpoint; there is nothing to pack.   */
+/* ------------------------------------------------------------------------ */
+
+/* x [M,K] bf16 -> q [M,K] E4M3 bytes, scale [M, ceil(K/128)] fp32: per block
+ * s = max |x| / 448 (binary32 divide), q = E4M3(RN(x / s)), nearest even.  A
+ * block of zeros gets s = 0 and codes 0; the maximum passes NaNs over, a NaN
+ * gets the NaN code; with an infinity s = inf, finite values get code 0 and
+ * infinities the NaN code.  K % 16 == 0, x and q 16-byte aligned. */
+W8A8_API w8a8_status w8a8_fp8_quant(const uint16_t* x, int64_t M, int64_t K, uint8_t* q, float* scale,
+                                    w8a8_stream_t stream);
+
+/* y13 [R,2I] bf16 (gate channels [0,I), up channels [I,2I)) -> q [R,I] E4M3,
+ * scale [R, ceil(I/128)]: the same quantisation of h = (g * sigmoid(g)) * u,
+ * which stays binary32 (not rounded to bf16 first).  exp and the reciprocal
+ * are within a few binary32 units in the last place. */
+W8A8_API w8a8_status w8a8_fp8_swiglu_quant(const uint16_t* y13, int64_t R, int64_t I, uint8_t* q, float* scale,
+                                           w8a8_stream_t stream);
+
+W8A8_API size_t w8a8_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* q [M,K] E4M3, x_scale [M, ceil(K/128)], w [N,K] E4M3, w_scale [ceil(N/128),
+ * ceil(K/128)], bias [N] bf16 or NULL -> y [M,N] bf16:
+ * y[m,n] = bf16( sum_b (x_scale[m,b] w_scale[n/128,b]) sum_{k in b} q[m,k] w[n,k] + bias[n] ),
+ * products and sums in binary32 (so within a bound of the exact value, not bit-
+ * exact; two calls on the same inputs give the same bits).  K % 16 == 0, q and
+ * w 16-byte aligned.  ws: zero-filled, at least the bytes above. */
+W8A8_API w8a8_status w8a8_fp8_matmul(const uint8_t* q, const float* x_scale, int64_t M, int64_t K, const uint8_t* w,
+                                     const float* w_scale, int64_t N, const uint16_t* bias, uint16_t* y, void* ws,
+                                     size_t ws_bytes, w8a8_stream_t stream);
+
+W8A8_API size_t w8a8_fp8_grouped_matmul_workspace_bytes(int64_t E, int64_t R, int64_t N, int64_t K);
+
+/* The same for rows grouped by expert (group_list as in w8a8_grouped_matmul):
+ * w [E,N,K], w_scale [E, ceil(N/128), ceil(K/128)], rows of expert e use w[e].
+ * Counts < 0 or a sum != R set W8A8_ERR_GROUP_LIST on the device and write
+ * nothing.  E * N <= INT32_MAX. */
+W8A8_API w8a8_status w8a8_fp8_grouped_matmul(const uint8_t* q, const float* x_scale, const int64_t* group_list,
+                                             int64_t E, int64_t R, int64_t K, const uint8_t* w, const float* w_scale,
+                                             int64_t N, uint16_t* y, void* ws, size_t ws_bytes,
+                                             w8a8_stream_t stream);
+
+/* The MoE layer on block-scaled FP8 weights, from token rows and router output:
+ * route -> each token quantised once and copied to its routed rows -> W13 ->
+ * SwiGLU + quantisation -> W2 -> combine (as moe_unpermute_combine).
+ * x [T,H] bf16, topk_ids int64 [T,k], topk_weights fp32 [T,k], w13 [E,2I,H]
+ * (gate rows, then up rows; its scale blocks run over the 2I rows), w2 [E,H,I]
+ * -> y [T,H] bf16.  H % 16 == 0, I % 16 == 0.  Device errors as in moe_layer. */
+W8A8_API size_t moe_fp8_layer_workspace_bytes(int64_t T, int64_t k, int64_t H, int64_t I, int64_t E);
+W8A8_API w8a8_status moe_fp8_layer(const uint16_t* x, const int64_t* topk_ids, const float* topk_weights, int64_t T,
+                                   int64_t k, int64_t E, int64_t H, int64_t I, const uint8_t* w13,
+                                   const float* w13_scale, const uint8_t* w2, const float* w2_scale, void* ws,
+                                   size_t ws_bytes, uint16_t* y, w8a8_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Dense quantised matmul without a caller workspace.  The pages have no     */
 /* counterpart: this exists for callers that cannot allocate device memory   */
 /* (a plugin interface without an allocator, a host that reserved all HBM    */

@@ -48,6 +48,15 @@ SIGNATURES = {
     "moe_layer": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp,
                          _vp]),
     "moe_layer_workspace_offset": (_i64, [_i64, _i64, _i64, _i64, _i64, _int]),
+    "moe_gate_topk": (_int, [_vp, _i64, _i64, _vp, _i64, _i64, _i64, ctypes.c_float, _u32, _vp, _vp, _vp]),
+    "w8a8_fp8_quant": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+    "w8a8_fp8_swiglu_quant": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+    "w8a8_fp8_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "w8a8_fp8_matmul": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "w8a8_fp8_grouped_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "w8a8_fp8_grouped_matmul": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "moe_fp8_layer_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "moe_fp8_layer": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
     "w8a8_quant_matmul_noalloc": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp]),
     "w8a8_quant_matmul_noalloc_status": (_int, [_vp]),
     "w8a8_read_device_status": (_int, [_vp, _vp]),
@@ -61,6 +70,7 @@ STATUS = {0: "W8A8_OK", 1: "W8A8_ERR_NULL", 2: "W8A8_ERR_SHAPE", 3: "W8A8_ERR_AL
 STATUS_BYTES = 256
 W8A8_OK, W8A8_ERR_WORKSPACE, W8A8_ERR_DEVICE_TIMEOUT, W8A8_ERR_PACKED = 0, 4, 6, 9
 PACK_GATE_UP = 1
+GATE_SIGMOID, GATE_GROUP_TOP2, GATE_RENORM, GATE_BF16 = 1, 2, 4, 8
 PACK_F16 = 2
 
 _lib = None

@@ -1,0 +1,211 @@
+// fp8_quant.cu -- rows to E4M3 codes with one binary32 scale per 128 values.
+//
+// The dynamic half of the block-scaled FP8 path: a row of K values is cut
+// into blocks of 128 (the last one may be shorter); per block
+//   s = max |v| / 448 (binary32 divide),  q = E4M3(RN(v / s)),
+// rounded to nearest, ties to even (448 is the largest E4M3 value).  A block
+// of zeros gets s = 0 and codes 0.  The maximum passes NaNs over; a NaN value
+// gets the NaN code.  A block holding an infinity has s = inf: its finite
+// values get code 0 and its infinities the NaN code.
+//
+// Two sources: BF16 rows, and the SwiGLU of a BF16 row [gate | up] of 2K,
+//   v = (g * sigmoid(g)) * u, sigmoid(g) = 1 / (1 + exp(-g)),
+// kept in binary32 into the quantisation (one rounding, to E4M3).  And two
+// destinations: the same row, or the k routed rows of a token.
+//
+// Memory-bound: 2 (plain) or 4 (SwiGLU) bytes read and 1 written per value,
+// 1/32 byte of scale.  Eight lanes own a block, 16 values each, so a lane's
+// codes leave as one 16-byte store; the block's maximum meets through three
+// shuffles.
+#include "kernels.cuh"
+
+namespace w8a8 {
+
+namespace {
+
+constexpr int kB = 128;          // values per scale
+constexpr int kLanes = 8;        // lanes per block
+constexpr int kPer = kB / kLanes;
+
+__device__ __forceinline__ void pdl_enter() {
+  pdl_trigger();
+  pdl_wait();
+}
+
+__device__ __forceinline__ uint4 ldg_stream16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
+// Two binary32 values -> two E4M3 bytes (nearest even, saturating), lo in the low byte.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 16 bf16 of two 16-byte words, widened.
+__device__ __forceinline__ void widen16(const uint4& a, const uint4& b, float (&v)[kPer]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// silu(g) * u.  exp and the reciprocal are the fast ones (a few units in the last place): the result is
+// rounded to three mantissa bits next.
+__device__ __forceinline__ float swiglu_fast(float g, float u) {
+  return g * __fdividef(1.0f, 1.0f + __expf(-g)) * u;
+}
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+// The codes of 16 values under scale s.  For s in [2^-100, 2^100] the quotient comes from the reciprocal
+// product with one correction (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990): y0 = RN(v * rs), y = RN(y0 + (v - y0 * s) * rs).  In that range the steps commute with
+// powers of two, so whether the code equals E4M3(RN(v / s)) depends only on the mantissas of v and of the
+// block's maximum and on their distance in exponent: every such triple of bf16 values agrees.
+__device__ __forceinline__ uint4 codes16(const float (&v)[kPer], float s) {
+  uint32_t c[4];
+  if (s >= 0x1p-100f && s <= 0x1p100f) {
+    const float rs = __frcp_rn(s);
+    const uint64_t rs2 = pair(rs, rs), ns2 = pair(-s, -s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = 0u;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint64_t x2 = pair(v[4 * i + 2 * h], v[4 * i + 2 * h + 1]);
+        uint64_t y0, r2, y2;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y0) : "l"(x2), "l"(rs2));
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r2) : "l"(y0), "l"(ns2), "l"(x2));
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y2) : "l"(r2), "l"(rs2), "l"(y0));
+        float lo, hi;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(y2));
+        c[i] |= to_e4m3x2(lo, hi) << (16 * h);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = 0u;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float a = v[4 * i + 2 * h], b = v[4 * i + 2 * h + 1];
+        // a block of zeros: +0, or NaN for a NaN value
+        const float lo = s == 0.0f ? __fadd_rn(__fmul_rn(a, 0.0f), 0.0f) : __fdiv_rn(a, s);
+        const float hi = s == 0.0f ? __fadd_rn(__fmul_rn(b, 0.0f), 0.0f) : __fdiv_rn(b, s);
+        c[i] |= to_e4m3x2(lo, hi) << (16 * h);
+      }
+    }
+  }
+  return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// Block b of the M * KB blocks: row b / KB, values [128 kb, 128 kb + 128) of it, kb = b % KB.  `dst` (or
+// nullptr): the k routed rows dst[row * k + j] of a token row; an index < 0 is skipped.
+template <bool SWIGLU, bool SCATTER>
+__global__ void __launch_bounds__(256) fp8_quant_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K, int KB,
+                                                        uint8_t* __restrict__ q, float* __restrict__ scale,
+                                                        const int32_t* __restrict__ dst, int k) {
+  pdl_enter();
+  const int64_t nblk = M * KB;
+  const int sub = threadIdx.x % kLanes;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (256 / kLanes);
+  // whole warps stay in the loop together: the shuffles below take the full mask
+  for (int64_t b0 = static_cast<int64_t>(blockIdx.x) * (256 / kLanes) + (threadIdx.x / 32) * (32 / kLanes); b0 < nblk;
+       b0 += step) {
+    const int64_t b = b0 + (threadIdx.x % 32) / kLanes;
+    const bool in_blk = b < nblk;
+    int64_t row;
+    int kb;
+    if (nblk <= 0xffffffffll) {  // 32-bit division where it fits
+      const uint32_t r32 = static_cast<uint32_t>(b) / static_cast<uint32_t>(KB);
+      row = r32;
+      kb = static_cast<int>(static_cast<uint32_t>(b) - r32 * static_cast<uint32_t>(KB));
+    } else {
+      row = b / KB;
+      kb = static_cast<int>(b - row * KB);
+    }
+    const int64_t col = static_cast<int64_t>(kb) * kB + sub * kPer;
+    const bool in = in_blk && col < K;  // K % 16 == 0: a lane's 16 values are all inside or all outside
+    float v[kPer];
+    if (in) {
+      if constexpr (SWIGLU) {
+        const uint16_t* g = x + row * 2 * K + col;
+        const uint4 g0 = ldg_stream16(g), g1 = ldg_stream16(g + 8);
+        const uint4 u0 = ldg_stream16(g + K), u1 = ldg_stream16(g + K + 8);
+        float u[kPer];
+        widen16(g0, g1, v);
+        widen16(u0, u1, u);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) v[i] = swiglu_fast(v[i], u[i]);
+      } else {
+        const uint16_t* p = x + row * K + col;
+        const uint4 a = ldg_stream16(p), c = ldg_stream16(p + 8);
+        widen16(a, c, v);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
+    }
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) amax = fmaxf(amax, fabsf(v[i]));  // fmaxf passes a NaN over
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float s = __fdiv_rn(amax, 448.0f);
+    const uint4 c = codes16(v, s);
+    if constexpr (SCATTER) {
+      if (in_blk) {
+        for (int j = 0; j < k; ++j) {
+          const int64_t r = dst[row * k + j];
+          if (r < 0) continue;
+          if (in) *reinterpret_cast<uint4*>(q + r * K + col) = c;
+          if (sub == 0) scale[r * KB + kb] = s;
+        }
+      }
+    } else {
+      if (in) *reinterpret_cast<uint4*>(q + row * K + col) = c;
+      if (in_blk && sub == 0) scale[row * KB + kb] = s;
+    }
+  }
+}
+
+template <bool SWIGLU, bool SCATTER>
+cudaError_t launch_t(const uint16_t* x, int64_t M, int64_t K, uint8_t* q, float* scale, const int32_t* dst, int k,
+                     cudaStream_t stream, int num_sms) {
+  if (M == 0) return cudaSuccess;
+  const int KB = static_cast<int>((K + kB - 1) / kB);
+  const int64_t ctas = (M * KB + 256 / kLanes - 1) / (256 / kLanes);
+  const int64_t grid = std::min<int64_t>(ctas, static_cast<int64_t>(num_sms) * 8);
+  return launch_pdl(fp8_quant_kernel<SWIGLU, SCATTER>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, x, M,
+                    K, KB, q, scale, dst, k);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_quant(const uint16_t* x, int64_t M, int64_t K, uint8_t* q, float* scale, cudaStream_t stream,
+                             int num_sms) {
+  return launch_t<false, false>(x, M, K, q, scale, nullptr, 0, stream, num_sms);
+}
+
+cudaError_t launch_fp8_quant_scatter(const uint16_t* x, int64_t T, int64_t K, const int32_t* dst, int k, uint8_t* q,
+                                     float* scale, cudaStream_t stream, int num_sms) {
+  return launch_t<false, true>(x, T, K, q, scale, dst, k, stream, num_sms);
+}
+
+cudaError_t launch_fp8_swiglu_quant(const uint16_t* y13, int64_t R, int64_t I, uint8_t* q, float* scale,
+                                    cudaStream_t stream, int num_sms) {
+  return launch_t<true, false>(y13, R, I, q, scale, nullptr, 0, stream, num_sms);
+}
+
+}  // namespace w8a8

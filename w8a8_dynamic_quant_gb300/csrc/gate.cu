@@ -1,0 +1,251 @@
+// gate.cu -- expert router: logits [T,E] -> the k chosen experts of each
+// token and their weights (the topk_ids and topk_weights of the MoE layers).
+//
+//   live     an expert whose logit is above -inf (a NaN or -inf logit masks it)
+//   score    sigmoid: s = 1 / (1 + exp(-l)); softmax: s = exp(l - m) / S over
+//            the live experts, m their largest logit, S the sum
+//   key      s + bias where a bias is given, else s (softmax: exp(l - m), the
+//            same order); a masked expert, or a key of -inf or NaN, ranks below
+//            every other
+//   groups   n_group runs of E / n_group experts; a group's score is its largest
+//            key, or the sum of its two largest ("top2"; a second key that is
+//            masked counts 0); the topk_group best groups stay
+//   choice   the k largest keys of those groups in falling order, ties to the
+//            lowest index; slots that only masked experts are left for take
+//            them by index
+//   weight   s of the chosen (0 for a masked one); renormalised: divided by
+//            their sum (0 where the sum is 0); times routed_scale
+//
+// exp, the reciprocal and every sum that decides an order are binary32
+// operations rounded as the formulas read, so that equal keys are equal
+// bit for bit.  S is summed with the rounding errors carried along (Knuth's
+// two-sum), so that its last bit does not depend on the order of the sum.
+//
+// One warp per token; lane l holds the experts [l * P, l * P + P), P = the
+// experts per lane.  A choice is the warp's maximum of the lanes' best keys
+// (as order-preserving integers), the lowest lane holding it, and a new best of
+// that lane.  Traffic is one read of the logits and 12 bytes per choice.
+#include "kernels.cuh"
+
+namespace w8a8 {
+
+namespace {
+
+constexpr int kGateWarps = 4;
+constexpr float kNegInf = -INFINITY;
+
+// Order-preserving map of binary32 (no NaN) to unsigned: larger values get larger integers; 0 is below all.
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+constexpr uint32_t kOrderedNegInf = 0x007fffffu;  // ordered(-inf)
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
+  if constexpr (BF16) return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
+  else return static_cast<const float*>(p)[i];
+}
+
+__device__ __forceinline__ float sigmoid_rn(float x) { return __frcp_rn(__fadd_rn(1.0f, expf(-x))); }
+
+// a + b as the rounded sum s and its error e, exactly (Knuth, TAOCP vol. 2, 4.2.2).
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+  s = __fadd_rn(a, b);
+  const float t = __fsub_rn(s, a);
+  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+}
+
+struct GateArgs {
+  const void* logits;
+  const float* bias;
+  int64_t T;
+  int E, k, n_group, topk_group;
+  bool top2, renorm;
+  float scale;
+  int64_t* ids;
+  float* weights;
+};
+
+template <int P, bool BF16, bool SIGMOID>
+__global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ uint32_t s_gkey[kGateWarps][W8A8_MAX_EXPERTS];
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
+  if (t >= a.T) return;
+  const int E = a.E;
+  const int64_t row = t * E;
+  float l[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int e = lane * P + i;
+    l[i] = e < E ? load_logit<BF16>(a.logits, row + e) : kNegInf;
+    if (!(l[i] > kNegInf)) l[i] = kNegInf;  // NaN
+  }
+  float m = kNegInf, S = 0.0f;
+  uint32_t key[P];
+  if constexpr (SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int e = lane * P + i;
+      float s = sigmoid_rn(l[i]);
+      if (a.bias != nullptr && e < E) s = __fadd_rn(s, a.bias[e]);
+      key[i] = (l[i] > kNegInf && s > kNegInf) ? ordered(s) : kOrderedNegInf;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) m = fmaxf(m, l[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float ex[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      ex[i] = !(l[i] > kNegInf) ? 0.0f : l[i] == m ? 1.0f : expf(__fsub_rn(l[i], m));
+    if (a.bias != nullptr || !a.renorm) {
+      float err = 0.0f;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        float e;
+        two_sum(S, ex[i], S, e);
+        err += e;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float S2 = __shfl_xor_sync(0xffffffffu, S, o), err2 = __shfl_xor_sync(0xffffffffu, err, o);
+        float e;
+        two_sum(S, S2, S, e);
+        err = err + err2 + e;
+      }
+      S = __fadd_rn(S, err);
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int e = lane * P + i;
+      float s = ex[i];
+      if (a.bias != nullptr && e < E) s = __fadd_rn(__fdiv_rn(s, S), a.bias[e]);
+      key[i] = (l[i] > kNegInf && s > kNegInf) ? ordered(s) : kOrderedNegInf;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (lane * P + i >= E) key[i] = 0u;
+
+  if (a.topk_group < a.n_group) {
+    // group scores: lane g scans group g's keys (n_group <= 32)
+    uint32_t* sk = s_gkey[warp];
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (lane * P + i < E) sk[lane * P + i] = key[i];
+    __syncwarp();
+    const int gs = E / a.n_group;
+    uint32_t gk = 0u;
+    if (lane < a.n_group) {
+      uint32_t k1 = 0u, k2 = 0u;
+      for (int j = 0; j < gs; ++j) {
+        const uint32_t v = sk[lane * gs + j];
+        k2 = max(k2, min(k1, v));
+        k1 = max(k1, v);
+      }
+      gk = k1;
+      if (a.top2 && k1 > kOrderedNegInf)
+        gk = ordered(__fadd_rn(unordered(k1), k2 > kOrderedNegInf ? unordered(k2) : 0.0f));
+    }
+    uint32_t keep = 0u;
+    for (int j = 0; j < a.topk_group; ++j) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, gk);
+      const unsigned who = __ballot_sync(0xffffffffu, gk == best);
+      const int g = __ffs(who) - 1;
+      keep |= 1u << g;
+      if (lane == g) gk = 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int e = lane * P + i;
+      if (e < E && !((keep >> (e / gs)) & 1u)) key[i] = 0u;
+    }
+  }
+
+  // the k largest keys; lane j keeps choice j
+  uint32_t best = 0u;
+  int at = 0;
+  auto local_best = [&]() {
+    best = key[0];
+    at = 0;
+#pragma unroll
+    for (int i = 1; i < P; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
+      }
+  };
+  local_best();
+  int my_id = 0;
+  uint32_t my_key = 0u;
+  for (int j = 0; j < a.k; ++j) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const int w = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+    const int id = __shfl_sync(0xffffffffu, lane * P + at, w);
+    if (lane == j) {
+      my_id = id;
+      my_key = top;
+    }
+    if (lane == w) {
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (i == at) key[i] = 0u;
+      local_best();
+    }
+  }
+  float wgt = 0.0f;
+  if (lane < a.k && my_key > kOrderedNegInf) {
+    const float x = load_logit<BF16>(a.logits, row + my_id);
+    if constexpr (SIGMOID) wgt = sigmoid_rn(x);
+    else wgt = x == m ? 1.0f : expf(__fsub_rn(x, m));
+  }
+  if (a.renorm) {
+    float d = wgt;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    wgt = d > 0.0f ? __fdiv_rn(wgt, d) : 0.0f;
+  } else if constexpr (!SIGMOID) {
+    wgt = S > 0.0f ? __fdiv_rn(wgt, S) : 0.0f;
+  }
+  if (lane < a.k) {
+    a.ids[t * a.k + lane] = my_id;
+    a.weights[t * a.k + lane] = wgt * a.scale;
+  }
+}
+
+template <int P>
+cudaError_t launch_p(const GateArgs& a, bool bf16, bool sigmoid, cudaStream_t stream) {
+  const dim3 g(static_cast<unsigned>((a.T + kGateWarps - 1) / kGateWarps)), b(32 * kGateWarps);
+  if (bf16) {
+    return sigmoid ? launch_pdl(gate_kernel<P, true, true>, g, b, 0, stream, a)
+                   : launch_pdl(gate_kernel<P, true, false>, g, b, 0, stream, a);
+  }
+  return sigmoid ? launch_pdl(gate_kernel<P, false, true>, g, b, 0, stream, a)
+                 : launch_pdl(gate_kernel<P, false, false>, g, b, 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_gate(const void* logits, bool bf16, int64_t T, int E, const float* bias, bool sigmoid, int n_group,
+                        int topk_group, bool top2, int k, bool renorm, float scale, int64_t* ids, float* weights,
+                        cudaStream_t stream) {
+  if (T == 0) return cudaSuccess;
+  const GateArgs a{logits, bias, T, E, k, n_group, topk_group, top2, renorm, scale, ids, weights};
+  if (E <= 32) return launch_p<1>(a, bf16, sigmoid, stream);
+  if (E <= 64) return launch_p<2>(a, bf16, sigmoid, stream);
+  if (E <= 128) return launch_p<4>(a, bf16, sigmoid, stream);
+  if (E <= 256) return launch_p<8>(a, bf16, sigmoid, stream);
+  if (E <= 512) return launch_p<16>(a, bf16, sigmoid, stream);
+  return launch_p<32>(a, bf16, sigmoid, stream);
+}
+
+}  // namespace w8a8
