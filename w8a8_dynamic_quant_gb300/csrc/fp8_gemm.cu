@@ -1,13 +1,42 @@
-// fp8_gemm.cu -- block-scaled FP8 contraction, dense and grouped by expert.
+// fp8_gemm.cu -- block-scaled FP8 contraction on the 5th-generation tensor
+// cores (tcgen05.mma.cta_group::2.kind::f8f6f4), dense and grouped by expert.
 //
 //   y[m,n] = bf16( sum_b xs[m,b] * ws[n / 128, b] * sum_{k in block b} q[m,k] * w[n,k]  (+ bias[n]) )
 //
 // q [R,K] E4M3 rows with a binary32 scale per 128 values, w [E,N,K] E4M3 with
-// a binary32 scale per 128 x 128 block.  The product of a block is summed in
-// binary32 by the tensor core, scaled by xs * ws and added into binary32 sums.
+// a binary32 scale per 128 x 128 block.  The scales are arbitrary binary32
+// numbers, so the tensor core cannot apply them (its block scales are powers
+// of two): every 128-deep block is one accumulator of its own, which the
+// epilogue warps drain, multiply by xs * ws and add into binary32 sums held in
+// registers, while the MMAs of the next blocks fill other accumulators.
 //
-// 64 x 64 output tiles on the warp-level FP8 instruction, one 128-deep block
-// at a time through shared memory.
+// Tile.  The weights are the MMA's M side, 256 output channels per CTA pair
+// (128 in each CTA: one weight scale per CTA and block), and a block of up to
+// NT tokens is N, sized to the tokens there are in steps of 16: the even CTA
+// holds the first half of the block's token rows, the odd CTA the rest.  So
+// ragged groups pad to 16 rows, not to a tile, and one kernel serves a stream
+// of weights for a few tokens as well as a large product.  A ring stage is one
+// 128-deep block: the CTA's 128 x 128-byte weight tile and its token rows by
+// TMA, 128-byte swizzle.
+//
+// Tensor memory (512 columns): 512 / NT accumulators of NT columns.
+//
+// Warp roles (384 threads, one CTA per SM):
+//   warp 0       TMA producer
+//   warp 1       TMEM owner; the even CTA's issues the MMAs (whole warp, one lane elected)
+//   warps 2-3    scales: xs * ws of four blocks at a time, [block][token], into a shared-memory ring (half of the
+//                tokens each)
+//   warps 4-11   epilogue: warp w reads TMEM lanes 32 * (w % 4) .. (channels) and one half of the tokens
+//
+// Work.  A unit is one tile over the whole of K.  With many units the pairs
+// take every C-th one.  With few, the units' blocks in sequence are cut into C
+// equal runs, one per pair: a run ends and begins inside units, every piece of
+// a cut unit leaves its partial sums in the workspace, and the warp that
+// arrives last at a unit adds the pieces in the order of K and writes the
+// result: no order of arrival changes a bit, and no warp waits for another.
+//
+// Every mbarrier wait is bounded (2 s): on expiry the CTA sets
+// W8A8_ERR_DEVICE_TIMEOUT, lets in-flight copies land, frees TMEM and returns.
 #include "kernels.cuh"
 #include "tc_common.cuh"
 
@@ -15,132 +44,624 @@ namespace w8a8 {
 
 namespace {
 
-constexpr int F_BT = 64, F_BN = 64, F_BK = 128;
-constexpr int F_STRIDE = F_BK + 16;  // padded rows: conflict-free fragment loads
-constexpr int F_THREADS = 128;
+using namespace tc;
 
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+constexpr int F_ROWS = 256;   // output channels per pair tile (MMA M)
+constexpr int F_HALF = 128;   // of them in each CTA
+constexpr int F_BK = 128;     // K per stage and per scale block (bytes = E4M3 values)
+constexpr int F_THREADS = 384;
+constexpr int F_EPI0 = 4;
+constexpr int F_EPI_WARPS = 8;
+constexpr int F_SG = 4;       // blocks per scale group
+constexpr int F_SRING = 2;    // scale groups in the ring
+constexpr int F_MAX_CLUSTERS = 76;
+constexpr int F_MAX_E = 1024;
+constexpr int F_SUPER = 32;   // token blocks per rasterisation group
+constexpr int F_MIN_RUN = 4;  // blocks per run at least
+constexpr uint16_t F_PAIR_MASK = 0x3;
+constexpr uint32_t F_TMEM_COLS = 512;
+constexpr uint32_t F_W_BYTES = F_HALF * F_BK;  // 16 KB
+constexpr uint32_t F_STG_BYTES = F_EPI_WARPS * 16 * 32 * 2;  // output staging: [16 tokens][32 channels] per warp
+
+template <int NT>
+struct Cfg {
+  static constexpr uint32_t kXBytes = NT / 2 * F_BK;
+  static constexpr uint32_t kStageBytes = F_W_BYTES + kXBytes;
+  static constexpr int kStages = NT == 256 ? 6 : NT == 128 ? 8 : NT == 64 ? 9 : 10;
+  static constexpr int kAcc = NT >= 64 ? 512 / NT : 8;   // accumulators
+  static constexpr int kCols = NT / 2;                    // token columns per epilogue warp
+  static constexpr int kChunk = kCols == 64 || kCols == 32 ? 32 : 16;  // columns per tensor-memory load
+  static constexpr int kBig = NT / 2 < 64 ? NT / 2 : 64;  // token rows per large TMA box
+  static constexpr uint32_t kScaleBytes = F_SRING * F_SG * NT * 4;
+  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes + kScaleBytes + F_STG_BYTES + 1024;
+  static constexpr size_t kPiece = static_cast<size_t>(F_EPI_WARPS) * kCols * 32;  // floats of one CTA's partial sums
+};
+
+constexpr size_t kCounterBytes = F_MAX_CLUSTERS * 2 * F_EPI_WARPS * 4;
+static_assert(kCounterBytes % 256 == 0, "pieces start 256-byte aligned");
+
+struct KArgs {
+  const float* xs;
+  const int64_t* group_list;
+  const float* wsc;
+  const uint16_t* bias;
+  uint16_t* y;
+  DeviceStatus* status;
+  uint32_t* counters;  // [clusters][2][epilogue warps], zero between calls
+  float* pieces;       // [clusters][2 slots][2 CTAs][kPiece]
+  int64_t R, N, K;
+  int E;
+};
+
+// D(tmem, both CTAs) (+)= A * B, kind::f8f6f4 with both operands E4M3, on the CTA pair (issued by the elected lane
+// of a converged warp).
+__device__ __forceinline__ void mma_pair_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor: binary32 accumulator, E4M3 operands (format 0), both K-major, M = 256, N = n.
+__device__ __forceinline__ uint32_t idesc_f8(int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(F_ROWS >> 4) << 24);
 }
 
-// Rows [r0, r0 + rows) of a [.., K] byte matrix, columns [k0, k0 + 128), into padded shared rows; outside: 0.
-__device__ __forceinline__ void load_tile(uint8_t* s, const uint8_t* p, int64_t r0, int64_t r_end, int64_t K, int k0) {
-  for (int i = threadIdx.x; i < 64 * 8; i += F_THREADS) {
-    const int r = i >> 3, c = (i & 7) * 16;
-    const bool in = r0 + r < r_end && k0 + c < K;
-    const uint4 v = in ? *reinterpret_cast<const uint4*>(p + (r0 + r) * K + k0 + c) : make_uint4(0u, 0u, 0u, 0u);
-    *reinterpret_cast<uint4*>(s + r * F_STRIDE + c) = v;
+template <int C>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[C]) {
+  static_assert(C == 32 || C == 16, "chunk");
+  if constexpr (C == 32) tmem_ld32(taddr, v);
+  else tmem_ld16(taddr, v);
+}
+
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+// One run of blocks of a unit: the tile and its K range.
+struct Seg {
+  int e, wb;       // expert, 256-channel block
+  int row0;        // first token row (of all R)
+  int tvalid, n;   // tokens, and tokens rounded up to 16
+  int kb0, kb1;    // blocks [kb0, kb1)
+  int unit;
+};
+
+// The sequence of segments of one pair.  Every role walks it on its own.
+struct Walk {
+  int64_t x, end;  // cut: block position; else: unit number
+  int step;        // 0: cut
+  int KB;
+};
+__device__ __forceinline__ int64_t run_begin(int64_t total, int C, int c) { return total * c / C; }
+// The pair whose run holds block position p.
+__device__ __forceinline__ int run_owner(int64_t total, int C, int64_t p) {
+  return static_cast<int>(((p + 1) * C - 1) / total);
+}
+
+template <int NT>
+__device__ __forceinline__ bool next_seg(Walk& w, int E, int WB, const int* s_prefix, const int* s_off, Seg& s) {
+  if (w.x >= w.end) return false;
+  int u;
+  if (w.step == 0) {
+    u = static_cast<int>(w.x / w.KB);
+    s.kb0 = static_cast<int>(w.x - static_cast<int64_t>(u) * w.KB);
+    s.kb1 = static_cast<int>(min(static_cast<int64_t>(w.KB), s.kb0 + (w.end - w.x)));
+    w.x += s.kb1 - s.kb0;
+  } else {
+    u = static_cast<int>(w.x);
+    s.kb0 = 0;
+    s.kb1 = w.KB;
+    w.x += w.step;
+  }
+  s.unit = u;
+  s.e = expert_of(u, E, s_prefix);
+  const int local = u - s_prefix[s.e];
+  const int cnt = s_off[s.e + 1] - s_off[s.e];
+  const int TB = (cnt + NT - 1) / NT;
+  // token blocks in groups of F_SUPER, the channel block outside: the pairs in flight share weight blocks, and the
+  // group's token rows stay in L2 while the weights sweep past
+  const int g = local / (WB * F_SUPER);
+  const int rem = local - g * WB * F_SUPER;
+  const int gt = min(F_SUPER, TB - g * F_SUPER);
+  s.wb = rem / gt;
+  const int tb = g * F_SUPER + rem - s.wb * gt;
+  const int per = ((cnt + TB - 1) / TB + 15) & ~15;  // tokens split evenly over the blocks
+  s.row0 = s_off[s.e] + tb * per;
+  s.tvalid = min(per, cnt - tb * per);
+  s.n = (s.tvalid + 15) & ~15;
+  return true;
+}
+
+// Rows [0, rows) of a warp's staging buffer [rows][32] bf16 to out[(row0 + r) * ld + c0 + c], c < min(32, ld - c0).
+__device__ __forceinline__ void store_rows(const uint16_t* stg, uint16_t* out, int64_t row0, int64_t ld, int64_t c0,
+                                           int rows, int lane) {
+  const int64_t ncols = ld - c0 < 32 ? ld - c0 : 32;
+  if (ncols == 32 && (ld & 7) == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0u) {
+    const int c = (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = (lane >> 2) + 8 * i;
+      if (r < rows)
+        *reinterpret_cast<uint4*>(out + (row0 + r) * ld + c0 + c) = *reinterpret_cast<const uint4*>(stg + r * 32 + c);
+    }
+  } else {
+    for (int r = 0; r < rows; ++r)
+      if (lane < ncols) out[(row0 + r) * ld + c0 + lane] = stg[r * 32 + lane];
   }
 }
 
-__global__ void __launch_bounds__(F_THREADS) fp8_gemm_kernel(const Fp8GemmArgs a) {
-  __shared__ __align__(16) uint8_t sx[F_BT * F_STRIDE];
-  __shared__ __align__(16) uint8_t sw[F_BN * F_STRIDE];
-  __shared__ int64_t s_row0, s_rows;
+template <int NT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
+fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmXbig,
+                const __grid_constant__ CUtensorMap tmXsmall, const KArgs a) {
+  using C = Cfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar_full[C::kStages];   // even CTA: both CTAs' tiles of the stage landed
+  __shared__ __align__(8) uint64_t bar_empty[C::kStages];  // the MMAs reading the stage are done
+  __shared__ __align__(8) uint64_t bar_accf[C::kAcc];      // the block's accumulator is complete
+  __shared__ __align__(8) uint64_t bar_acce[C::kAcc];      // even CTA: both CTAs drained it
+  __shared__ __align__(8) uint64_t bar_scf[F_SRING];       // the group's scales are in shared memory
+  __shared__ __align__(8) uint64_t bar_sce[F_SRING];       // the epilogue warps read them
+  __shared__ uint32_t s_tmem_base;
+  __shared__ volatile int s_abort;
   __shared__ int s_bad;
-  const int e = blockIdx.z;
-  if (threadIdx.x == 0) {
-    int64_t before = 0, sum = 0, mine = a.R;
-    int bad = 0;
-    if (a.group_list != nullptr) {
-      for (int i = 0; i < a.E; ++i) {
-        const int64_t c = a.group_list[i];
-        if (c < 0 || c > a.R) bad = 1;
-        if (i == e) {
-          before = sum;
-          mine = c;
-        }
-        sum += c < 0 ? 0 : c;
-      }
-      if (sum != a.R) bad = 1;
-      if (bad && blockIdx.x == 0 && blockIdx.y == 0 && e == 0) set_status(a.status, W8A8_ERR_GROUP_LIST, 0u);
+  __shared__ int s_prefix[F_MAX_E + 1];
+  __shared__ int s_off[F_MAX_E + 1];
+  __shared__ int s_warp[F_THREADS / 32];
+  __shared__ Seg s_seg[F_EPI_WARPS];    // the epilogue warps' segment and place in the walk: 128 sums a thread leave
+  __shared__ Walk s_walk[F_EPI_WARPS];  // no registers to hold them through the block loop
+  __shared__ unsigned long long s_rows;  // the counts' sum where 32 bits may not hold it
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const int E = a.E;
+  const int64_t N = a.N;
+  const int KB = static_cast<int>((a.K + F_BK - 1) / F_BK);
+  const int WB = static_cast<int>((N + F_ROWS - 1) / F_ROWS);
+
+  uint8_t* stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t stage_base = smem_u32(stages);
+  float* s_scale = reinterpret_cast<float*>(stages + C::kStages * C::kStageBytes);  // [ring][4 blocks][NT]
+  uint16_t* s_out = reinterpret_cast<uint16_t*>(stages + C::kStages * C::kStageBytes + C::kScaleBytes);
+  uint32_t rank, cluster_id, nclusters;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(cluster_id));
+  asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(nclusters));
+
+  if (tid == 0) {
+    s_abort = 0;
+    s_bad = 0;
+    s_rows = 0ull;
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&bar_full[s]), 1);
+      mbar_init(smem_u32(&bar_empty[s]), 1);
     }
-    s_row0 = before;
-    s_rows = mine;
-    s_bad = bad;
+    for (int b = 0; b < C::kAcc; ++b) {
+      mbar_init(smem_u32(&bar_accf[b]), 1);
+      mbar_init(smem_u32(&bar_acce[b]), 2 * F_EPI_WARPS);
+    }
+    for (int s = 0; s < F_SRING; ++s) {
+      mbar_init(smem_u32(&bar_scf[s]), 2);
+      mbar_init(smem_u32(&bar_sce[s]), F_EPI_WARPS);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmXbig);
+    tma_prefetch_desc(&tmXsmall);
   }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem_base)),
+                 "r"(F_TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  __syncthreads();  // s_bad, before the scan may set it
+  pdl_trigger();
+  pdl_wait();
+  GemmArgs ga;
+  ga.group_list = a.group_list;
+  ga.R = a.R;
+  int units;
+  const int rows_total = scan_groups<F_THREADS, F_MAX_E>(
+      ga, E, [WB](int c) { return ((c + NT - 1) / NT) * WB; }, s_off, s_prefix, s_warp, &s_bad, &units);
+  const bool wide = a.R > INT32_MAX / E;
+  if (wide && a.group_list != nullptr)
+    for (int e = tid; e < E; e += F_THREADS)
+      atomicAdd(&s_rows, static_cast<unsigned long long>(max(0ll, static_cast<long long>(a.group_list[e]))));
+  tc_fence_before();
+  cluster_sync_all();  // both CTAs' barriers and tensor memory exist before either touches the other's
+  tc_fence_after();
+  const uint32_t tmem_base = s_tmem_base;
+  if (s_bad || rows_total != a.R || (wide && a.group_list != nullptr && s_rows != static_cast<unsigned long long>(a.R))) {
+    if (tid == 0 && blockIdx.x == 0) set_status(a.status, W8A8_ERR_GROUP_LIST, 0u);
+    units = 0;
+  }
+  // many units: every C-th; few: equal runs of blocks, at least F_MIN_RUN each
+  const int64_t total = static_cast<int64_t>(units) * KB;
+  const int nc = static_cast<int>(nclusters);
+  const bool cut = units < 4 * nc;
+  const int runs = static_cast<int>(min(static_cast<int64_t>(nc), max(static_cast<int64_t>(1), total / F_MIN_RUN)));
+  const int me = static_cast<int>(cluster_id);
+  Walk walk0;
+  walk0.KB = KB;
+  walk0.step = cut ? 0 : nc;
+  walk0.x = !cut ? me : me < runs ? run_begin(total, runs, me) : 0;
+  walk0.end = !cut ? units : me < runs ? run_begin(total, runs, me + 1) : 0;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      Walk w = walk0;
+      Seg s;
+      while (!s_abort && next_seg<NT>(w, E, WB, s_prefix, s_off, s)) {
+        const int xrows = s.n >> 1;
+        const int yx = s.row0 + static_cast<int>(rank) * xrows;
+        const int yw = static_cast<int>(static_cast<int64_t>(s.e) * N) + s.wb * F_ROWS + static_cast<int>(rank) * F_HALF;
+        const uint32_t bytes = 2u * (F_W_BYTES + static_cast<uint32_t>(xrows) * F_BK);
+        for (int kb = s.kb0; kb < s.kb1; ++kb) {
+          if (!mbar_wait(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 1u)) break;
+          const uint32_t full = smem_u32(&bar_full[stage]);
+          if (rank == 0) mbar_expect_tx(full, bytes);
+          const uint32_t full_even = smem_cluster_addr(full, 0);
+          const uint32_t sa = stage_base + stage * C::kStageBytes;
+          tma_load_2d_pair(sa, &tmW, kb * F_BK, yw, full_even);
+          int r = 0;
+          for (; r + C::kBig <= xrows; r += C::kBig)
+            tma_load_2d_pair(sa + F_W_BYTES + r * F_BK, &tmXbig, kb * F_BK, yx + r, full_even);
+          for (; r < xrows; r += 8)
+            tma_load_2d_pair(sa + F_W_BYTES + r * F_BK, &tmXsmall, kb * F_BK, yx + r, full_even);
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Drain: the last fill of every stage has been consumed, so no copy into this CTA and no MMA arrival on its
+      // barriers is still in flight when the cluster leaves.
+      for (int i = 0; i < C::kStages && !s_abort; ++i) {
+        if (!mbar_wait(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 5u)) break;
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- MMA issuer (even CTA, whole warp)
+    if (rank == 0) {
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, bphase = 0;
+      Walk w = walk0;
+      Seg s;
+      bool ok = true;
+      while (ok && !s_abort && next_seg<NT>(w, E, WB, s_prefix, s_off, s)) {
+        const uint32_t idesc = idesc_f8(s.n);
+        for (int kb = s.kb0; kb < s.kb1; ++kb) {
+          if (!warp_wait(smem_u32(&bar_acce[buf]), bphase ^ 1u, &s_abort, a.status, 2u) ||
+              !warp_wait(smem_u32(&bar_full[stage]), phase, &s_abort, a.status, 3u)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = stage_base + stage * C::kStageBytes;
+          const uint64_t adesc = smem_desc_sw128(sa);
+          const uint64_t bdesc = smem_desc_sw128(sa + F_W_BYTES);
+#pragma unroll
+          for (int k = 0; k < F_BK / 32; ++k)
+            mma_pair_f8(tmem_base + buf * NT, adesc + 2u * k, bdesc + 2u * k, idesc, k > 0 ? 1u : 0u);
+          tc_commit_pair_mc(smem_u32(&bar_empty[stage]), F_PAIR_MASK);  // frees the stage in both CTAs
+          tc_commit_pair_mc(smem_u32(&bar_accf[buf]), F_PAIR_MASK);
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++buf == C::kAcc) {
+            buf = 0;
+            bphase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp < F_EPI0) {
+    // ------------------------------------------------------------- scales (both CTAs)
+    constexpr int kPerLane = NT >= 64 ? NT / 64 : 1;
+    const int t0 = lane + (warp - 2) * (NT >= 64 ? NT / 2 : 32);  // NT = 32: the second warp has no token
+    const int NB = static_cast<int>((N + 127) / 128);
+    const bool vec = (KB & 3) == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 15u) == 0u;
+    int slot = 0;
+    uint32_t phase = 0;
+    Walk w = walk0;
+    Seg s;
+    bool ok = true;
+    while (ok && !s_abort && next_seg<NT>(w, E, WB, s_prefix, s_off, s)) {
+      const int nb = s.wb * 2 + static_cast<int>(rank);
+      const float* wrow = a.wsc + (static_cast<int64_t>(s.e) * NB + nb) * KB;
+      for (int g = s.kb0 / F_SG; ok && g * F_SG < s.kb1; ++g) {
+        const int k0 = g * F_SG;
+        float wv[F_SG];
+#pragma unroll
+        for (int j = 0; j < F_SG; ++j) wv[j] = nb < NB && k0 + j < KB ? wrow[k0 + j] : 0.0f;
+        float v[kPerLane][F_SG];
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+          const int t = t0 + 32 * i;
+          const float* p = a.xs + (static_cast<int64_t>(s.row0) + t) * KB + k0;
+          const bool in = t < s.tvalid;
+          if (vec) {
+            const float4 f = in ? *reinterpret_cast<const float4*>(p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
+          } else {
+#pragma unroll
+            for (int j = 0; j < F_SG; ++j) v[i][j] = in && k0 + j < KB ? p[j] : 0.0f;
+          }
+        }
+        ok = warp_wait(smem_u32(&bar_sce[slot]), phase ^ 1u, &s_abort, a.status, 11u);
+        if (!ok) break;
+        float* d = s_scale + slot * F_SG * NT;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i)
+#pragma unroll
+          for (int j = 0; j < F_SG; ++j)
+            if (t0 + 32 * i < NT) d[j * NT + t0 + 32 * i] = v[i][j] * wv[j];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_scf[slot]));
+        if (++slot == F_SRING) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue (both CTAs)
+    const int ew = warp - F_EPI0;
+    const int q = warp & 3;
+    const int h = ew >> 2;
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+    const uint32_t acce_even = smem_cluster_addr(smem_u32(&bar_acce[0]), 0);
+    uint16_t* stg = s_out + ew * 16 * 32;
+    int buf = 0, slot = 0;
+    uint32_t bphase = 0, sphase = 0;
+    s_walk[ew] = walk0;
+    while (!s_abort) {
+      __syncwarp();
+      {
+        Walk w = s_walk[ew];
+        Seg s;
+        if (!next_seg<NT>(w, E, WB, s_prefix, s_off, s)) break;
+        __syncwarp();
+        if (lane == 0) {
+          s_walk[ew] = w;
+          s_seg[ew] = s;
+        }
+        __syncwarp();
+      }
+      bool ok = true;
+      const int kb0 = s_seg[ew].kb0, kb1 = s_seg[ew].kb1;
+      const int split = ((s_seg[ew].n >> 1) + 15) & ~15;  // tokens [0, split) are the first half's, [split, n) the second's
+      const int c0 = h == 0 ? 0 : split;
+      const int nc_cols = h == 0 ? split : s_seg[ew].n - split;
+      uint64_t acc[C::kCols / 2];
+#pragma unroll
+      for (int i = 0; i < C::kCols / 2; ++i) acc[i] = 0ull;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        int got = 1;
+        if (lane == 0) {
+          got = mbar_wait(smem_u32(&bar_accf[buf]), bphase, &s_abort, a.status, 4u) ? 1 : 0;
+          if (got && (kb == kb0 || (kb & (F_SG - 1)) == 0))
+            got = mbar_wait(smem_u32(&bar_scf[slot]), sphase, &s_abort, a.status, 6u) ? 1 : 0;
+        }
+        if (!__shfl_sync(0xffffffffu, got, 0)) {
+          ok = false;
+          break;
+        }
+        __syncwarp();  // what lane 0 saw released (the scales) is visible to the warp
+        tc_fence_after();
+        const float* sc = s_scale + (slot * F_SG + (kb & (F_SG - 1))) * NT + c0;
+#pragma unroll
+        for (int j = 0; j < C::kCols / C::kChunk; ++j) {
+          if (j * C::kChunk < nc_cols) {
+            uint32_t v[C::kChunk];
+            tmem_ld<C::kChunk>(lane_addr + buf * NT + c0 + j * C::kChunk, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < C::kChunk / 4; ++i) {
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(sc + j * C::kChunk + 4 * i);
+              uint64_t& a0 = acc[j * (C::kChunk / 2) + 2 * i];
+              uint64_t& a1 = acc[j * (C::kChunk / 2) + 2 * i + 1];
+              asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a0) : "l"(pack2(v[4 * i], v[4 * i + 1])), "l"(f.x));
+              asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a1) : "l"(pack2(v[4 * i + 2], v[4 * i + 3])), "l"(f.y));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acce_even + 8u * buf);
+        if (++buf == C::kAcc) {
+          buf = 0;
+          bphase ^= 1u;
+        }
+        if ((kb & (F_SG - 1)) == F_SG - 1 || kb == kb1 - 1) {
+          if (lane == 0) mbar_arrive(smem_u32(&bar_sce[slot]));
+          if (++slot == F_SRING) {
+            slot = 0;
+            sphase ^= 1u;
+          }
+        }
+      }
+      if (!ok) break;
+      const Seg s = s_seg[ew];
+      const int64_t n0 = static_cast<int64_t>(s.wb) * F_ROWS + static_cast<int64_t>(rank) * F_HALF + 32 * q;
+      const int tv = min(nc_cols, s.tvalid - c0);  // tokens of this warp that exist (may be <= 0)
+      const float bias = a.bias != nullptr && n0 + lane < N ? bf16_bits_to_f32(a.bias[n0 + lane]) : 0.0f;
+      if (s.kb0 == 0 && s.kb1 == KB) {
+        if (n0 < N) {
+#pragma unroll
+          for (int t = 0; t < C::kCols / 16; ++t) {
+            if (16 * t < tv) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float lo, hi;
+                unpack2(acc[8 * t + i], lo, hi);
+                if (a.bias != nullptr) {
+                  lo += bias;
+                  hi += bias;
+                }
+                const uint32_t p = f32x2_to_bf16x2_bits(lo, hi);
+                stg[(2 * i) * 32 + lane] = static_cast<uint16_t>(p);
+                stg[(2 * i + 1) * 32 + lane] = static_cast<uint16_t>(p >> 16);
+              }
+              __syncwarp();
+              store_rows(stg, a.y, static_cast<int64_t>(s.row0) + c0 + 16 * t, N, n0, min(16, tv - 16 * t), lane);
+              __syncwarp();
+            }
+          }
+        }
+      } else if (n0 < N && tv > 0) {
+        // a piece of a cut unit: partial sums to this pair's slot (0: the unit began in an earlier run, 1: it began in
+        // this one), then the last warp to arrive adds the unit's pieces in the order of K
+        const int64_t u0 = static_cast<int64_t>(s.unit) * KB;
+        const int first = run_owner(total, runs, u0), last = run_owner(total, runs, u0 + KB - 1);
+        auto piece = [&](int c) {
+          return a.pieces + ((static_cast<int64_t>(c) * 2 + (c == first ? 1 : 0)) * 2 + rank) * C::kPiece +
+                 static_cast<int64_t>(ew) * C::kCols * 32 + lane;
+        };
+        // a unit that begins exactly where its first run begins uses that run's slot 1 as well
+        float* mine = piece(me);
+#pragma unroll
+        for (int i = 0; i < C::kCols / 2; ++i) {
+          if (2 * i < tv) {
+            float lo, hi;
+            unpack2(acc[i], lo, hi);
+            __stcg(mine + (2 * i) * 32, lo);
+            __stcg(mine + (2 * i + 1) * 32, hi);
+          }
+        }
+        __threadfence();
+        __syncwarp();
+        uint32_t* ctr = a.counters + (first * 2 + static_cast<int>(rank)) * F_EPI_WARPS + ew;
+        uint32_t arrived = 0;
+        if (lane == 0) arrived = atomicAdd(ctr, 1u);
+        arrived = __shfl_sync(0xffffffffu, arrived, 0);
+        if (arrived == static_cast<uint32_t>(last - first)) {
+          __threadfence();
+          if (lane == 0) *ctr = 0u;
+          for (int t = 0; t < tv; t += 16) {
+            float sum[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
+            for (int c = first; c <= last; ++c) {
+              const float* p = piece(c) + t * 32;
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (t + i < ((tv + 1) & ~1)) sum[i] += __ldcg(p + i * 32);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float v = sum[i];
+              if (a.bias != nullptr) v += bias;
+              stg[i * 32 + lane] = f32_to_bf16_bits(v);
+            }
+            __syncwarp();
+            store_rows(stg, a.y, static_cast<int64_t>(s.row0) + c0 + t, N, n0, min(16, tv - t), lane);
+            __syncwarp();
+          }
+        }
+      }
+    }
+  }
+
+  // ---- teardown: on abort, give in-flight copies and MMAs time to land first, then the pair leaves together.
+  __syncwarp();
+  tc_fence_before();
   __syncthreads();
-  if (s_bad) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * F_BN;
-  const int KB = static_cast<int>((a.K + 127) / 128), NB = static_cast<int>((a.N + 127) / 128);
-  const int wt = (warp & 1) * 32, wn = (warp >> 1) * 32;
-  const uint8_t* we = a.w + static_cast<int64_t>(e) * a.N * a.K;
-  const float* wse = a.w_scale + (static_cast<int64_t>(e) * NB + n0 / 128) * KB;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * F_BT; t0 < s_rows; t0 += static_cast<int64_t>(gridDim.y) * F_BT) {
-    float acc[2][4][4] = {};
-    for (int kb = 0; kb < KB; ++kb) {
-      __syncthreads();
-      load_tile(sx, a.q, s_row0 + t0, s_row0 + s_rows, a.K, kb * 128);
-      load_tile(sw, we, n0, a.N, a.K, kb * 128);
-      __syncthreads();
-      float part[2][4][4] = {};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = k * 32 + (lane & 3) * 4;
-        uint32_t fa[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint8_t* p = sx + (wt + i * 16 + (lane >> 2)) * F_STRIDE + c;
-          fa[i][0] = *reinterpret_cast<const uint32_t*>(p);
-          fa[i][1] = *reinterpret_cast<const uint32_t*>(p + 8 * F_STRIDE);
-          fa[i][2] = *reinterpret_cast<const uint32_t*>(p + 16);
-          fa[i][3] = *reinterpret_cast<const uint32_t*>(p + 8 * F_STRIDE + 16);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint8_t* p = sw + (wn + j * 8 + (lane >> 2)) * F_STRIDE + c;
-          const uint32_t b0 = *reinterpret_cast<const uint32_t*>(p), b1 = *reinterpret_cast<const uint32_t*>(p + 16);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) mma_e4m3(part[i][j], fa[i], b0, b1);
-        }
-      }
-      const float w = wse[kb];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t t = t0 + wt + i * 16 + h * 8 + (lane >> 2);
-          const float s = t < s_rows ? a.x_scale[(s_row0 + t) * KB + kb] * w : 0.0f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[i][j][2 * h] = fmaf(part[i][j][2 * h], s, acc[i][j][2 * h]);
-            acc[i][j][2 * h + 1] = fmaf(part[i][j][2 * h + 1], s, acc[i][j][2 * h + 1]);
-          }
-        }
+  if (s_abort) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 20000000ull) {
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int64_t t = t0 + wt + i * 16 + (h >> 1) * 8 + (lane >> 2);
-          const int64_t n = n0 + wn + j * 8 + (lane & 3) * 2 + (h & 1);
-          if (t < s_rows && n < a.N) {
-            float v = acc[i][j][h];
-            if (a.bias != nullptr) v += bf16_bits_to_f32(a.bias[n]);
-            a.y[(s_row0 + t) * a.N + n] = f32_to_bf16_bits(v);
-          }
-        }
   }
+  cluster_sync_all();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(F_TMEM_COLS)
+                 : "memory");
+  }
+}
+
+// Tokens per tile: the power of two from 32 to 256 that holds the rows (dense), or twice the mean rows of a group.
+int tile_tokens(int64_t E, int64_t R, bool grouped) {
+  const int64_t want = grouped ? 2 * ((R + E - 1) / E) : R;
+  return want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
+}
+// Pairs to launch.
+int64_t pairs_for(int64_t E, int64_t R, int64_t N, int64_t K, bool grouped, int64_t most) {
+  if (grouped) return most;
+  const int nt = tile_tokens(E, R, grouped);
+  const int64_t units = ((R + nt - 1) / nt) * ((N + F_ROWS - 1) / F_ROWS);
+  const int64_t total = units * ((K + F_BK - 1) / F_BK);
+  return std::max<int64_t>(1, std::min<int64_t>(most, total / F_MIN_RUN));
+}
+
+template <int NT>
+cudaError_t launch_nt(const Fp8GemmArgs& g, const KArgs& a, int64_t pairs, cudaStream_t stream) {
+  using C = Cfg<NT>;
+  CUtensorMap mw, mb, ms;
+  const auto type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  if (!encode_map_2d(&mw, g.w, type, 1, g.E * g.N, g.K, F_BK, F_HALF, sw) ||
+      !encode_map_2d(&mb, g.q, type, 1, g.R, g.K, F_BK, C::kBig, sw) ||
+      !encode_map_2d(&ms, g.q, type, 1, g.R, g.K, F_BK, 8, sw))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(C::kSmem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(fp8_gemm_kernel<NT>, dim3(static_cast<unsigned>(2 * pairs)), dim3(F_THREADS), C::kSmem, stream, mw,
+                    mb, ms, a);
 }
 
 }  // namespace
 
-size_t fp8_gemm_ws_bytes(int64_t, int64_t, int64_t, int64_t, bool) { return 0; }
+size_t fp8_gemm_ws_bytes(int64_t E, int64_t R, int64_t N, int64_t K, bool grouped) {
+  const int64_t pairs = pairs_for(E, R, N, K, grouped, F_MAX_CLUSTERS);
+  return kCounterBytes + static_cast<size_t>(pairs) * 4 * F_HALF * tile_tokens(E, R, grouped) * 4;
+}
 
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, void*, int, cudaStream_t stream) {
-  if (a.R == 0) return cudaSuccess;
-  const int64_t tb = a.group_list != nullptr ? std::min<int64_t>(a.R, 512) : a.R;
-  const dim3 g(static_cast<unsigned>((a.N + F_BN - 1) / F_BN),
-               static_cast<unsigned>(std::min<int64_t>(65535, (tb + F_BT - 1) / F_BT)), static_cast<unsigned>(a.E));
-  fp8_gemm_kernel<<<g, F_THREADS, 0, stream>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, void* ws, int num_sms, cudaStream_t stream) {
+  if (g.R == 0) return cudaSuccess;
+  const bool grouped = g.group_list != nullptr;
+  const int nt = tile_tokens(g.E, g.R, grouped);
+  const int64_t most_units = (g.R / nt + g.E) * ((g.N + F_ROWS - 1) / F_ROWS);
+  if (most_units > INT32_MAX) return cudaErrorInvalidValue;
+  KArgs a;
+  a.xs = g.x_scale;
+  a.group_list = g.group_list;
+  a.wsc = g.w_scale;
+  a.bias = g.bias;
+  a.y = g.y;
+  a.status = g.status;
+  a.counters = static_cast<uint32_t*>(ws);
+  a.pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
+  a.R = g.R;
+  a.N = g.N;
+  a.K = g.K;
+  a.E = static_cast<int>(g.E);
+  const int64_t pairs = pairs_for(g.E, g.R, g.N, g.K, grouped, std::min(num_sms / 2, F_MAX_CLUSTERS));
+  switch (nt) {
+    case 32: return launch_nt<32>(g, a, pairs, stream);
+    case 64: return launch_nt<64>(g, a, pairs, stream);
+    case 128: return launch_nt<128>(g, a, pairs, stream);
+    default: return launch_nt<256>(g, a, pairs, stream);
+  }
 }
 
 }  // namespace w8a8
