@@ -37,29 +37,18 @@
 //
 // Every mbarrier wait is bounded (2 s): on expiry the CTA sets
 // W8A8_ERR_DEVICE_TIMEOUT, lets in-flight copies land, frees TMEM and returns.
-#include "kernels.cuh"
-#include "tc_common.cuh"
+#include "fp8_common.cuh"
 
 namespace w8a8 {
 
 namespace {
 
-using namespace tc;
+using namespace fp8;
 
 constexpr int F_ROWS = 256;   // output channels per pair tile (MMA M)
 constexpr int F_HALF = 128;   // of them in each CTA
-constexpr int F_BK = 128;     // K per stage and per scale block (bytes = E4M3 values)
 constexpr int F_THREADS = 384;
 constexpr int F_EPI0 = 4;
-constexpr int F_EPI_WARPS = 8;
-constexpr int F_SG = 4;       // blocks per scale group
-constexpr int F_SRING = 2;    // scale groups in the ring
-constexpr int F_MAX_CLUSTERS = 76;
-constexpr int F_MAX_E = 1024;
-constexpr int F_SUPER = 32;   // token blocks per rasterisation group
-constexpr int F_MIN_RUN = 4;  // blocks per run at least
-constexpr uint16_t F_PAIR_MASK = 0x3;
-constexpr uint32_t F_TMEM_COLS = 512;
 constexpr uint32_t F_W_BYTES = F_HALF * F_BK;  // 16 KB
 constexpr uint32_t F_STG_BYTES = F_EPI_WARPS * 16 * 32 * 2;  // output staging: [16 tokens][32 channels] per warp
 
@@ -67,111 +56,56 @@ template <int NT>
 struct Cfg {
   static constexpr uint32_t kXBytes = NT / 2 * F_BK;
   static constexpr uint32_t kStageBytes = F_W_BYTES + kXBytes;
-  static constexpr int kStages = NT == 256 ? 6 : NT == 128 ? 8 : NT == 64 ? 9 : 10;
-  static constexpr int kAcc = NT >= 64 ? 512 / NT : 8;   // accumulators
-  static constexpr int kCols = NT / 2;                    // token columns per epilogue warp
-  static constexpr int kChunk = kCols == 64 || kCols == 32 ? 32 : 16;  // columns per tensor-memory load
-  static constexpr int kBig = NT / 2 < 64 ? NT / 2 : 64;  // token rows per large TMA box
+  static constexpr int kStages = NT == 128 ? 8 : NT == 64 ? 9 : 10;
+  static constexpr int kAcc = NT >= 64 ? 512 / NT : 8;  // accumulators of NT columns
+  static constexpr int kCols = NT / 2;                  // of them read by one epilogue warp
+  static constexpr int kBig = NT / 2;                   // token rows per large TMA box
   static constexpr uint32_t kScaleBytes = F_SRING * F_SG * NT * 4;
   static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes + kScaleBytes + F_STG_BYTES + 1024;
   static constexpr size_t kPiece = static_cast<size_t>(F_EPI_WARPS) * kCols * 32;  // floats of one CTA's partial sums
 };
 
-constexpr size_t kCounterBytes = F_MAX_CLUSTERS * 2 * F_EPI_WARPS * 4;
-static_assert(kCounterBytes % 256 == 0, "pieces start 256-byte aligned");
-
-struct KArgs {
-  const float* xs;
-  const int64_t* group_list;
-  const float* wsc;
-  const uint16_t* bias;
-  uint16_t* y;
-  DeviceStatus* status;
-  uint32_t* counters;  // [clusters][2][epilogue warps], zero between calls
-  float* pieces;       // [clusters][2 slots][2 CTAs][kPiece]
-  int64_t R, N, K;
-  int E;
-};
-
-// D(tmem, both CTAs) (+)= A * B, kind::f8f6f4 with both operands E4M3, on the CTA pair (issued by the elected lane
-// of a converged warp).
-__device__ __forceinline__ void mma_pair_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Instruction descriptor: binary32 accumulator, E4M3 operands (format 0), both K-major, M = 256, N = n.
-__device__ __forceinline__ uint32_t idesc_f8(int n) {
-  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(F_ROWS >> 4) << 24);
-}
-
-template <int C>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[C]) {
-  static_assert(C == 32 || C == 16, "chunk");
-  if constexpr (C == 32) tmem_ld32(taddr, v);
-  else tmem_ld16(taddr, v);
-}
-
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+// acc[c] += accumulator column c * sc[c], c < cols (rounded up to 16).  The warp's columns come in one load, and once
+// it is complete the accumulator is released (arrival on `release`), before the sums.
+template <int COLS>
+__device__ __forceinline__ void drain(uint32_t taddr, const float* sc, int cols, uint32_t release, int lane,
+                                      float (&acc)[COLS]) {
+  uint32_t v[COLS];
+  tmem_fetch(taddr, v);
+  tmem_ready(v);
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive_cluster(release);
+#pragma unroll
+  for (int j = 0; j < COLS; j += 16) {
+    if (j < cols) {
+#pragma unroll
+      for (int i = j; i < j + 16; i += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(sc + i);
+        acc[i] = fmaf(__uint_as_float(v[i]), f.x, acc[i]);
+        acc[i + 1] = fmaf(__uint_as_float(v[i + 1]), f.y, acc[i + 1]);
+        acc[i + 2] = fmaf(__uint_as_float(v[i + 2]), f.z, acc[i + 2]);
+        acc[i + 3] = fmaf(__uint_as_float(v[i + 3]), f.w, acc[i + 3]);
+      }
+    }
+  }
 }
 
 // One run of blocks of a unit: the tile and its K range.
 struct Seg {
   int e, wb;       // expert, 256-channel block
   int row0;        // first token row (of all R)
-  int tvalid, n;   // tokens, and tokens rounded up to 16
+  int tvalid;      // tokens
+  int n;           // tokens rounded up to 16
   int kb0, kb1;    // blocks [kb0, kb1)
   int unit;
 };
 
-// The sequence of segments of one pair.  Every role walks it on its own.
-struct Walk {
-  int64_t x, end;  // cut: block position; else: unit number
-  int step;        // 0: cut
-  int KB;
-};
-__device__ __forceinline__ int64_t run_begin(int64_t total, int C, int c) { return total * c / C; }
-// The pair whose run holds block position p.
-__device__ __forceinline__ int run_owner(int64_t total, int C, int64_t p) {
-  return static_cast<int>(((p + 1) * C - 1) / total);
-}
-
 template <int NT>
 __device__ __forceinline__ bool next_seg(Walk& w, int E, int WB, const int* s_prefix, const int* s_off, Seg& s) {
-  if (w.x >= w.end) return false;
-  int u;
-  if (w.step == 0) {
-    u = static_cast<int>(w.x / w.KB);
-    s.kb0 = static_cast<int>(w.x - static_cast<int64_t>(u) * w.KB);
-    s.kb1 = static_cast<int>(min(static_cast<int64_t>(w.KB), s.kb0 + (w.end - w.x)));
-    w.x += s.kb1 - s.kb0;
-  } else {
-    u = static_cast<int>(w.x);
-    s.kb0 = 0;
-    s.kb1 = w.KB;
-    w.x += w.step;
-  }
-  s.unit = u;
-  s.e = expert_of(u, E, s_prefix);
-  const int local = u - s_prefix[s.e];
-  const int cnt = s_off[s.e + 1] - s_off[s.e];
-  const int TB = (cnt + NT - 1) / NT;
-  // token blocks in groups of F_SUPER, the channel block outside: the pairs in flight share weight blocks, and the
-  // group's token rows stay in L2 while the weights sweep past
-  const int g = local / (WB * F_SUPER);
-  const int rem = local - g * WB * F_SUPER;
-  const int gt = min(F_SUPER, TB - g * F_SUPER);
-  s.wb = rem / gt;
-  const int tb = g * F_SUPER + rem - s.wb * gt;
+  if (!next_unit(w, s.unit, s.kb0, s.kb1)) return false;
+  int tb, cnt, TB;
+  unit_tile(s.unit, E, WB, s_prefix, s_off, [](int c) { return (c + NT - 1) / NT; }, s.e, s.wb, tb, cnt, TB);
   const int per = ((cnt + TB - 1) / TB + 15) & ~15;  // tokens split evenly over the blocks
   s.row0 = s_off[s.e] + tb * per;
   s.tvalid = min(per, cnt - tb * per);
@@ -215,12 +149,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   __shared__ int s_prefix[F_MAX_E + 1];
   __shared__ int s_off[F_MAX_E + 1];
   __shared__ int s_warp[F_THREADS / 32];
-  __shared__ Seg s_seg[F_EPI_WARPS];    // the epilogue warps' segment and place in the walk: 128 sums a thread leave
-  __shared__ Walk s_walk[F_EPI_WARPS];  // no registers to hold them through the block loop
   __shared__ unsigned long long s_rows;  // the counts' sum where 32 bits may not hold it
 
   const int tid = threadIdx.x;
-  const int warp = tid >> 5;
+  const int warp = uni(tid >> 5);
   const int lane = tid & 31;
   const int E = a.E;
   const int64_t N = a.N;
@@ -266,74 +198,64 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   __syncthreads();  // s_bad, before the scan may set it
   pdl_trigger();
   pdl_wait();
-  GemmArgs ga;
-  ga.group_list = a.group_list;
-  ga.R = a.R;
   int units;
-  const int rows_total = scan_groups<F_THREADS, F_MAX_E>(
-      ga, E, [WB](int c) { return ((c + NT - 1) / NT) * WB; }, s_off, s_prefix, s_warp, &s_bad, &units);
-  const bool wide = a.R > INT32_MAX / E;
-  if (wide && a.group_list != nullptr)
-    for (int e = tid; e < E; e += F_THREADS)
-      atomicAdd(&s_rows, static_cast<unsigned long long>(max(0ll, static_cast<long long>(a.group_list[e]))));
+  const int rows_total = scan_checked<F_THREADS>(
+      a, [WB](int c) { return ((c + NT - 1) / NT) * WB; }, s_off, s_prefix, s_warp, &s_bad, &s_rows, &units);
   tc_fence_before();
   cluster_sync_all();  // both CTAs' barriers and tensor memory exist before either touches the other's
   tc_fence_after();
-  const uint32_t tmem_base = s_tmem_base;
-  if (s_bad || rows_total != a.R || (wide && a.group_list != nullptr && s_rows != static_cast<unsigned long long>(a.R))) {
+  const uint32_t tmem_base = static_cast<uint32_t>(uni(static_cast<int>(s_tmem_base)));
+  if (bad_list(a, rows_total, s_bad, s_rows)) {
     if (tid == 0 && blockIdx.x == 0) set_status(a.status, W8A8_ERR_GROUP_LIST, 0u);
     units = 0;
   }
-  // many units: every C-th; few: equal runs of blocks, at least F_MIN_RUN each
-  const int64_t total = static_cast<int64_t>(units) * KB;
-  const int nc = static_cast<int>(nclusters);
-  const bool cut = units < 4 * nc;
-  const int runs = static_cast<int>(min(static_cast<int64_t>(nc), max(static_cast<int64_t>(1), total / F_MIN_RUN)));
   const int me = static_cast<int>(cluster_id);
-  Walk walk0;
-  walk0.KB = KB;
-  walk0.step = cut ? 0 : nc;
-  walk0.x = !cut ? me : me < runs ? run_begin(total, runs, me) : 0;
-  walk0.end = !cut ? units : me < runs ? run_begin(total, runs, me + 1) : 0;
+  int64_t total;
+  int runs;
+  const Walk walk0 = start_walk(units, KB, static_cast<int>(nclusters), me, total, runs);
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      Walk w = walk0;
-      Seg s;
-      while (!s_abort && next_seg<NT>(w, E, WB, s_prefix, s_off, s)) {
-        const int xrows = s.n >> 1;
-        const int yx = s.row0 + static_cast<int>(rank) * xrows;
-        const int yw = static_cast<int>(static_cast<int64_t>(s.e) * N) + s.wb * F_ROWS + static_cast<int>(rank) * F_HALF;
-        const uint32_t bytes = 2u * (F_W_BYTES + static_cast<uint32_t>(xrows) * F_BK);
-        for (int kb = s.kb0; kb < s.kb1; ++kb) {
-          if (!mbar_wait(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 1u)) break;
+    int stage = 0;
+    uint32_t phase = 0;
+    Walk w = walk0;
+    Seg s;
+    bool ok = true;
+    while (ok && uni(next_seg<NT>(w, E, WB, s_prefix, s_off, s))) {
+      const int yw = static_cast<int>(static_cast<int64_t>(s.e) * N) + s.wb * F_ROWS + static_cast<int>(rank) * F_HALF;
+      const uint32_t bytes = 2u * F_W_BYTES + static_cast<uint32_t>(s.n) * F_BK;
+      const int kb1 = uni(s.kb1);
+      for (int kb = uni(s.kb0); kb < kb1; ++kb) {
+        ok = wait_all(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 1u);
+        if (!ok) break;
+        if (lane == 0) {
           const uint32_t full = smem_u32(&bar_full[stage]);
           if (rank == 0) mbar_expect_tx(full, bytes);
           const uint32_t full_even = smem_cluster_addr(full, 0);
-          const uint32_t sa = stage_base + stage * C::kStageBytes;
-          tma_load_2d_pair(sa, &tmW, kb * F_BK, yw, full_even);
-          int r = 0;
-          for (; r + C::kBig <= xrows; r += C::kBig)
-            tma_load_2d_pair(sa + F_W_BYTES + r * F_BK, &tmXbig, kb * F_BK, yx + r, full_even);
-          for (; r < xrows; r += 8)
-            tma_load_2d_pair(sa + F_W_BYTES + r * F_BK, &tmXsmall, kb * F_BK, yx + r, full_even);
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          uint32_t dst = stage_base + stage * C::kStageBytes;
+          tma_load_2d_pair(dst, &tmW, kb * F_BK, yw, full_even);
+          dst += F_W_BYTES;
+          // the block's first n / 2 token rows go to the even CTA, the rest to the odd one
+          int rows = s.n >> 1, yx = s.row0 + static_cast<int>(rank) * rows;
+          for (; rows >= C::kBig; rows -= C::kBig, yx += C::kBig, dst += C::kBig * F_BK)
+            tma_load_2d_pair(dst, &tmXbig, kb * F_BK, yx, full_even);
+          for (; rows > 0; rows -= 8, yx += 8, dst += 8 * F_BK)
+            tma_load_2d_pair(dst, &tmXsmall, kb * F_BK, yx, full_even);
         }
-      }
-      // Drain: the last fill of every stage has been consumed, so no copy into this CTA and no MMA arrival on its
-      // barriers is still in flight when the cluster leaves.
-      for (int i = 0; i < C::kStages && !s_abort; ++i) {
-        if (!mbar_wait(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 5u)) break;
+        __syncwarp();
         if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1u;
         }
+      }
+    }
+    // Drain: the last fill of every stage has been consumed, so no copy into this CTA and no MMA arrival on its
+    // barriers is still in flight when the cluster leaves.
+    for (int i = 0; i < C::kStages && ok; ++i) {
+      ok = wait_all(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 5u);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1u;
       }
     }
   } else if (warp == 1) {
@@ -344,14 +266,13 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       Walk w = walk0;
       Seg s;
       bool ok = true;
-      while (ok && !s_abort && next_seg<NT>(w, E, WB, s_prefix, s_off, s)) {
-        const uint32_t idesc = idesc_f8(s.n);
-        for (int kb = s.kb0; kb < s.kb1; ++kb) {
-          if (!warp_wait(smem_u32(&bar_acce[buf]), bphase ^ 1u, &s_abort, a.status, 2u) ||
-              !warp_wait(smem_u32(&bar_full[stage]), phase, &s_abort, a.status, 3u)) {
-            ok = false;
-            break;
-          }
+      while (ok && uni(next_seg<NT>(w, E, WB, s_prefix, s_off, s))) {
+        const uint32_t idesc = idesc_f8(uni(s.n));
+        const int kb1 = uni(s.kb1);
+        for (int kb = uni(s.kb0); kb < kb1; ++kb) {
+          ok = wait_all(smem_u32(&bar_full[stage]), phase, &s_abort, a.status, 3u) &&
+               wait_all(smem_u32(&bar_acce[buf]), bphase ^ 1u, &s_abort, a.status, 2u);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t sa = stage_base + stage * C::kStageBytes;
           const uint64_t adesc = smem_desc_sw128(sa);
@@ -359,8 +280,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 #pragma unroll
           for (int k = 0; k < F_BK / 32; ++k)
             mma_pair_f8(tmem_base + buf * NT, adesc + 2u * k, bdesc + 2u * k, idesc, k > 0 ? 1u : 0u);
-          tc_commit_pair_mc(smem_u32(&bar_empty[stage]), F_PAIR_MASK);  // frees the stage in both CTAs
           tc_commit_pair_mc(smem_u32(&bar_accf[buf]), F_PAIR_MASK);
+          tc_commit_pair_mc(smem_u32(&bar_empty[stage]), F_PAIR_MASK);  // frees the stage in both CTAs
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1u;
@@ -383,7 +304,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     Walk w = walk0;
     Seg s;
     bool ok = true;
-    while (ok && !s_abort && next_seg<NT>(w, E, WB, s_prefix, s_off, s)) {
+    while (ok && uni(next_seg<NT>(w, E, WB, s_prefix, s_off, s))) {
       const int nb = s.wb * 2 + static_cast<int>(rank);
       const float* wrow = a.wsc + (static_cast<int64_t>(s.e) * NB + nb) * KB;
       for (int g = s.kb0 / F_SG; ok && g * F_SG < s.kb1; ++g) {
@@ -405,7 +326,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             for (int j = 0; j < F_SG; ++j) v[i][j] = in && k0 + j < KB ? p[j] : 0.0f;
           }
         }
-        ok = warp_wait(smem_u32(&bar_sce[slot]), phase ^ 1u, &s_abort, a.status, 11u);
+        ok = wait_all(smem_u32(&bar_sce[slot]), phase ^ 1u, &s_abort, a.status, 11u);
         if (!ok) break;
         float* d = s_scale + slot * F_SG * NT;
 #pragma unroll
@@ -431,66 +352,32 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     uint16_t* stg = s_out + ew * 16 * 32;
     int buf = 0, slot = 0;
     uint32_t bphase = 0, sphase = 0;
-    s_walk[ew] = walk0;
-    while (!s_abort) {
-      __syncwarp();
-      {
-        Walk w = s_walk[ew];
-        Seg s;
-        if (!next_seg<NT>(w, E, WB, s_prefix, s_off, s)) break;
-        __syncwarp();
-        if (lane == 0) {
-          s_walk[ew] = w;
-          s_seg[ew] = s;
-        }
-        __syncwarp();
-      }
-      bool ok = true;
-      const int kb0 = s_seg[ew].kb0, kb1 = s_seg[ew].kb1;
-      const int split = ((s_seg[ew].n >> 1) + 15) & ~15;  // tokens [0, split) are the first half's, [split, n) the second's
+    Walk w = walk0;
+    Seg s;
+    bool ok = true;
+    while (ok && uni(next_seg<NT>(w, E, WB, s_prefix, s_off, s))) {
+      // the first half's warps read tokens [0, split), the second's [split, n)
+      const int n = uni(s.n), kb0 = uni(s.kb0), kb1 = uni(s.kb1);
+      const int split = ((n >> 1) + 15) & ~15;
       const int c0 = h == 0 ? 0 : split;
-      const int nc_cols = h == 0 ? split : s_seg[ew].n - split;
-      uint64_t acc[C::kCols / 2];
+      const int cols = h == 0 ? split : n - split;
+      float acc[C::kCols];
 #pragma unroll
-      for (int i = 0; i < C::kCols / 2; ++i) acc[i] = 0ull;
+      for (int i = 0; i < C::kCols; ++i) acc[i] = 0.0f;
       for (int kb = kb0; kb < kb1; ++kb) {
-        int got = 1;
-        if (lane == 0) {
-          got = mbar_wait(smem_u32(&bar_accf[buf]), bphase, &s_abort, a.status, 4u) ? 1 : 0;
-          if (got && (kb == kb0 || (kb & (F_SG - 1)) == 0))
-            got = mbar_wait(smem_u32(&bar_scf[slot]), sphase, &s_abort, a.status, 6u) ? 1 : 0;
-        }
-        if (!__shfl_sync(0xffffffffu, got, 0)) {
-          ok = false;
-          break;
-        }
-        __syncwarp();  // what lane 0 saw released (the scales) is visible to the warp
+        if (kb == kb0 || (kb & (F_SG - 1)) == 0)
+          ok = wait_all(smem_u32(&bar_scf[slot]), sphase, &s_abort, a.status, 6u);
+        ok = ok && wait_all(smem_u32(&bar_accf[buf]), bphase, &s_abort, a.status, 4u);
+        if (!ok) break;
         tc_fence_after();
-        const float* sc = s_scale + (slot * F_SG + (kb & (F_SG - 1))) * NT + c0;
-#pragma unroll
-        for (int j = 0; j < C::kCols / C::kChunk; ++j) {
-          if (j * C::kChunk < nc_cols) {
-            uint32_t v[C::kChunk];
-            tmem_ld<C::kChunk>(lane_addr + buf * NT + c0 + j * C::kChunk, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < C::kChunk / 4; ++i) {
-              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(sc + j * C::kChunk + 4 * i);
-              uint64_t& a0 = acc[j * (C::kChunk / 2) + 2 * i];
-              uint64_t& a1 = acc[j * (C::kChunk / 2) + 2 * i + 1];
-              asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a0) : "l"(pack2(v[4 * i], v[4 * i + 1])), "l"(f.x));
-              asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a1) : "l"(pack2(v[4 * i + 2], v[4 * i + 3])), "l"(f.y));
-            }
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acce_even + 8u * buf);
+        drain<C::kCols>(lane_addr + buf * NT + c0, s_scale + (slot * F_SG + (kb & (F_SG - 1))) * NT + c0, cols,
+                        acce_even + 8u * buf, lane, acc);
         if (++buf == C::kAcc) {
           buf = 0;
           bphase ^= 1u;
         }
         if ((kb & (F_SG - 1)) == F_SG - 1 || kb == kb1 - 1) {
+          __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bar_sce[slot]));
           if (++slot == F_SRING) {
             slot = 0;
@@ -499,53 +386,44 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         }
       }
       if (!ok) break;
-      const Seg s = s_seg[ew];
       const int64_t n0 = static_cast<int64_t>(s.wb) * F_ROWS + static_cast<int64_t>(rank) * F_HALF + 32 * q;
-      const int tv = min(nc_cols, s.tvalid - c0);  // tokens of this warp that exist (may be <= 0)
+      const int tv = min(cols, s.tvalid - c0);  // tokens of this warp that exist (may be <= 0)
+      if (n0 >= N || tv <= 0) continue;
       const float bias = a.bias != nullptr && n0 + lane < N ? bf16_bits_to_f32(a.bias[n0 + lane]) : 0.0f;
-      if (s.kb0 == 0 && s.kb1 == KB) {
-        if (n0 < N) {
+      const int64_t row0 = static_cast<int64_t>(s.row0) + c0;
+      if (kb0 == 0 && kb1 == KB) {
 #pragma unroll
-          for (int t = 0; t < C::kCols / 16; ++t) {
-            if (16 * t < tv) {
+        for (int t = 0; t < C::kCols; t += 16) {
+          if (t < tv) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float lo, hi;
-                unpack2(acc[8 * t + i], lo, hi);
-                if (a.bias != nullptr) {
-                  lo += bias;
-                  hi += bias;
-                }
-                const uint32_t p = f32x2_to_bf16x2_bits(lo, hi);
-                stg[(2 * i) * 32 + lane] = static_cast<uint16_t>(p);
-                stg[(2 * i + 1) * 32 + lane] = static_cast<uint16_t>(p >> 16);
+            for (int i = 0; i < 16; i += 2) {
+              float lo = acc[t + i], hi = acc[t + i + 1];
+              if (a.bias != nullptr) {
+                lo += bias;
+                hi += bias;
               }
-              __syncwarp();
-              store_rows(stg, a.y, static_cast<int64_t>(s.row0) + c0 + 16 * t, N, n0, min(16, tv - 16 * t), lane);
-              __syncwarp();
+              const uint32_t v = f32x2_to_bf16x2_bits(lo, hi);
+              stg[i * 32 + lane] = static_cast<uint16_t>(v);
+              stg[(i + 1) * 32 + lane] = static_cast<uint16_t>(v >> 16);
             }
+            __syncwarp();
+            store_rows(stg, a.y, row0 + t, N, n0, min(16, tv - t), lane);
+            __syncwarp();
           }
         }
-      } else if (n0 < N && tv > 0) {
-        // a piece of a cut unit: partial sums to this pair's slot (0: the unit began in an earlier run, 1: it began in
-        // this one), then the last warp to arrive adds the unit's pieces in the order of K
+      } else {
+        // a piece of a cut unit: partial sums to this pair's slot (1: the unit begins in this run, 0: it began in an
+        // earlier one), then the last warp to arrive adds the unit's pieces in the order of K
         const int64_t u0 = static_cast<int64_t>(s.unit) * KB;
         const int first = run_owner(total, runs, u0), last = run_owner(total, runs, u0 + KB - 1);
         auto piece = [&](int c) {
           return a.pieces + ((static_cast<int64_t>(c) * 2 + (c == first ? 1 : 0)) * 2 + rank) * C::kPiece +
                  static_cast<int64_t>(ew) * C::kCols * 32 + lane;
         };
-        // a unit that begins exactly where its first run begins uses that run's slot 1 as well
         float* mine = piece(me);
 #pragma unroll
-        for (int i = 0; i < C::kCols / 2; ++i) {
-          if (2 * i < tv) {
-            float lo, hi;
-            unpack2(acc[i], lo, hi);
-            __stcg(mine + (2 * i) * 32, lo);
-            __stcg(mine + (2 * i + 1) * 32, hi);
-          }
-        }
+        for (int i = 0; i < C::kCols; ++i)
+          if (i < tv) __stcg(mine + i * 32, acc[i]);
         __threadfence();
         __syncwarp();
         uint32_t* ctr = a.counters + (first * 2 + static_cast<int>(rank)) * F_EPI_WARPS + ew;
@@ -560,19 +438,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 #pragma unroll
             for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
             for (int c = first; c <= last; ++c) {
-              const float* p = piece(c) + t * 32;
+              const float* src = piece(c) + t * 32;
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                if (t + i < ((tv + 1) & ~1)) sum[i] += __ldcg(p + i * 32);
+                if (t + i < tv) sum[i] += __ldcg(src + i * 32);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float v = sum[i];
-              if (a.bias != nullptr) v += bias;
-              stg[i * 32 + lane] = f32_to_bf16_bits(v);
-            }
+            for (int i = 0; i < 16; ++i) stg[i * 32 + lane] = f32_to_bf16_bits(a.bias != nullptr ? sum[i] + bias : sum[i]);
             __syncwarp();
-            store_rows(stg, a.y, static_cast<int64_t>(s.row0) + c0 + t, N, n0, min(16, tv - t), lane);
+            store_rows(stg, a.y, row0 + t, N, n0, min(16, tv - t), lane);
             __syncwarp();
           }
         }
@@ -660,7 +534,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, void* ws, int num_sms, cudaStr
     case 32: return launch_nt<32>(g, a, pairs, stream);
     case 64: return launch_nt<64>(g, a, pairs, stream);
     case 128: return launch_nt<128>(g, a, pairs, stream);
-    default: return launch_nt<256>(g, a, pairs, stream);
+    default: return launch_fp8_wide(g, a, pairs, stream);
   }
 }
 

@@ -1,0 +1,546 @@
+// fp8_wide.cu -- block-scaled FP8 contraction for many tokens (see
+// fp8_gemm.cu for the formula and for few): tokens as the MMA's M side.
+//
+// Tile.  256 tokens x 256 output channels per CTA pair, in two parts of 128
+// channels (one weight block each); a CTA holds 128 token rows and 64 weight
+// rows of each part of every 128-deep stage.  A part and block of K is one
+// accumulator (128 lanes x 128 columns of tensor memory), four in all: two parts
+// times two.  A thread of the epilogue owns one token row of one part, so xs * ws
+// is one number for all of its 128 columns and block: a fused multiply-add a
+// value with its scale in a register.  (With the weights as M side every column
+// has its own scale, which comes from shared memory: four values a 16-byte load.)
+//
+// What bounds it.  Per 128-deep block a pair's MMAs take 512 cycles; an epilogue
+// warp's round -- barrier, two tensor-memory loads of 64 columns, 128 sums,
+// release -- takes about 820, most of it latency that does not grow with the
+// columns.  So few, wide rounds win: measured on 8192 x 14336 x 4096, 2 x 128
+// channels a tile 392 us, 2 x 96 452 us, one part of 160 with three accumulators
+// 486 us; without the drain the same pipeline takes 261 us, near the MMAs' own time.
+// Each part has its own issuing warp and its own four epilogue warps.
+//
+// Warp roles (384 threads, one CTA per SM):
+//   warp 0       TMA producer
+//   warps 1, 2   issue the MMAs of part 0, 1 (even CTA); warp 1 owns the TMEM
+//   warp 3       scales: xs * ws, [block][part][token], four blocks at a time, into a shared-memory ring
+//   warps 4-11   epilogue: part (w - 4) / 4, TMEM lanes 32 * (w % 4) ..
+// Whole rows of 32 tokens leave through shared memory by TMA.  Work, cut units and bounded waits as in fp8_gemm.cu.
+#include "fp8_common.cuh"
+
+namespace w8a8 {
+
+namespace {
+
+using namespace fp8;
+
+constexpr int G_TOK = 256;    // tokens per pair tile (MMA M)
+constexpr int G_HALF = 128;   // of them in each CTA
+constexpr int G_CH = 256;     // channels per tile
+constexpr int G_PART = 128;   // channels per part (MMA N)
+constexpr int G_THREADS = 384;
+constexpr int G_EPI0 = 4;
+constexpr int G_STAGES = 5;
+constexpr uint32_t G_X_BYTES = G_HALF * F_BK;       // 16 KB: the CTA's token rows
+constexpr uint32_t G_P_BYTES = G_PART / 2 * F_BK;   // 8 KB: its weight rows of a part
+constexpr uint32_t G_STAGE_BYTES = G_X_BYTES + 2 * G_P_BYTES;
+constexpr uint32_t G_SCALE_BYTES = F_SRING * F_SG * 2 * G_HALF * 4;
+constexpr uint32_t G_STG_WARP = 32 * 128;            // output staging: [32 tokens][64 channels] bf16 per warp
+constexpr uint32_t G_STG_BYTES = F_EPI_WARPS * G_STG_WARP;
+constexpr size_t kWideSmem = static_cast<size_t>(G_STAGES) * G_STAGE_BYTES + G_SCALE_BYTES + G_STG_BYTES + 1024;
+constexpr size_t kWidePiece = static_cast<size_t>(F_EPI_WARPS) * G_PART * 32;  // floats of one CTA's partial sums
+
+
+struct WSeg {
+  int e, wb;     // expert, 256-channel block
+  int row0;      // first token row (of all R)
+  int tvalid;    // tokens
+  int kb0, kb1;  // blocks [kb0, kb1)
+  int unit;
+};
+
+__device__ __forceinline__ int wide_blocks(int c) { return (c + G_TOK - 1) / G_TOK; }
+
+__device__ __forceinline__ bool next_wide(Walk& w, int E, int WB, const int* s_prefix, const int* s_off, WSeg& s) {
+  if (!next_unit(w, s.unit, s.kb0, s.kb1)) return false;
+  int tb, cnt, TB;
+  unit_tile(s.unit, E, WB, s_prefix, s_off, [](int c) { return wide_blocks(c); }, s.e, s.wb, tb, cnt, TB);
+  s.row0 = s_off[s.e] + tb * G_TOK;
+  s.tvalid = min(G_TOK, cnt - tb * G_TOK);
+  return true;
+}
+
+// acc[i] += s * v[i], two values an instruction.
+template <int C>
+__device__ __forceinline__ void fma_scaled(float* acc, const uint32_t* v, float s) {
+  uint64_t s2;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
+#pragma unroll
+  for (int i = 0; i < C; i += 2) {
+    uint64_t a, x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(acc[i]), "f"(acc[i + 1]));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(v[i]), "r"(v[i + 1]));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(x), "l"(s2));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[i]), "=f"(acc[i + 1]) : "l"(a));
+  }
+}
+
+// Arrival of lane 0 on a cluster-window mbarrier, without a branch.
+__device__ __forceinline__ void arrive_lane0(uint32_t bar, int lane) {
+  asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cluster.b64 _, [%0];\n}\n" ::"r"(bar), "r"(lane)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint32_t a, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(a), "r"(parity) : "memory");
+  return ok != 0u;
+}
+
+// acc += s * the warp's 128 accumulator columns.  The accumulator is released once its last load is complete, and the
+// next one's barrier probed while the sums run.
+__device__ __forceinline__ bool drain_wide(uint32_t taddr, float s, uint32_t release, int lane, uint32_t next_bar,
+                                           uint32_t next_parity, float (&acc)[G_PART]) {
+  uint32_t v[64];
+  tmem_fetch(taddr, v);
+  tmem_ready(v);
+  fma_scaled<64>(acc, v, s);
+  tmem_fetch(taddr + 64, v);
+  tmem_ready(v);
+  tc_fence_before();
+  arrive_lane0(release, lane);
+  const bool next = mbar_test(next_bar, next_parity);
+  fma_scaled<64>(acc + 64, v, s);
+  return next;
+}
+
+// The warp's staging buffer holds 64 channels of 32 token rows as [32][64] bf16 in the 128-byte swizzle: 16-byte chunk
+// c of row r at c ^ (r & 7), so neither the row-wise writes nor the reads conflict.
+__device__ __forceinline__ uint32_t stg_at(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// The staged rows to y rows row0 + r < row0 + rows, channels n0 ..
+__device__ __forceinline__ void store_wide(const uint8_t* stg, uint16_t* y, int64_t row0, int rows, int64_t N,
+                                           int64_t n0, bool vec, int lane) {
+  const int c = lane & 7;
+#pragma unroll 1
+  for (int r = lane >> 3; r < rows; r += 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(stg + stg_at(r, c));
+    uint16_t* d = y + (row0 + r) * N + n0 + 8 * c;
+    if (vec && n0 + 8 * c + 8 <= N) {
+      *reinterpret_cast<uint4*>(d) = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (n0 + 8 * c + k < N) d[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+    }
+  }
+}
+
+// The same by TMA (32 whole rows; columns past N are cut off by the map), asynchronously: stg_free() before the
+// buffer is written again.
+__device__ __forceinline__ void tma_store_rows(const CUtensorMap* map, uint32_t stg, int x, int y) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n"
+      " @e cp.async.bulk.commit_group;\n}\n" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(stg), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void stg_free() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G_THREADS, 1)
+fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                const __grid_constant__ CUtensorMap tmY, const int y_tma, const KArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar_full[G_STAGES];   // even CTA: both CTAs' tiles of the stage landed
+  __shared__ __align__(8) uint64_t bar_empty[G_STAGES];  // both parts' MMAs reading the stage are done
+  __shared__ __align__(8) uint64_t bar_accf[4];          // [part][2]: the accumulator is complete
+  __shared__ __align__(8) uint64_t bar_acce[4];          // even CTA: both CTAs drained it
+  __shared__ __align__(8) uint64_t bar_scf[F_SRING];     // the group's scales are in shared memory
+  __shared__ __align__(8) uint64_t bar_sce[F_SRING];     // the epilogue warps read them
+  __shared__ uint32_t s_tmem_base;
+  __shared__ volatile int s_abort;
+  __shared__ int s_bad;
+  __shared__ int s_prefix[F_MAX_E + 1];
+  __shared__ int s_off[F_MAX_E + 1];
+  __shared__ int s_warp[G_THREADS / 32];
+  __shared__ WSeg s_seg[F_EPI_WARPS];   // the epilogue warps' segment and place in the walk: 128 sums a thread leave
+  __shared__ Walk s_walk[F_EPI_WARPS];  // no registers to hold them through the block loop
+  __shared__ unsigned long long s_rows;
+
+  const int tid = threadIdx.x;
+  const int warp = uni(tid >> 5);
+  const int lane = tid & 31;
+  const int E = a.E;
+  const int64_t N = a.N;
+  const int KB = static_cast<int>((a.K + F_BK - 1) / F_BK);
+  const int WB = static_cast<int>((N + G_CH - 1) / G_CH);
+
+  uint8_t* stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t stage_base = smem_u32(stages);
+  float* s_scale = reinterpret_cast<float*>(stages + G_STAGES * G_STAGE_BYTES);  // [ring][4 blocks][2 parts][128]
+  uint8_t* s_out = stages + G_STAGES * G_STAGE_BYTES + G_SCALE_BYTES;
+  uint32_t rank, cluster_id, nclusters;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(cluster_id));
+  asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(nclusters));
+
+  if (tid == 0) {
+    s_abort = 0;
+    s_bad = 0;
+    s_rows = 0ull;
+    for (int s = 0; s < G_STAGES; ++s) {
+      mbar_init(smem_u32(&bar_full[s]), 1);
+      mbar_init(smem_u32(&bar_empty[s]), 2);
+    }
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(smem_u32(&bar_accf[b]), 1);
+      mbar_init(smem_u32(&bar_acce[b]), F_EPI_WARPS);  // four warps of each CTA
+    }
+    for (int s = 0; s < F_SRING; ++s) {
+      mbar_init(smem_u32(&bar_scf[s]), 1);
+      mbar_init(smem_u32(&bar_sce[s]), F_EPI_WARPS);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmW);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem_base)),
+                 "r"(F_TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  __syncthreads();  // s_bad and s_rows, before the scan may set them
+  pdl_trigger();
+  pdl_wait();
+  int units;
+  const int rows_total = scan_checked<G_THREADS>(
+      a, [WB](int c) { return wide_blocks(c) * WB; }, s_off, s_prefix, s_warp, &s_bad, &s_rows, &units);
+  tc_fence_before();
+  cluster_sync_all();  // both CTAs' barriers and tensor memory exist before either touches the other's
+  tc_fence_after();
+  const uint32_t tmem_base = static_cast<uint32_t>(uni(static_cast<int>(s_tmem_base)));
+  if (bad_list(a, rows_total, s_bad, s_rows)) {
+    if (tid == 0 && blockIdx.x == 0) set_status(a.status, W8A8_ERR_GROUP_LIST, 0u);
+    units = 0;
+  }
+  const int me = static_cast<int>(cluster_id);
+  int64_t total;
+  int runs;
+  const Walk walk0 = start_walk(units, KB, static_cast<int>(nclusters), me, total, runs);
+
+  if (warp < G_EPI0) {
+    // the epilogue's 128 sums a thread take registers from these warps (384 x 168 at launch = 128 x 88 + 256 x 208)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0) {
+      // ---------------------------------------------------------- TMA producer (both CTAs)
+      const uint32_t full_even0 = smem_cluster_addr(smem_u32(&bar_full[0]), 0);
+      int stage = 0;
+      uint32_t phase = 0;
+      Walk w = walk0;
+      WSeg s;
+      bool ok = true;
+      while (ok && uni(next_wide(w, E, WB, s_prefix, s_off, s))) {
+        const int yx = uni(s.row0 + static_cast<int>(rank) * G_HALF);
+        const int yw = uni(static_cast<int>(static_cast<int64_t>(s.e) * N) + s.wb * G_CH +
+                           static_cast<int>(rank) * (G_PART / 2));
+        const int kb1 = uni(s.kb1);
+        for (int kb = uni(s.kb0); kb < kb1; ++kb) {
+          ok = wait_all(smem_u32(&bar_empty[0]) + 8 * stage, phase ^ 1u, &s_abort, a.status, 1u);
+          if (!ok) break;
+          if (rank == 0) expect_tx_elect(smem_u32(&bar_full[0]) + 8 * stage, 2u * G_STAGE_BYTES);
+          const uint32_t full = full_even0 + 8 * stage;
+          const uint32_t sa = stage_base + stage * G_STAGE_BYTES;
+          tma_pair_elect(sa, &tmX, kb * F_BK, yx, full);
+          tma_pair_elect(sa + G_X_BYTES, &tmW, kb * F_BK, yw, full);
+          tma_pair_elect(sa + G_X_BYTES + G_P_BYTES, &tmW, kb * F_BK, yw + G_PART, full);
+          if (++stage == G_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Drain: the last fill of every stage has been consumed, so no copy into this CTA and no MMA arrival on its
+      // barriers is still in flight when the cluster leaves.
+      for (int i = 0; i < G_STAGES && ok; ++i) {
+        ok = wait_all(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 5u);
+        if (++stage == G_STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    } else if (warp < 3) {
+      // ----------------------------------------------------------- MMA issuers (even CTA, whole warps)
+      if (rank == 0) {
+        // The blocks of all segments in one sequence (the accumulators restart at every block, so tiles do not matter
+        // here), unrolled over the ring: stage and accumulator are constants of each body, and the descriptors stay in
+        // uniform registers.
+        const int p = warp - 1;
+        constexpr uint32_t idesc = (1u << 4) | (uint32_t(G_PART >> 3) << 17) | (uint32_t(G_TOK >> 4) << 24);
+        const int64_t blocks = walk0.step == 0 ? walk0.end - walk0.x
+                               : walk0.x < walk0.end ? (walk0.end - walk0.x + walk0.step - 1) / walk0.step * KB : 0;
+        const int nblk = uni(static_cast<int>(min(blocks, static_cast<int64_t>(INT32_MAX))));
+        const uint64_t adesc0 = smem_desc_sw128(stage_base);
+        const uint64_t bdesc0 = smem_desc_sw128(stage_base + G_X_BYTES + p * G_P_BYTES);
+        const uint32_t acc0 = tmem_base + 2 * p * G_PART;
+        const uint32_t accf0 = smem_u32(&bar_accf[2 * p]), acce0 = smem_u32(&bar_acce[2 * p]);
+        const uint32_t full0 = smem_u32(&bar_full[0]), empty0 = smem_u32(&bar_empty[0]);
+        bool ok = true;
+        uint32_t round = 0;
+        for (int g = 0; ok && g < nblk; g += G_STAGES, ++round) {
+#pragma unroll
+          for (int s = 0; s < G_STAGES; ++s) {
+            if (g + s >= nblk) break;
+            const uint32_t gi = round * G_STAGES + s;
+            const uint32_t b = gi & 1u;
+            ok = wait_all(full0 + 8 * s, round & 1u, &s_abort, a.status, 3u) &&
+                 wait_all(acce0 + 8 * b, ((gi >> 1) + 1u) & 1u, &s_abort, a.status, 2u);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < F_BK / 32; ++k)
+              mma_pair_f8(acc0 + b * G_PART, adesc0 + (s * (G_STAGE_BYTES >> 4) + 2u * k),
+                          bdesc0 + (s * (G_STAGE_BYTES >> 4) + 2u * k), idesc, k > 0 ? 1u : 0u);
+            tc_commit_pair_mc(accf0 + 8 * b, F_PAIR_MASK);
+            tc_commit_pair_mc(empty0 + 8 * s, F_PAIR_MASK);  // this part is done with the stage
+          }
+        }
+      }
+    } else {
+      // ----------------------------------------------------------- scales (both CTAs)
+      const int NB = static_cast<int>((N + 127) / 128);
+      const bool vec = (KB & 3) == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 15u) == 0u;
+      int slot = 0;
+      uint32_t phase = 0;
+      Walk w = walk0;
+      WSeg s;
+      bool ok = true;
+      while (ok && uni(next_wide(w, E, WB, s_prefix, s_off, s))) {
+        const int nb = 2 * s.wb;
+        const float* w0 = a.wsc + (static_cast<int64_t>(s.e) * NB + nb) * KB;
+        const bool two = nb + 1 < NB;
+        const int t0 = static_cast<int>(rank) * G_HALF + lane;
+        for (int g = s.kb0 / F_SG; g * F_SG < s.kb1; ++g) {
+          const int k0 = g * F_SG;
+          float v[4][F_SG];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float* p = a.xs + (static_cast<int64_t>(s.row0) + t0 + 32 * i) * KB + k0;
+            const bool in = t0 + 32 * i < s.tvalid;
+            if (vec) {
+              const float4 f = in ? *reinterpret_cast<const float4*>(p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
+            } else {
+#pragma unroll
+              for (int j = 0; j < F_SG; ++j) v[i][j] = in && k0 + j < KB ? p[j] : 0.0f;
+            }
+          }
+          float wv[2][F_SG];
+#pragma unroll
+          for (int j = 0; j < F_SG; ++j) {
+            wv[0][j] = k0 + j < KB ? w0[k0 + j] : 0.0f;
+            wv[1][j] = two && k0 + j < KB ? w0[KB + k0 + j] : 0.0f;
+          }
+          ok = wait_all(smem_u32(&bar_sce[slot]), phase ^ 1u, &s_abort, a.status, 11u);
+          if (!ok) break;
+          float* d = s_scale + slot * F_SG * 2 * G_HALF + lane;
+#pragma unroll
+          for (int j = 0; j < F_SG; ++j)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) d[(j * 2 + p) * G_HALF + 32 * i] = v[i][j] * wv[p][j];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bar_scf[slot]));
+          if (++slot == F_SRING) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue (both CTAs)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int ew = warp - G_EPI0;
+    const int q = warp & 3;
+    const int p = ew >> 2;
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + 2 * p * G_PART;
+    const uint32_t acce_even = smem_cluster_addr(smem_u32(&bar_acce[2 * p]), 0);
+    uint8_t* stg = s_out + ew * G_STG_WARP;
+    int buf = 0, slot = 0;
+    uint32_t bphase = 0, sphase = 0;
+    bool probed = false;  // the next accumulator was seen complete
+    const uint32_t accf0 = smem_u32(&bar_accf[2 * p]);
+    s_walk[ew] = walk0;
+    bool ok = true;
+    while (ok) {
+      __syncwarp();
+      {
+        Walk w = s_walk[ew];
+        WSeg s;
+        if (!uni(next_wide(w, E, WB, s_prefix, s_off, s))) break;
+        __syncwarp();
+        if (lane == 0) {
+          s_walk[ew] = w;
+          s_seg[ew] = s;
+        }
+        __syncwarp();
+      }
+      const int kb1 = uni(s_seg[ew].kb1);
+      float acc[G_PART];
+#pragma unroll
+      for (int i = 0; i < G_PART; ++i) acc[i] = 0.0f;
+      int kb = uni(s_seg[ew].kb0);
+      bool fresh = true;
+      for (; kb < kb1; ++kb) {
+        if (fresh || (kb & (F_SG - 1)) == 0)
+          ok = wait_all(smem_u32(&bar_scf[slot]), sphase, &s_abort, a.status, 6u);
+        fresh = false;
+        if (!ok) break;
+        const float* sc = s_scale + (slot * F_SG + (kb & (F_SG - 1))) * 2 * G_HALF + 32 * q + lane;
+        const float s0 = sc[p * G_HALF];
+        if (!probed) ok = wait_all(accf0 + 8u * buf, bphase, &s_abort, a.status, 4u);
+        if (!ok) break;
+        tc_fence_after();
+        probed = __all_sync(0xffffffffu, drain_wide(lane_addr + buf * G_PART, s0, acce_even + 8u * buf, lane, accf0 + 8u * (buf ^ 1),
+                                                    bphase ^ static_cast<uint32_t>(buf), acc));
+        buf ^= 1;
+        if (buf == 0) bphase ^= 1u;
+        if ((kb & (F_SG - 1)) == F_SG - 1 || kb == kb1 - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bar_sce[slot]));
+          if (++slot == F_SRING) {
+            slot = 0;
+            sphase ^= 1u;
+          }
+        }
+      }
+      if (!ok) break;
+      const WSeg s = s_seg[ew];
+      const int64_t n0 = static_cast<int64_t>(s.wb) * G_CH + p * G_PART;
+      const int rbase = static_cast<int>(rank) * G_HALF + 32 * q;  // first token of the warp inside the tile
+      const int rows = min(32, s.tvalid - rbase);
+      if (n0 >= N || rows <= 0) continue;
+      const int64_t row0 = static_cast<int64_t>(s.row0) + rbase;
+      const bool vec = (N & 7) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0u;
+      // 8 channels (16 bytes) of the lane's row into the staging buffer
+      auto stage8 = [&](int c, const float (&f)[8]) {
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float lo = f[2 * k], hi = f[2 * k + 1];
+          if (a.bias != nullptr) {
+            const int64_t n = n0 + 8 * c + 2 * k;
+            lo += n < N ? bf16_bits_to_f32(a.bias[n]) : 0.0f;
+            hi += n + 1 < N ? bf16_bits_to_f32(a.bias[n + 1]) : 0.0f;
+          }
+          o[k] = f32x2_to_bf16x2_bits(lo, hi);
+        }
+        *reinterpret_cast<uint4*>(stg + stg_at(lane, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+      };
+      if (s.kb0 == 0 && s.kb1 == KB) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (n0 + half * 64 >= N) break;
+          stg_free();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = acc[(half * 8 + c) * 8 + k];
+            stage8(half * 8 + c, f);
+          }
+          if (y_tma != 0 && rows == 32) {
+            tma_store_rows(&tmY, smem_u32(stg), static_cast<int>(n0) + half * 64, static_cast<int>(row0));
+          } else {
+            __syncwarp();
+            store_wide(stg, a.y, row0, rows, N, n0 + half * 64, vec, lane);
+          }
+        }
+      } else {
+        // a piece of a cut unit (as in fp8_gemm.cu): [channel][token] partial sums
+        const int64_t u0 = static_cast<int64_t>(s.unit) * KB;
+        const int first = run_owner(total, runs, u0), last = run_owner(total, runs, u0 + KB - 1);
+        auto piece = [&](int c) {
+          return a.pieces + ((static_cast<int64_t>(c) * 2 + (c == first ? 1 : 0)) * 2 + rank) * kWidePiece +
+                 static_cast<int64_t>(ew) * G_PART * 32 + lane;
+        };
+        float* mine = piece(me);
+#pragma unroll
+        for (int i = 0; i < G_PART; ++i) __stcg(mine + i * 32, acc[i]);
+        __threadfence();
+        __syncwarp();
+        uint32_t* ctr = a.counters + (first * 2 + static_cast<int>(rank)) * F_EPI_WARPS + ew;
+        uint32_t arrived = 0;
+        if (lane == 0) arrived = atomicAdd(ctr, 1u);
+        arrived = __shfl_sync(0xffffffffu, arrived, 0);
+        if (arrived == static_cast<uint32_t>(last - first)) {
+          __threadfence();
+          if (lane == 0) *ctr = 0u;
+          for (int half = 0; half < 2; ++half) {
+            if (n0 + half * 64 >= N) break;
+            stg_free();
+            for (int c = 0; c < 8; ++c) {
+              float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+              for (int r = first; r <= last; ++r) {
+                const float* src = piece(r) + (half * 8 + c) * 8 * 32;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] += __ldcg(src + k * 32);
+              }
+              stage8(half * 8 + c, f);
+            }
+            __syncwarp();
+            store_wide(stg, a.y, row0, rows, N, n0 + half * 64, vec, lane);
+          }
+        }
+      }
+    }
+  }
+
+  // (a warp's last TMA stores read their staging buffer before it exits)
+  if (warp >= G_EPI0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+
+  // ---- teardown: on abort, give in-flight copies and MMAs time to land first, then the pair leaves together.
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (s_abort) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 20000000ull) {
+    }
+  }
+  cluster_sync_all();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(F_TMEM_COLS)
+                 : "memory");
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_wide(const Fp8GemmArgs& g, const fp8::KArgs& a, int64_t pairs, cudaStream_t stream) {
+  CUtensorMap mx, mw, my;
+  const auto type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  if (!encode_map_2d(&mx, g.q, type, 1, g.R, g.K, F_BK, G_HALF, sw) ||
+      !encode_map_2d(&mw, g.w, type, 1, g.E * g.N, g.K, F_BK, G_PART / 2, sw))
+    return cudaErrorInvalidValue;
+  // bf16 y in boxes of 32 rows x 64 channels, where its rows start on 16-byte boundaries
+  const int y_tma = g.N % 8 == 0 && (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0u ? 1 : 0;
+  if (!y_tma) my = mx;
+  else if (!encode_map_2d(&my, g.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.R, g.N, 64, 32, sw)) return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(fp8_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kWideSmem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(fp8_wide_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(G_THREADS), kWideSmem, stream, mx,
+                    mw, my, y_tma, a);
+}
+
+}  // namespace w8a8
