@@ -467,6 +467,69 @@ def moe_layer(x: torch.Tensor, x_scale: Optional[torch.Tensor], topk_ids: torch.
     return y
 
 
+# The calls below run a few microseconds of GPU work at decode sizes, so their host side is kept short: one pass of
+# plain attribute tests per tensor (the full _need only to say what is wrong), no device guard where the tensors'
+# device is already current, and the library's functions looked up once.  On the GPU host (aarch64) a quantisation
+# call takes 6 us this way, 16 us with a guard, _stream and _need for every tensor.
+
+_bound = {}
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call(name: str, index: int, *args):
+    """The library's `name` on the current stream of CUDA device `index` (the last argument)."""
+    fn = _bound.get(name)
+    if fn is None:
+        fn = _bound[name] = getattr(_capi.lib(), name)
+    if torch.cuda.current_device() == index:
+        code = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, _raw_stream(index))
+    if code:
+        raise W8A8Error(name, code)
+
+
+def _size(name: str, *args) -> int:
+    return int(getattr(_capi.lib(), name)(*args))
+
+
+def _check(t, name: str, dtype: torch.dtype, shape, index: int):
+    """_need for a tensor of known shape on CUDA device `index`."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == index >= 0 and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape, torch.device("cuda", index) if index >= 0 else None)
+
+
+def _check_e4m3(t, name: str, shape, index: int):
+    """E4M3 codes: torch.float8_e4m3fn, or their bytes as torch.uint8."""
+    if not (type(t) is torch.Tensor and t.dtype is torch.float8_e4m3fn and t.get_device() == index >= 0
+            and t.shape == shape and t.is_contiguous()):
+        as_bytes = isinstance(t, torch.Tensor) and t.dtype is torch.uint8
+        _need(t, name, torch.uint8 if as_bytes else torch.float8_e4m3fn, shape,
+              torch.device("cuda", index) if index >= 0 else None)
+
+
+def _dims(t, name: str, n: int):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
+    return t.shape
+
+
+def _check_ws(ws, need_fn, index: int):
+    if ws is None:
+        return workspace(need_fn(), torch.device("cuda", index))
+    if not (type(ws) is torch.Tensor and ws.dtype is torch.uint8 and ws.get_device() == index and ws.is_contiguous()):
+        _need(ws, "ws", torch.uint8, None, torch.device("cuda", index))
+    return ws
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
 def moe_gate_topk(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, scoring: str = "softmax",
                   n_group: int = 1, topk_group: int = 1, group_score: str = "max", renormalize: bool = True,
                   routed_scale: float = 1.0, ids: Optional[torch.Tensor] = None,
@@ -477,59 +540,63 @@ def moe_gate_topk(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = N
     weights; n_group runs of E / n_group experts of which the topk_group best stay, by their largest key
     (group_score "max") or the sum of their two largest ("top2").  Ties go to the lowest index; an expert whose
     logit is -inf or NaN is chosen only when no other is left, with weight 0."""
-    if not isinstance(logits, torch.Tensor):
-        raise TypeError("logits must be a torch.Tensor")
-    if logits.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"logits must be torch.float32 or torch.bfloat16, got {logits.dtype}")
-    if logits.dim() != 2:
-        raise ValueError("logits must be [T,E]")
-    _need(logits, "logits", logits.dtype)
-    T, E = logits.shape
-    dev = logits.device
+    T, E = _dims(logits, "logits", 2)
+    dtype, dev = logits.dtype, logits.get_device()
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise TypeError(f"logits must be torch.float32 or torch.bfloat16, got {dtype}")
+    _check(logits, "logits", dtype, (T, E), dev)
     if bias is not None:
-        _need(bias, "bias", torch.float32, (E,), dev)
-    if scoring not in ("softmax", "sigmoid"):
+        _check(bias, "bias", torch.float32, (E,), dev)
+    if scoring == "sigmoid":
+        flags = _capi.GATE_SIGMOID
+    elif scoring == "softmax":
+        flags = 0
+    else:
         raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
-    if group_score not in ("max", "top2"):
+    if group_score == "top2":
+        flags |= _capi.GATE_GROUP_TOP2
+    elif group_score != "max":
         raise ValueError(f"group_score must be 'max' or 'top2', got {group_score!r}")
-    if n_group > 0 and 1 <= topk_group <= n_group and E % n_group == 0 and k > topk_group * (E // n_group):
+    if 1 <= topk_group <= n_group and E % n_group == 0 and k > topk_group * (E // n_group):
         raise ValueError(f"k = {k} exceeds the {topk_group * (E // n_group)} experts of {topk_group} groups")
-    flags = ((_capi.GATE_SIGMOID if scoring == "sigmoid" else 0)
-             | (_capi.GATE_GROUP_TOP2 if group_score == "top2" else 0)
-             | (_capi.GATE_RENORM if renormalize else 0)
-             | (_capi.GATE_BF16 if logits.dtype == torch.bfloat16 else 0))
-    ids = torch.empty((T, max(k, 0)), dtype=torch.int64, device=dev) if ids is None else ids
-    weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev) if weights is None else weights
-    _need(ids, "ids", torch.int64, (T, k), dev)
-    _need(weights, "weights", torch.float32, (T, k), dev)
-    with torch.cuda.device(dev):
-        _capi.check("moe_gate_topk", _capi.lib().moe_gate_topk(
-            logits.data_ptr(), T, E, _ptr(bias), n_group, topk_group, k, float(routed_scale), flags,
-            ids.data_ptr(), weights.data_ptr(), _stream(dev)))
+    if renormalize:
+        flags |= _capi.GATE_RENORM
+    if dtype is torch.bfloat16:
+        flags |= _capi.GATE_BF16
+    if ids is None:
+        ids = torch.empty((T, max(k, 0)), dtype=torch.int64, device=logits.device)
+    else:
+        _check(ids, "ids", torch.int64, (T, k), dev)
+    if weights is None:
+        weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
+    else:
+        _check(weights, "weights", torch.float32, (T, k), dev)
+    _call("moe_gate_topk", dev, logits.data_ptr(), T, E, None if bias is None else bias.data_ptr(), n_group, topk_group,
+          k, routed_scale, flags, ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
-def _need_e4m3(t: torch.Tensor, name: str, shape=None, device=None):
-    """E4M3 codes: torch.float8_e4m3fn, or their bytes as torch.uint8."""
-    dtype = t.dtype if isinstance(t, torch.Tensor) and t.dtype == torch.uint8 else torch.float8_e4m3fn
-    _need(t, name, dtype, shape, device)
-
-
-def _blocks(n: int) -> int:
-    return (n + 127) // 128
+def _quant_out(q, scale, rows: int, K: int, device, dev: int):
+    kb = _blocks(K)
+    if q is None:
+        q = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=device)
+    else:
+        _check_e4m3(q, "q", (rows, K), dev)
+    if scale is None:
+        scale = torch.empty((rows, kb), dtype=torch.float32, device=device)
+    else:
+        _check(scale, "scale", torch.float32, (rows, kb), dev)
+    return q, scale
 
 
 def w8a8_fp8_quant(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None):
     """BF16 x [M,K] (K % 16 == 0) -> (float8_e4m3fn q [M,K], float32 scale [M, ceil(K/128)])."""
-    _need(x, "x", torch.bfloat16)
-    M, K = x.shape
-    q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device) if q is None else q
-    scale = torch.empty((M, _blocks(K)), dtype=torch.float32, device=x.device) if scale is None else scale
-    _need_e4m3(q, "q", (M, K), x.device)
-    _need(scale, "scale", torch.float32, (M, _blocks(K)), x.device)
-    with torch.cuda.device(x.device):
-        _capi.check("w8a8_fp8_quant", _capi.lib().w8a8_fp8_quant(
-            x.data_ptr(), M, K, q.data_ptr(), scale.data_ptr(), _stream(x.device)))
+    M, K = _dims(x, "x", 2)
+    dev = x.get_device()
+    if not (x.dtype is torch.bfloat16 and dev >= 0 and x.is_contiguous()):
+        _check(x, "x", torch.bfloat16, (M, K), dev)
+    q, scale = _quant_out(q, scale, M, K, x.device, dev)
+    _call("w8a8_fp8_quant", dev, x.data_ptr(), M, K, q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -537,24 +604,18 @@ def w8a8_fp8_swiglu_quant(y13: torch.Tensor, q: Optional[torch.Tensor] = None,
                           scale: Optional[torch.Tensor] = None):
     """BF16 y13 [R,2I] (gate half, up half) -> SwiGLU, quantised: (float8_e4m3fn q [R,I], float32 scale
     [R, ceil(I/128)])."""
-    _need(y13, "y13", torch.bfloat16)
-    R, two = y13.shape
+    R, two = _dims(y13, "y13", 2)
     if two % 2:
         raise ValueError("y13 must be [R,2I]")
-    I = two // 2
-    dev = y13.device
-    q = torch.empty((R, I), dtype=torch.float8_e4m3fn, device=dev) if q is None else q
-    scale = torch.empty((R, _blocks(I)), dtype=torch.float32, device=dev) if scale is None else scale
-    _need_e4m3(q, "q", (R, I), dev)
-    _need(scale, "scale", torch.float32, (R, _blocks(I)), dev)
-    with torch.cuda.device(dev):
-        _capi.check("w8a8_fp8_swiglu_quant", _capi.lib().w8a8_fp8_swiglu_quant(
-            y13.data_ptr(), R, I, q.data_ptr(), scale.data_ptr(), _stream(dev)))
+    dev = y13.get_device()
+    _check(y13, "y13", torch.bfloat16, (R, two), dev)
+    q, scale = _quant_out(q, scale, R, two // 2, y13.device, dev)
+    _call("w8a8_fp8_swiglu_quant", dev, y13.data_ptr(), R, two // 2, q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
 def fp8_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
-    return int(_capi.lib().w8a8_fp8_matmul_workspace_bytes(M, N, K))
+    return _size("w8a8_fp8_matmul_workspace_bytes", M, N, K)
 
 
 def w8a8_fp8_matmul(q: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -562,29 +623,27 @@ def w8a8_fp8_matmul(q: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_s
                     y: Optional[torch.Tensor] = None):
     """E4M3 q [M,K] with x_scale [M, ceil(K/128)] x E4M3 w [N,K] with w_scale [ceil(N/128), ceil(K/128)]
     (+ bf16 bias [N]) -> bf16 y [M,N]."""
-    _need_e4m3(q, "q")
-    _need_e4m3(w, "w", None, q.device)
-    M, K = q.shape
-    N = w.shape[0]
-    dev = q.device
-    _need_e4m3(w, "w", (N, K), dev)
-    _need(x_scale, "x_scale", torch.float32, (M, _blocks(K)), dev)
-    _need(w_scale, "w_scale", torch.float32, (_blocks(N), _blocks(K)), dev)
+    M, K = _dims(q, "q", 2)
+    N = _dims(w, "w", 2)[0]
+    dev, kb = q.get_device(), (K + 127) // 128
+    _check_e4m3(q, "q", (M, K), dev)
+    _check_e4m3(w, "w", (N, K), dev)
+    _check(x_scale, "x_scale", torch.float32, (M, kb), dev)
+    _check(w_scale, "w_scale", torch.float32, ((N + 127) // 128, kb), dev)
     if bias is not None:
-        _need(bias, "bias", torch.bfloat16, (N,), dev)
-    ws = workspace(fp8_matmul_workspace_bytes(M, N, K), dev) if ws is None else ws
-    _need(ws, "ws", torch.uint8, None, dev)
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if y is None else y
-    _need(y, "y", torch.bfloat16, (M, N), dev)
-    with torch.cuda.device(dev):
-        _capi.check("w8a8_fp8_matmul", _capi.lib().w8a8_fp8_matmul(
-            q.data_ptr(), x_scale.data_ptr(), M, K, w.data_ptr(), w_scale.data_ptr(), N, _ptr(bias), y.data_ptr(),
-            ws.data_ptr(), ws.numel(), _stream(dev)))
+        _check(bias, "bias", torch.bfloat16, (N,), dev)
+    ws = _check_ws(ws, lambda: fp8_matmul_workspace_bytes(M, N, K), dev)
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=q.device)
+    else:
+        _check(y, "y", torch.bfloat16, (M, N), dev)
+    _call("w8a8_fp8_matmul", dev, q.data_ptr(), x_scale.data_ptr(), M, K, w.data_ptr(), w_scale.data_ptr(), N,
+          None if bias is None else bias.data_ptr(), y.data_ptr(), ws.data_ptr(), ws.numel())
     return y
 
 
 def fp8_grouped_matmul_workspace_bytes(E: int, R: int, N: int, K: int) -> int:
-    return int(_capi.lib().w8a8_fp8_grouped_matmul_workspace_bytes(E, R, N, K))
+    return _size("w8a8_fp8_grouped_matmul_workspace_bytes", E, R, N, K)
 
 
 def w8a8_fp8_grouped_matmul(q: torch.Tensor, x_scale: torch.Tensor, group_list: torch.Tensor, w: torch.Tensor,
@@ -592,30 +651,26 @@ def w8a8_fp8_grouped_matmul(q: torch.Tensor, x_scale: torch.Tensor, group_list: 
                             y: Optional[torch.Tensor] = None):
     """E4M3 q [R,K] (rows grouped by expert) with x_scale [R, ceil(K/128)] x E4M3 w [E,N,K] with w_scale
     [E, ceil(N/128), ceil(K/128)] -> bf16 y [R,N]."""
-    _need_e4m3(q, "q")
-    R, K = q.shape
-    dev = q.device
-    _need_e4m3(w, "w", None, dev)
-    if w.dim() != 3:
-        raise ValueError("w must be [E,N,K]")
-    E, N, _ = w.shape
-    _need_e4m3(w, "w", (E, N, K), dev)
-    _need(group_list, "group_list", torch.int64, (E,), dev)
-    _need(x_scale, "x_scale", torch.float32, (R, _blocks(K)), dev)
-    _need(w_scale, "w_scale", torch.float32, (E, _blocks(N), _blocks(K)), dev)
-    ws = workspace(fp8_grouped_matmul_workspace_bytes(E, R, N, K), dev) if ws is None else ws
-    _need(ws, "ws", torch.uint8, None, dev)
-    y = torch.empty((R, N), dtype=torch.bfloat16, device=dev) if y is None else y
-    _need(y, "y", torch.bfloat16, (R, N), dev)
-    with torch.cuda.device(dev):
-        _capi.check("w8a8_fp8_grouped_matmul", _capi.lib().w8a8_fp8_grouped_matmul(
-            q.data_ptr(), x_scale.data_ptr(), group_list.data_ptr(), E, R, K, w.data_ptr(), w_scale.data_ptr(), N,
-            y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)))
+    R, K = _dims(q, "q", 2)
+    E, N, _ = _dims(w, "w", 3)
+    dev, kb = q.get_device(), _blocks(K)
+    _check_e4m3(q, "q", (R, K), dev)
+    _check_e4m3(w, "w", (E, N, K), dev)
+    _check(group_list, "group_list", torch.int64, (E,), dev)
+    _check(x_scale, "x_scale", torch.float32, (R, kb), dev)
+    _check(w_scale, "w_scale", torch.float32, (E, _blocks(N), kb), dev)
+    ws = _check_ws(ws, lambda: fp8_grouped_matmul_workspace_bytes(E, R, N, K), dev)
+    if y is None:
+        y = torch.empty((R, N), dtype=torch.bfloat16, device=q.device)
+    else:
+        _check(y, "y", torch.bfloat16, (R, N), dev)
+    _call("w8a8_fp8_grouped_matmul", dev, q.data_ptr(), x_scale.data_ptr(), group_list.data_ptr(), E, R, K,
+          w.data_ptr(), w_scale.data_ptr(), N, y.data_ptr(), ws.data_ptr(), ws.numel())
     return y
 
 
 def moe_fp8_layer_workspace_bytes(T: int, k: int, H: int, I: int, E: int) -> int:
-    return int(_capi.lib().moe_fp8_layer_workspace_bytes(T, k, H, I, E))
+    return _size("moe_fp8_layer_workspace_bytes", T, k, H, I, E)
 
 
 def moe_fp8_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor, w13: torch.Tensor,
@@ -623,31 +678,29 @@ def moe_fp8_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.T
                   ws: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
     """MoE layer on block-scaled FP8 weights: bf16 x [T,H], topk_ids int64 [T,k] and topk_weights float32 [T,k]
     (moe_gate_topk), E4M3 w13 [E,2I,H] and w2 [E,H,I] with their float32 block scales -> bf16 y [T,H]."""
-    _need(x, "x", torch.bfloat16)
-    T, H = x.shape
-    dev = x.device
-    _need(topk_ids, "topk_ids", torch.int64, None, dev)
-    if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
+    T, H = _dims(x, "x", 2)
+    T2, k = _dims(topk_ids, "topk_ids", 2)
+    E, two, _ = _dims(w13, "w13", 3)
+    if T2 != T:
         raise ValueError("topk_ids must be [T,k]")
-    k = topk_ids.shape[1]
-    _need(topk_weights, "topk_weights", torch.float32, (T, k), dev)
-    _need_e4m3(w13, "w13", None, dev)
-    if w13.dim() != 3 or w13.shape[1] % 2:
+    if two % 2:
         raise ValueError("w13 must be [E,2I,H]")
-    E, I = w13.shape[0], w13.shape[1] // 2
-    _need_e4m3(w13, "w13", (E, 2 * I, H), dev)
-    _need_e4m3(w2, "w2", (E, H, I), dev)
-    _need(w13_scale, "w13_scale", torch.float32, (E, _blocks(2 * I), _blocks(H)), dev)
-    _need(w2_scale, "w2_scale", torch.float32, (E, _blocks(H), _blocks(I)), dev)
-    ws = workspace(moe_fp8_layer_workspace_bytes(T, k, H, I, E), dev) if ws is None else ws
-    _need(ws, "ws", torch.uint8, None, dev)
-    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if y is None else y
-    _need(y, "y", torch.bfloat16, (T, H), dev)
-    with torch.cuda.device(dev):
-        _capi.check("moe_fp8_layer", _capi.lib().moe_fp8_layer(
-            x.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), T, k, E, H, I, w13.data_ptr(),
-            w13_scale.data_ptr(), w2.data_ptr(), w2_scale.data_ptr(), ws.data_ptr(), ws.numel(), y.data_ptr(),
-            _stream(dev)))
+    I, dev = two // 2, x.get_device()
+    _check(x, "x", torch.bfloat16, (T, H), dev)
+    _check(topk_ids, "topk_ids", torch.int64, (T, k), dev)
+    _check(topk_weights, "topk_weights", torch.float32, (T, k), dev)
+    _check_e4m3(w13, "w13", (E, two, H), dev)
+    _check_e4m3(w2, "w2", (E, H, I), dev)
+    _check(w13_scale, "w13_scale", torch.float32, (E, _blocks(two), _blocks(H)), dev)
+    _check(w2_scale, "w2_scale", torch.float32, (E, _blocks(H), _blocks(I)), dev)
+    ws = _check_ws(ws, lambda: moe_fp8_layer_workspace_bytes(T, k, H, I, E), dev)
+    if y is None:
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    else:
+        _check(y, "y", torch.bfloat16, (T, H), dev)
+    _call("moe_fp8_layer", dev, x.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), T, k, E, H, I,
+          w13.data_ptr(), w13_scale.data_ptr(), w2.data_ptr(), w2_scale.data_ptr(), ws.data_ptr(), ws.numel(),
+          y.data_ptr())
     return y
 
 

@@ -16,9 +16,8 @@ constexpr int F_SRING = 2;           // scale groups in the ring
 constexpr int F_MAX_CLUSTERS = 76;   // CTA pairs, one CTA per SM
 constexpr int F_MAX_E = 1024;
 constexpr int F_SUPER = 32;          // token blocks per rasterisation group
-constexpr int F_MIN_RUN = 4;         // blocks per run at least
+constexpr int F_MAX_SPLIT = 8;        // pairs of a cluster that share a unit's K
 constexpr int F_EPI_WARPS = 8;
-constexpr uint16_t F_PAIR_MASK = 0x3;
 constexpr uint32_t F_TMEM_COLS = 512;
 constexpr size_t kCounterBytes = F_MAX_CLUSTERS * 2 * F_EPI_WARPS * 4;
 static_assert(kCounterBytes % 256 == 0, "pieces start 256-byte aligned");
@@ -34,6 +33,8 @@ struct KArgs {
   float* pieces;       // [clusters][2 slots][2 CTAs][kPiece]
   int64_t R, N, K;
   int E;
+  int split;  // pairs per cluster: 1, or the parts of K of a unit whose sums meet in distributed shared memory
+  int runs;   // dense: runs of cut units (0: units are not cut); grouped: -1, chosen on the device
 };
 
 // D(tmem, both CTAs) (+)= A * B, kind::f8f6f4 with both operands E4M3, on the CTA pair (issued by the elected lane
@@ -68,6 +69,13 @@ __device__ __forceinline__ void tma_pair_elect(uint32_t dst, const CUtensorMap* 
       " [%0], [%1, {%2, %3}], [%4];\n}\n"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(mbar_cluster)
       : "memory");
+}
+
+// A shared-memory word of CTA `rank` of the cluster.
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 // The value of lane 0.  Warp-uniform values and control flow (votes as loop conditions, bounds and indices passed
@@ -189,6 +197,16 @@ __device__ __forceinline__ void unit_tile(int unit, int E, int WB, const int* s_
 template <int NT, typename UnitsOf>
 __device__ __forceinline__ int scan_checked(const KArgs& a, UnitsOf units_of, int* s_off, int* s_prefix, int* s_warp,
                                             int* s_bad, unsigned long long* s_rows, int* units) {
+  if (a.group_list == nullptr) {  // one group of R rows (R <= INT32_MAX)
+    const int u = units_of(static_cast<int>(a.R));
+    if (threadIdx.x == 0) {
+      s_off[0] = s_prefix[0] = 0;
+      s_off[1] = static_cast<int>(a.R);
+      s_prefix[1] = u;
+    }
+    *units = u;
+    return static_cast<int>(a.R);
+  }
   GemmArgs ga;
   ga.group_list = a.group_list;
   ga.R = a.R;
@@ -203,22 +221,91 @@ __device__ __forceinline__ bool bad_list(const KArgs& a, int rows, int s_bad, un
          (a.group_list != nullptr && a.R > INT32_MAX / a.E && s_rows != static_cast<unsigned long long>(a.R));
 }
 
-// Many units: every C-th one; few: equal runs of blocks, at least F_MIN_RUN each.
-__device__ __forceinline__ Walk start_walk(int units, int KB, int nc, int me, int64_t& total, int& runs) {
+// How the units' blocks are shared out over C pairs, from costs in eighths of a block's time (about 0.4 us).  Uncut:
+// whole units, every C-th one to a pair.  Cut: equal runs of blocks, aligned to units where there are fewer runs
+// than pairs; the pieces of a cut unit cost about 9 blocks (write, fence, arrival) and one or three blocks a piece
+// to add (measured: 64 x 7168 x 2048 7.1 us uncut, 10.9 us in two pieces, 64 x 2048 x 7168 13.1 us in seven).
+struct RunPlan {
+  int runs;      // 0: uncut
+  int64_t cost;
+};
+__host__ __device__ inline RunPlan plan_runs(int64_t units, int KB, int C, bool wide) {
+  const int64_t fixed = 72, per = wide ? 24 : 8;
+  RunPlan p{0, (units + C - 1) / C * KB * 8};
+  if (units <= 0) return p;
+  const int64_t total = units * KB;
+  const int64_t all = total < C ? total : C;
+  if (units % C != 0) {
+    const int64_t c = (total + all - 1) / all * 8 + fixed + per * (all / units + 2);
+    if (c < p.cost) p = RunPlan{static_cast<int>(all), c};
+  }
+  for (int64_t ks = 2; ks * units <= C && ks <= KB; ++ks) {
+    const int64_t c = (KB + ks - 1) / ks * 8 + fixed + per * ks;
+    if (c < p.cost) p = RunPlan{static_cast<int>(ks * units), c};
+  }
+  return p;
+}
+
+// The walk of pair `me` of C.  split > 1: the pair's part of K of its cluster's one unit.
+__device__ __forceinline__ Walk start_walk(const KArgs& a, int units, int KB, int C, int me, bool wide, int64_t& total,
+                                           int& runs) {
   total = static_cast<int64_t>(units) * KB;
-  const bool cut = units < 4 * nc;
-  runs = static_cast<int>(min(static_cast<int64_t>(nc), max(static_cast<int64_t>(1), total / F_MIN_RUN)));
   Walk w;
   w.KB = KB;
-  w.step = cut ? 0 : nc;
-  w.x = !cut ? me : me < runs ? run_begin(total, runs, me) : 0;
-  w.end = !cut ? units : me < runs ? run_begin(total, runs, me + 1) : 0;
+  w.step = 0;
+  w.x = w.end = 0;
+  if (a.split > 1) {
+    runs = 0;
+    const int unit = me / a.split, part = me % a.split;
+    if (unit < units) {
+      w.x = static_cast<int64_t>(unit) * KB + static_cast<int64_t>(KB) * part / a.split;
+      w.end = static_cast<int64_t>(unit) * KB + static_cast<int64_t>(KB) * (part + 1) / a.split;
+    }
+    return w;
+  }
+  runs = a.runs >= 0 ? min(a.runs, static_cast<int>(min(total, static_cast<int64_t>(C)))) : plan_runs(units, KB, C, wide).runs;
+  if (runs == 0) {
+    w.step = C;
+    w.x = me;
+    w.end = units;
+  } else if (me < runs) {
+    w.x = run_begin(total, runs, me);
+    w.end = run_begin(total, runs, me + 1);
+  }
   return w;
 }
 
 }  // namespace fp8
 
 // The contraction with tokens as the MMA's M side (fp8_wide.cu).
-cudaError_t launch_fp8_wide(const Fp8GemmArgs& g, const fp8::KArgs& a, int64_t pairs, cudaStream_t stream);
+cudaError_t launch_fp8_wide(const Fp8GemmArgs& g, const fp8::KArgs& a, int pairs, cudaStream_t stream);
+
+namespace fp8 {
+
+// Launch of `pairs` CTA pairs in clusters of `split` pairs, with programmatic stream serialization.
+template <typename... KArgsT, typename... Args>
+inline cudaError_t launch_pairs(void (*k)(KArgsT...), int pairs, int split, int threads, size_t smem, cudaStream_t stream,
+                                Args... args) {
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess && 2 * split > 8) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(2 * split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+}  // namespace fp8
 
 }  // namespace w8a8

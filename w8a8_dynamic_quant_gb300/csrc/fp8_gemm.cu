@@ -132,7 +132,7 @@ __device__ __forceinline__ void store_rows(const uint16_t* stg, uint16_t* out, i
 }
 
 template <int NT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
+__global__ void __launch_bounds__(F_THREADS, 1)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmXbig,
                 const __grid_constant__ CUtensorMap tmXsmall, const KArgs a) {
   using C = Cfg<NT>;
@@ -162,11 +162,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   uint8_t* stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t stage_base = smem_u32(stages);
   float* s_scale = reinterpret_cast<float*>(stages + C::kStages * C::kStageBytes);  // [ring][4 blocks][NT]
+  float* s_part = reinterpret_cast<float*>(stages);  // [epilogue warp][token][channel], after the last block
   uint16_t* s_out = reinterpret_cast<uint16_t*>(stages + C::kStages * C::kStageBytes + C::kScaleBytes);
-  uint32_t rank, cluster_id, nclusters;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  // CTAs 2i and 2i + 1 of a cluster are a pair; rank: the CTA's place in it
+  uint32_t crank, cluster_id, nclusters;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
   asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(cluster_id));
   asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(nclusters));
+  const uint32_t rank = crank & 1u, even = crank & ~1u;
+  const uint16_t pair_mask = static_cast<uint16_t>(3u << even);
 
   if (tid == 0) {
     s_abort = 0;
@@ -209,40 +213,38 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     if (tid == 0 && blockIdx.x == 0) set_status(a.status, W8A8_ERR_GROUP_LIST, 0u);
     units = 0;
   }
-  const int me = static_cast<int>(cluster_id);
+  const int me = static_cast<int>(cluster_id) * a.split + static_cast<int>(crank >> 1);
   int64_t total;
   int runs;
-  const Walk walk0 = start_walk(units, KB, static_cast<int>(nclusters), me, total, runs);
+  const Walk walk0 = start_walk(a, units, KB, static_cast<int>(nclusters), me, false, total, runs);
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
+    const uint32_t full_even0 = smem_cluster_addr(smem_u32(&bar_full[0]), even);
     int stage = 0;
     uint32_t phase = 0;
     Walk w = walk0;
     Seg s;
     bool ok = true;
     while (ok && uni(next_seg<NT>(w, E, WB, s_prefix, s_off, s))) {
-      const int yw = static_cast<int>(static_cast<int64_t>(s.e) * N) + s.wb * F_ROWS + static_cast<int>(rank) * F_HALF;
-      const uint32_t bytes = 2u * F_W_BYTES + static_cast<uint32_t>(s.n) * F_BK;
+      const int yw = uni(static_cast<int>(static_cast<int64_t>(s.e) * N) + s.wb * F_ROWS + static_cast<int>(rank) * F_HALF);
+      const int rows = uni(s.n >> 1);
+      const int yx = uni(s.row0 + static_cast<int>(rank) * (s.n >> 1));
+      const uint32_t bytes = 2u * F_W_BYTES + static_cast<uint32_t>(2 * rows) * F_BK;
       const int kb1 = uni(s.kb1);
       for (int kb = uni(s.kb0); kb < kb1; ++kb) {
         ok = wait_all(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 1u);
         if (!ok) break;
-        if (lane == 0) {
-          const uint32_t full = smem_u32(&bar_full[stage]);
-          if (rank == 0) mbar_expect_tx(full, bytes);
-          const uint32_t full_even = smem_cluster_addr(full, 0);
-          uint32_t dst = stage_base + stage * C::kStageBytes;
-          tma_load_2d_pair(dst, &tmW, kb * F_BK, yw, full_even);
-          dst += F_W_BYTES;
-          // the block's first n / 2 token rows go to the even CTA, the rest to the odd one
-          int rows = s.n >> 1, yx = s.row0 + static_cast<int>(rank) * rows;
-          for (; rows >= C::kBig; rows -= C::kBig, yx += C::kBig, dst += C::kBig * F_BK)
-            tma_load_2d_pair(dst, &tmXbig, kb * F_BK, yx, full_even);
-          for (; rows > 0; rows -= 8, yx += 8, dst += 8 * F_BK)
-            tma_load_2d_pair(dst, &tmXsmall, kb * F_BK, yx, full_even);
+        if (rank == 0) expect_tx_elect(smem_u32(&bar_full[0]) + 8 * stage, bytes);
+        const uint32_t full = full_even0 + 8 * stage;
+        const uint32_t dst = stage_base + stage * C::kStageBytes;
+        tma_pair_elect(dst, &tmW, kb * F_BK, yw, full);
+        // the block's first n / 2 token rows go to the even CTA, the rest to the odd one
+        if (rows == C::kBig) {
+          tma_pair_elect(dst + F_W_BYTES, &tmXbig, kb * F_BK, yx, full);
+        } else {
+          for (int r = 0; r < rows; r += 8) tma_pair_elect(dst + F_W_BYTES + r * F_BK, &tmXsmall, kb * F_BK, yx + r, full);
         }
-        __syncwarp();
         if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1u;
@@ -280,8 +282,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 #pragma unroll
           for (int k = 0; k < F_BK / 32; ++k)
             mma_pair_f8(tmem_base + buf * NT, adesc + 2u * k, bdesc + 2u * k, idesc, k > 0 ? 1u : 0u);
-          tc_commit_pair_mc(smem_u32(&bar_accf[buf]), F_PAIR_MASK);
-          tc_commit_pair_mc(smem_u32(&bar_empty[stage]), F_PAIR_MASK);  // frees the stage in both CTAs
+          tc_commit_pair_mc(smem_u32(&bar_accf[buf]), pair_mask);
+          tc_commit_pair_mc(smem_u32(&bar_empty[stage]), pair_mask);  // frees the stage in both CTAs
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1u;
@@ -348,7 +350,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const int q = warp & 3;
     const int h = ew >> 2;
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
-    const uint32_t acce_even = smem_cluster_addr(smem_u32(&bar_acce[0]), 0);
+    const uint32_t acce_even = smem_cluster_addr(smem_u32(&bar_acce[0]), even);
     uint16_t* stg = s_out + ew * 16 * 32;
     int buf = 0, slot = 0;
     uint32_t bphase = 0, sphase = 0;
@@ -411,6 +413,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             __syncwarp();
           }
         }
+      } else if (a.split > 1) {  // a part of K of the cluster's unit: its sums to the ring, which is at rest
+        float* d = s_part + ew * C::kCols * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < C::kCols; ++i)
+          if (i < tv) d[i * 32] = acc[i];
       } else {
         // a piece of a cut unit: partial sums to this pair's slot (1: the unit begins in this run, 0: it began in an
         // earlier one), then the last warp to arrive adds the unit's pieces in the order of K
@@ -437,11 +444,20 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             float sum[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
-            for (int c = first; c <= last; ++c) {
-              const float* src = piece(c) + t * 32;
+            for (int c = first; c <= last; c += 4) {  // four pieces' loads in flight, added in order
+              float v[4][16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (t + i < tv) sum[i] += __ldcg(src + i * 32);
+              for (int j = 0; j < 4; ++j) {
+                const float* src = piece(min(c + j, last)) + t * 32;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[j][i] = t + i < tv ? __ldcg(src + i * 32) : 0.0f;
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (c + j <= last) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) sum[i] += v[j][i];
+                }
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) stg[i * 32 + lane] = f32_to_bf16_bits(a.bias != nullptr ? sum[i] + bias : sum[i]);
@@ -449,6 +465,43 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             store_rows(stg, a.y, row0 + t, N, n0, min(16, tv - t), lane);
             __syncwarp();
           }
+        }
+      }
+    }
+  }
+
+  if (a.split > 1) {
+    // the parts' sums meet: every CTA adds its share of the tokens over its peers' shared memory, in the order of K
+    __syncwarp();
+    cluster_sync_all();
+    Walk w = walk0;
+    Seg s;
+    if (warp >= F_EPI0 && uni(next_seg<NT>(w, E, WB, s_prefix, s_off, s))) {
+      const int ew = warp - F_EPI0, h = ew >> 2;
+      const int split = ((s.n >> 1) + 15) & ~15;
+      const int tv = min(h == 0 ? split : s.n - split, s.tvalid - (h == 0 ? 0 : split));
+      const int64_t n0 = static_cast<int64_t>(s.wb) * F_ROWS + static_cast<int64_t>(rank) * F_HALF + 32 * (warp & 3);
+      if (n0 < N && tv > 0) {
+        const int part = static_cast<int>(crank >> 1);
+        const int t1 = tv * (part + 1) / a.split;
+        const float bias = a.bias != nullptr && n0 + lane < N ? bf16_bits_to_f32(a.bias[n0 + lane]) : 0.0f;
+        const uint32_t src = smem_u32(s_part + ew * C::kCols * 32 + lane);
+        uint16_t* stg = s_out + ew * 16 * 32;
+        for (int t = tv * part / a.split; t < t1; t += 16) {
+          float sum[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
+          for (int j = 0; j < a.split; ++j) {
+            const uint32_t p = smem_cluster_addr(src, 2 * j + rank) + t * 128;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (t + i < t1) sum[i] += ld_cluster(p + i * 128);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) stg[i * 32 + lane] = f32_to_bf16_bits(a.bias != nullptr ? sum[i] + bias : sum[i]);
+          __syncwarp();
+          store_rows(stg, a.y, static_cast<int64_t>(s.row0) + (h == 0 ? 0 : split) + t, N, n0, min(16, t1 - t), lane);
+          __syncwarp();
         }
       }
     }
@@ -477,17 +530,38 @@ int tile_tokens(int64_t E, int64_t R, bool grouped) {
   const int64_t want = grouped ? 2 * ((R + E - 1) / E) : R;
   return want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
 }
-// Pairs to launch.
-int64_t pairs_for(int64_t E, int64_t R, int64_t N, int64_t K, bool grouped, int64_t most) {
-  if (grouped) return most;
-  const int nt = tile_tokens(E, R, grouped);
-  const int64_t units = ((R + nt - 1) / nt) * ((N + F_ROWS - 1) / F_ROWS);
-  const int64_t total = units * ((K + F_BK - 1) / F_BK);
-  return std::max<int64_t>(1, std::min<int64_t>(most, total / F_MIN_RUN));
+
+struct Plan {
+  int nt, pairs, split, runs;
+};
+// Up to `most` pairs.  A dense problem of few tiles lets the pairs of a cluster share each tile's K (their sums meet
+// in distributed shared memory, about 3 or 7 blocks' time), as far as the clusters fit the GPU at once; else plan_runs.
+Plan make_plan(int64_t E, int64_t R, int64_t N, int64_t K, bool grouped, int most) {
+  Plan p{tile_tokens(E, R, grouped), most, 1, -1};
+  if (grouped) return p;
+  const bool wide = p.nt == 256;
+  const int64_t units = ((R + p.nt - 1) / p.nt) * ((N + F_ROWS - 1) / F_ROWS);
+  const int KB = static_cast<int>((K + F_BK - 1) / F_BK);
+  const RunPlan r = plan_runs(units, KB, most, wide);
+  p.runs = r.runs;
+  p.pairs = static_cast<int>(r.runs > 0 ? r.runs : std::min<int64_t>(units, most));
+  int64_t best = r.cost;
+  // clusters of 2 ks CTAs (one a SM) that are resident at once on 152 SMs, as the occupancy query gives them
+  constexpr int kFit[F_MAX_SPLIT + 1] = {0, 76, 36, 23, 15, 13, 8, 7, 7};
+  for (int ks = 2; ks <= F_MAX_SPLIT; ++ks) {
+    const int64_t cost = (KB + ks - 1) / ks * 8 + (wide ? 56 : 24);
+    if (units > kFit[ks] || units * ks > most || 2 * ks > KB || cost >= best) continue;
+    if (wide && 16 % ks != 0) continue;  // equal shares of a part's sixteen 8-channel chunks
+    best = cost;
+    p.split = ks;
+    p.runs = 0;
+    p.pairs = static_cast<int>(units) * ks;
+  }
+  return p;
 }
 
 template <int NT>
-cudaError_t launch_nt(const Fp8GemmArgs& g, const KArgs& a, int64_t pairs, cudaStream_t stream) {
+cudaError_t launch_nt(const Fp8GemmArgs& g, const KArgs& a, int pairs, cudaStream_t stream) {
   using C = Cfg<NT>;
   CUtensorMap mw, mb, ms;
   const auto type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -496,26 +570,23 @@ cudaError_t launch_nt(const Fp8GemmArgs& g, const KArgs& a, int64_t pairs, cudaS
       !encode_map_2d(&mb, g.q, type, 1, g.R, g.K, F_BK, C::kBig, sw) ||
       !encode_map_2d(&ms, g.q, type, 1, g.R, g.K, F_BK, 8, sw))
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(C::kSmem));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(fp8_gemm_kernel<NT>, dim3(static_cast<unsigned>(2 * pairs)), dim3(F_THREADS), C::kSmem, stream, mw,
-                    mb, ms, a);
+  return launch_pairs(fp8_gemm_kernel<NT>, pairs, a.split, F_THREADS, C::kSmem, stream, mw, mb, ms, a);
 }
 
 }  // namespace
 
 size_t fp8_gemm_ws_bytes(int64_t E, int64_t R, int64_t N, int64_t K, bool grouped) {
-  const int64_t pairs = pairs_for(E, R, N, K, grouped, F_MAX_CLUSTERS);
-  return kCounterBytes + static_cast<size_t>(pairs) * 4 * F_HALF * tile_tokens(E, R, grouped) * 4;
+  // pieces of cut units: at most two a pair, [2 CTAs][128 channels or tokens][tile tokens or channels] binary32 each
+  const Plan p = make_plan(E, R, N, K, grouped, F_MAX_CLUSTERS);
+  const size_t pieces = p.runs != 0 ? static_cast<size_t>(p.pairs) * 4 * F_HALF * p.nt * 4 : 0;
+  return kCounterBytes + pieces;
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, void* ws, int num_sms, cudaStream_t stream) {
   if (g.R == 0) return cudaSuccess;
   const bool grouped = g.group_list != nullptr;
-  const int nt = tile_tokens(g.E, g.R, grouped);
-  const int64_t most_units = (g.R / nt + g.E) * ((g.N + F_ROWS - 1) / F_ROWS);
-  if (most_units > INT32_MAX) return cudaErrorInvalidValue;
+  const Plan p = make_plan(g.E, g.R, g.N, g.K, grouped, std::min(num_sms / 2, F_MAX_CLUSTERS));
+  if ((g.R / p.nt + g.E) * ((g.N + F_ROWS - 1) / F_ROWS) > INT32_MAX) return cudaErrorInvalidValue;
   KArgs a;
   a.xs = g.x_scale;
   a.group_list = g.group_list;
@@ -529,12 +600,13 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, void* ws, int num_sms, cudaStr
   a.N = g.N;
   a.K = g.K;
   a.E = static_cast<int>(g.E);
-  const int64_t pairs = pairs_for(g.E, g.R, g.N, g.K, grouped, std::min(num_sms / 2, F_MAX_CLUSTERS));
-  switch (nt) {
-    case 32: return launch_nt<32>(g, a, pairs, stream);
-    case 64: return launch_nt<64>(g, a, pairs, stream);
-    case 128: return launch_nt<128>(g, a, pairs, stream);
-    default: return launch_fp8_wide(g, a, pairs, stream);
+  a.split = p.split;
+  a.runs = p.runs;
+  switch (p.nt) {
+    case 32: return launch_nt<32>(g, a, p.pairs, stream);
+    case 64: return launch_nt<64>(g, a, p.pairs, stream);
+    case 128: return launch_nt<128>(g, a, p.pairs, stream);
+    default: return launch_fp8_wide(g, a, p.pairs, stream);
   }
 }
 

@@ -115,10 +115,28 @@ __device__ __forceinline__ bool drain_wide(uint32_t taddr, float s, uint32_t rel
 // c of row r at c ^ (r & 7), so neither the row-wise writes nor the reads conflict.
 __device__ __forceinline__ uint32_t stg_at(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// The staged rows to y rows row0 + r < row0 + rows, channels n0 ..
+// 8 channels n0 + 8c .. (16 bytes; + bias) of the lane's row into the staging buffer.
+__device__ __forceinline__ void stage_chunk(uint8_t* stg, int c, int lane, const float (&f)[8], const uint16_t* bias,
+                                            int64_t n0, int64_t N) {
+  uint32_t o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float lo = f[2 * k], hi = f[2 * k + 1];
+    if (bias != nullptr) {
+      const int64_t n = n0 + 8 * c + 2 * k;
+      lo += n < N ? bf16_bits_to_f32(bias[n]) : 0.0f;
+      hi += n + 1 < N ? bf16_bits_to_f32(bias[n + 1]) : 0.0f;
+    }
+    o[k] = f32x2_to_bf16x2_bits(lo, hi);
+  }
+  *reinterpret_cast<uint4*>(stg + stg_at(lane, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// The staged rows to y rows row0 + r < row0 + rows, channels n0 .. (16-byte chunks [c_lo, c_hi) of them)
 __device__ __forceinline__ void store_wide(const uint8_t* stg, uint16_t* y, int64_t row0, int rows, int64_t N,
-                                           int64_t n0, bool vec, int lane) {
+                                           int64_t n0, bool vec, int lane, int c_lo = 0, int c_hi = 8) {
   const int c = lane & 7;
+  if (c < c_lo || c >= c_hi) return;
 #pragma unroll 1
   for (int r = lane >> 3; r < rows; r += 4) {
     const uint4 v = *reinterpret_cast<const uint4*>(stg + stg_at(r, c));
@@ -151,7 +169,7 @@ __device__ __forceinline__ void stg_free() {
   __syncwarp();
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G_THREADS, 1)
+__global__ void __launch_bounds__(G_THREADS, 1)
 fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                 const __grid_constant__ CUtensorMap tmY, const int y_tma, const KArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -182,11 +200,15 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   uint8_t* stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t stage_base = smem_u32(stages);
   float* s_scale = reinterpret_cast<float*>(stages + G_STAGES * G_STAGE_BYTES);  // [ring][4 blocks][2 parts][128]
+  float* s_part = reinterpret_cast<float*>(stages);  // [epilogue warp][channel][token], after the last block
   uint8_t* s_out = stages + G_STAGES * G_STAGE_BYTES + G_SCALE_BYTES;
-  uint32_t rank, cluster_id, nclusters;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  // CTAs 2i and 2i + 1 of a cluster are a pair; rank: the CTA's place in it
+  uint32_t crank, cluster_id, nclusters;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
   asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(cluster_id));
   asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(nclusters));
+  const uint32_t rank = crank & 1u, even = crank & ~1u;
+  const uint16_t pair_mask = static_cast<uint16_t>(3u << even);
 
   if (tid == 0) {
     s_abort = 0;
@@ -228,17 +250,17 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     if (tid == 0 && blockIdx.x == 0) set_status(a.status, W8A8_ERR_GROUP_LIST, 0u);
     units = 0;
   }
-  const int me = static_cast<int>(cluster_id);
+  const int me = static_cast<int>(cluster_id) * a.split + static_cast<int>(crank >> 1);
   int64_t total;
   int runs;
-  const Walk walk0 = start_walk(units, KB, static_cast<int>(nclusters), me, total, runs);
+  const Walk walk0 = start_walk(a, units, KB, static_cast<int>(nclusters), me, true, total, runs);
 
   if (warp < G_EPI0) {
     // the epilogue's 128 sums a thread take registers from these warps (384 x 168 at launch = 128 x 88 + 256 x 208)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
       // ---------------------------------------------------------- TMA producer (both CTAs)
-      const uint32_t full_even0 = smem_cluster_addr(smem_u32(&bar_full[0]), 0);
+      const uint32_t full_even0 = smem_cluster_addr(smem_u32(&bar_full[0]), even);
       int stage = 0;
       uint32_t phase = 0;
       Walk w = walk0;
@@ -305,8 +327,8 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             for (int k = 0; k < F_BK / 32; ++k)
               mma_pair_f8(acc0 + b * G_PART, adesc0 + (s * (G_STAGE_BYTES >> 4) + 2u * k),
                           bdesc0 + (s * (G_STAGE_BYTES >> 4) + 2u * k), idesc, k > 0 ? 1u : 0u);
-            tc_commit_pair_mc(accf0 + 8 * b, F_PAIR_MASK);
-            tc_commit_pair_mc(empty0 + 8 * s, F_PAIR_MASK);  // this part is done with the stage
+            tc_commit_pair_mc(accf0 + 8 * b, pair_mask);
+            tc_commit_pair_mc(empty0 + 8 * s, pair_mask);  // this part is done with the stage
           }
         }
       }
@@ -370,7 +392,7 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     const int q = warp & 3;
     const int p = ew >> 2;
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + 2 * p * G_PART;
-    const uint32_t acce_even = smem_cluster_addr(smem_u32(&bar_acce[2 * p]), 0);
+    const uint32_t acce_even = smem_cluster_addr(smem_u32(&bar_acce[2 * p]), even);
     uint8_t* stg = s_out + ew * G_STG_WARP;
     int buf = 0, slot = 0;
     uint32_t bphase = 0, sphase = 0;
@@ -420,6 +442,8 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
           }
         }
       }
+      // every part's MMAs are done with the ring before it takes the sums of a shared unit
+      if (a.split > 1) asm volatile("bar.sync 1, 256;" ::: "memory");
       if (!ok) break;
       const WSeg s = s_seg[ew];
       const int64_t n0 = static_cast<int64_t>(s.wb) * G_CH + p * G_PART;
@@ -428,21 +452,7 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       if (n0 >= N || rows <= 0) continue;
       const int64_t row0 = static_cast<int64_t>(s.row0) + rbase;
       const bool vec = (N & 7) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0u;
-      // 8 channels (16 bytes) of the lane's row into the staging buffer
-      auto stage8 = [&](int c, const float (&f)[8]) {
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float lo = f[2 * k], hi = f[2 * k + 1];
-          if (a.bias != nullptr) {
-            const int64_t n = n0 + 8 * c + 2 * k;
-            lo += n < N ? bf16_bits_to_f32(a.bias[n]) : 0.0f;
-            hi += n + 1 < N ? bf16_bits_to_f32(a.bias[n + 1]) : 0.0f;
-          }
-          o[k] = f32x2_to_bf16x2_bits(lo, hi);
-        }
-        *reinterpret_cast<uint4*>(stg + stg_at(lane, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
-      };
+      auto stage8 = [&](int c, const float (&f)[8]) { stage_chunk(stg, c, lane, f, a.bias, n0, N); };
       if (s.kb0 == 0 && s.kb1 == KB) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -462,6 +472,10 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             store_wide(stg, a.y, row0, rows, N, n0 + half * 64, vec, lane);
           }
         }
+      } else if (a.split > 1) {  // a part of K of the cluster's unit
+        float* d = s_part + ew * G_PART * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < G_PART; ++i) d[i * 32] = acc[i];
       } else {
         // a piece of a cut unit (as in fp8_gemm.cu): [channel][token] partial sums
         const int64_t u0 = static_cast<int64_t>(s.unit) * KB;
@@ -485,19 +499,62 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
           for (int half = 0; half < 2; ++half) {
             if (n0 + half * 64 >= N) break;
             stg_free();
-            for (int c = 0; c < 8; ++c) {
-              float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-              for (int r = first; r <= last; ++r) {
-                const float* src = piece(r) + (half * 8 + c) * 8 * 32;
+            for (int c = 0; c < 8; c += 2) {
+              float f[2][8] = {};
+              for (int r = first; r <= last; r += 4) {  // four pieces' loads in flight, added in order
+                float v[4][16];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) f[k] += __ldcg(src + k * 32);
+                for (int j = 0; j < 4; ++j) {
+                  const float* src = piece(min(r + j, last)) + (half * 8 + c) * 8 * 32;
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) v[j][k] = __ldcg(src + k * 32);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (r + j <= last) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) f[k >> 3][k & 7] += v[j][k];
+                  }
               }
-              stage8(half * 8 + c, f);
+              stage8(half * 8 + c, f[0]);
+              stage8(half * 8 + c + 1, f[1]);
             }
             __syncwarp();
             store_wide(stg, a.y, row0, rows, N, n0 + half * 64, vec, lane);
           }
         }
+      }
+    }
+  }
+
+  if (a.split > 1) {
+    // the parts' sums meet: every CTA adds its share of the channels over its peers' shared memory, in the order of K
+    __syncwarp();
+    cluster_sync_all();
+    Walk w = walk0;
+    WSeg s;
+    if (warp >= G_EPI0 && uni(next_wide(w, E, WB, s_prefix, s_off, s))) {
+      const int ew = warp - G_EPI0;
+      const int64_t n0 = static_cast<int64_t>(s.wb) * G_CH + (ew >> 2) * G_PART;
+      const int rbase = static_cast<int>(rank) * G_HALF + 32 * (warp & 3);
+      const int rows = min(32, s.tvalid - rbase);
+      if (n0 < N && rows > 0) {
+        const bool vec = (N & 7) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0u;
+        const int share = G_PART / 8 / a.split, lo = share * static_cast<int>(crank >> 1);  // 8-channel chunks
+        const uint32_t src = smem_u32(s_part + ew * G_PART * 32 + lane);
+        uint8_t* stg = s_out + ew * G_STG_WARP;
+        for (int c = lo; c < lo + share; ++c) {
+          float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+          for (int j = 0; j < a.split; ++j) {
+            const uint32_t p = smem_cluster_addr(src, 2 * j + rank) + c * 8 * 128;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] += ld_cluster(p + k * 128);
+          }
+          stage_chunk(stg, c, lane, f, a.bias, n0, N);
+        }
+        __syncwarp();
+        store_wide(stg, a.y, static_cast<int64_t>(s.row0) + rbase, rows, N, n0 + (lo >> 3) * 64, vec, lane, lo & 7,
+                   (lo & 7) + share);
       }
     }
   }
@@ -525,7 +582,7 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
 
 }  // namespace
 
-cudaError_t launch_fp8_wide(const Fp8GemmArgs& g, const fp8::KArgs& a, int64_t pairs, cudaStream_t stream) {
+cudaError_t launch_fp8_wide(const Fp8GemmArgs& g, const fp8::KArgs& a, int pairs, cudaStream_t stream) {
   CUtensorMap mx, mw, my;
   const auto type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
@@ -536,11 +593,7 @@ cudaError_t launch_fp8_wide(const Fp8GemmArgs& g, const fp8::KArgs& a, int64_t p
   const int y_tma = g.N % 8 == 0 && (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0u ? 1 : 0;
   if (!y_tma) my = mx;
   else if (!encode_map_2d(&my, g.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.R, g.N, 64, 32, sw)) return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(fp8_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(kWideSmem));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(fp8_wide_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(G_THREADS), kWideSmem, stream, mx,
-                    mw, my, y_tma, a);
+  return launch_pairs(fp8_wide_kernel, pairs, a.split, G_THREADS, kWideSmem, stream, mx, mw, my, y_tma, a);
 }
 
 }  // namespace w8a8
