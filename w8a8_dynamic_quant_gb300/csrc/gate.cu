@@ -59,6 +59,12 @@ __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
   e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
 }
 
+// A group's score from its two largest keys (a masked second counts 0), order-preserving.
+__device__ __forceinline__ uint32_t group_key(uint32_t k1, uint32_t k2, bool top2) {
+  if (!top2 || k1 <= kOrderedNegInf) return k1;
+  return ordered(__fadd_rn(unordered(k1), k2 > kOrderedNegInf ? unordered(k2) : 0.0f));
+}
+
 struct GateArgs {
   const void* logits;
   const float* bias;
@@ -137,52 +143,78 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
     if (lane * P + i >= E) key[i] = 0u;
 
   if (a.topk_group < a.n_group) {
-    // group scores: lane g scans group g's keys (n_group <= 32)
-    uint32_t* sk = s_gkey[warp];
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (lane * P + i < E) sk[lane * P + i] = key[i];
-    __syncwarp();
     const int gs = E / a.n_group;
-    uint32_t gk = 0u;
-    if (lane < a.n_group) {
-      uint32_t k1 = 0u, k2 = 0u;
-      for (int j = 0; j < gs; ++j) {
-        const uint32_t v = sk[lane * gs + j];
-        k2 = max(k2, min(k1, v));
-        k1 = max(k1, v);
-      }
-      gk = k1;
-      if (a.top2 && k1 > kOrderedNegInf)
-        gk = ordered(__fadd_rn(unordered(k1), k2 > kOrderedNegInf ? unordered(k2) : 0.0f));
-    }
-    uint32_t keep = 0u;
-    for (int j = 0; j < a.topk_group; ++j) {
-      const uint32_t best = __reduce_max_sync(0xffffffffu, gk);
-      const unsigned who = __ballot_sync(0xffffffffu, gk == best);
-      const int g = __ffs(who) - 1;
-      keep |= 1u << g;
-      if (lane == g) gk = 0u;
-    }
+    // group scores: every lane of group g's lanes holds its key, and then whether the group stays: fewer than
+    // topk_group groups rank above it
+    const int lanes = gs / P;
+    if (lanes * P == gs && (lanes & (lanes - 1)) == 0) {  // a group is a power of two of whole lanes
+      uint32_t k1 = key[0], k2 = 0u;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int e = lane * P + i;
-      if (e < E && !((keep >> (e / gs)) & 1u)) key[i] = 0u;
+      for (int i = 1; i < P; ++i) {
+        k2 = max(k2, min(k1, key[i]));
+        k1 = max(k1, key[i]);
+      }
+      for (int o = 1; o < lanes; o <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(0xffffffffu, k1, o), o2 = __shfl_xor_sync(0xffffffffu, k2, o);
+        k2 = max(max(k2, o2), min(k1, o1));
+        k1 = max(k1, o1);
+      }
+      const uint32_t gk = group_key(k1, k2, a.top2);
+      const int mine = lane / lanes;
+      int above = 0;
+      for (int g = 0; g < a.n_group; ++g) {
+        const uint32_t other = __shfl_sync(0xffffffffu, gk, g * lanes);
+        above += other > gk || (other == gk && g < mine) ? 1 : 0;
+      }
+      if (above >= a.topk_group) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) key[i] = 0u;
+      }
+    } else {  // through shared memory: lane g scans group g's keys (n_group <= 32)
+      uint32_t* sk = s_gkey[warp];
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (lane * P + i < E) sk[lane * P + i] = key[i];
+      __syncwarp();
+      uint32_t gk = 0u;
+      if (lane < a.n_group) {
+        uint32_t k1 = 0u, k2 = 0u;
+        for (int j = 0; j < gs; ++j) {
+          const uint32_t v = sk[lane * gs + j];
+          k2 = max(k2, min(k1, v));
+          k1 = max(k1, v);
+        }
+        gk = group_key(k1, k2, a.top2);
+      }
+      int above = 0;
+      for (int g = 0; g < a.n_group; ++g) {
+        const uint32_t other = __shfl_sync(0xffffffffu, gk, g);
+        above += other > gk || (other == gk && g < lane) ? 1 : 0;
+      }
+      const uint32_t keep = __ballot_sync(0xffffffffu, lane < a.n_group && above < a.topk_group);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const int e = lane * P + i;
+        if (e < E && !((keep >> (e / gs)) & 1u)) key[i] = 0u;
+      }
     }
   }
 
   // the k largest keys; lane j keeps choice j
   uint32_t best = 0u;
   int at = 0;
-  auto local_best = [&]() {
-    best = key[0];
-    at = 0;
+  auto local_best = [&]() {  // a tree for the key, then its first place
+    uint32_t t[P];
 #pragma unroll
-    for (int i = 1; i < P; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-      }
+    for (int i = 0; i < P; ++i) t[i] = key[i];
+#pragma unroll
+    for (int n = P / 2; n > 0; n /= 2)
+#pragma unroll
+      for (int i = 0; i < n; ++i) t[i] = max(t[i], t[i + n]);
+    best = t[0];
+    at = P - 1;
+#pragma unroll
+    for (int i = P - 2; i >= 0; --i) at = key[i] == best ? i : at;
   };
   local_best();
   int my_id = 0;
