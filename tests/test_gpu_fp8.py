@@ -327,3 +327,44 @@ def test_refusals():
     with pytest.raises(ValueError):
         W.w8a8_fp8_swiglu_quant(torch.zeros(2, 33, dtype=torch.bfloat16, device="cuda"))
     assert _capi.STATUS[3] == "W8A8_ERR_ALIGN"
+
+
+def test_quant_offsets_past_32_bits():
+    M, K = 300_000, 8192  # 2.4 G values
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn(3, K, generator=gen(2), device="cuda").to(torch.bfloat16)
+    q, s = W.w8a8_fp8_quant(x)
+    rq, rs = quant_reference(x[-4:].float())
+    assert torch.equal(s[-4:], rs) and same_codes(q[-4:], rq)
+    assert int(q[:-3].view(torch.uint8).amax()) == 0 and float(s[:-3].amax()) == 0.0
+
+
+def test_dense_offsets_past_32_bits():
+    M, N, K = 66_000, 65_792, 128  # 4.3 G outputs
+    q, xs, w, ws = problem(5, M, N, K)
+    y = W.w8a8_fp8_matmul(q, xs, w, ws)
+    rows = torch.tensor([0, 255, 256, 32_767, 65_279, 65_999], device="cuda")
+    ref = (q[rows].double() * spread(xs[rows], K)) @ (w.double() * spread_w(ws, N, K)).t()
+    err = (y[rows].double() - ref).abs()
+    assert bool((err <= bound(q[rows], xs[rows], w, ws, K, ref)).all())
+
+
+@pytest.mark.parametrize("M,N,K", [(48, 1100, 4096), (300, 1100, 4096), (700, 2000, 1536)])
+def test_matmul_in_a_graph(M, N, K):
+    """Captured and replayed on changed inputs: nothing of a call is left on the host, the workspace stays ready."""
+    q, xs, w, ws = problem(8, M, N, K)
+    work = W.workspace(W.fp8_matmul_workspace_bytes(M, N, K))
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    W.w8a8_fp8_matmul(q, xs, w, ws, ws=work, y=y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            W.w8a8_fp8_matmul(q, xs, w, ws, ws=work, y=y)
+    q2, xs2, _, _ = problem(9, M, N, K)
+    q.copy_(q2)
+    xs.copy_(xs2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y.view(torch.int16), W.w8a8_fp8_matmul(q, xs, w, ws).view(torch.int16))
+    assert W.read_device_status(work) == 0

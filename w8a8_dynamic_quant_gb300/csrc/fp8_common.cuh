@@ -2,6 +2,8 @@
 // the MMA issue.  The kernels are in fp8_gemm.cu (weights as the MMA's M side) and fp8_wide.cu (tokens as M side).
 #pragma once
 
+#include <atomic>
+
 #include "kernels.cuh"
 #include "tc_common.cuh"
 
@@ -282,13 +284,24 @@ cudaError_t launch_fp8_wide(const Fp8GemmArgs& g, const fp8::KArgs& a, int pairs
 
 namespace fp8 {
 
+// The kernel's attributes on the current device, set once (`done`: one bit a device): a call costs as much as a
+// tensor map.
+inline cudaError_t allow_smem(const void* k, size_t smem, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit) != 0u) return cudaSuccess;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 // Launch of `pairs` CTA pairs in clusters of `split` pairs, with programmatic stream serialization.
 template <typename... KArgsT, typename... Args>
 inline cudaError_t launch_pairs(void (*k)(KArgsT...), int pairs, int split, int threads, size_t smem, cudaStream_t stream,
                                 Args... args) {
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e == cudaSuccess && 2 * split > 8) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));

@@ -572,9 +572,13 @@ cudaError_t launch_nt(const Fp8GemmArgs& g, const KArgs& a, int pairs, cudaStrea
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   // token boxes of a whole tile's half and of 8 rows (for the tiles that hold fewer)
   if (!encode_map_2d(&mw, g.w, type, 1, g.E * g.N, g.K, F_BK, F_HALF, sw) ||
-      !encode_map_2d(&mb, g.q, type, 1, g.R, g.K, F_BK, C::kBig, sw) ||
       !encode_map_2d(&ms, g.q, type, 1, g.R, g.K, F_BK, 8, sw))
     return cudaErrorInvalidValue;
+  if (g.group_list == nullptr && g.R <= NT - 16) mb = ms;  // no tile is full: the large box is not used
+  else if (!encode_map_2d(&mb, g.q, type, 1, g.R, g.K, F_BK, C::kBig, sw)) return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fp8_gemm_kernel<NT>), C::kSmem, ready);
+  if (e != cudaSuccess) return e;
   return launch_pairs(fp8_gemm_kernel<NT>, pairs, a.split, F_THREADS, C::kSmem, stream, mw, mb, ms, a);
 }
 

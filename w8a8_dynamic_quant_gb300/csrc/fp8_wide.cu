@@ -596,6 +596,9 @@ cudaError_t launch_fp8_wide(const Fp8GemmArgs& g, const fp8::KArgs& a, int pairs
   const int y_tma = g.N % 8 == 0 && (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0u ? 1 : 0;
   if (!y_tma) my = mx;
   else if (!encode_map_2d(&my, g.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.R, g.N, 64, 32, sw)) return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fp8_wide_kernel), kWideSmem, ready);
+  if (e != cudaSuccess) return e;
   return launch_pairs(fp8_wide_kernel, pairs, a.split, G_THREADS, kWideSmem, stream, mx, mw, my, y_tma, a);
 }
 
