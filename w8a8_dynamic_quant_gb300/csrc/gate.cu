@@ -23,8 +23,9 @@
 //
 // One warp per token; lane l holds the experts [l * P, l * P + P), P = the
 // experts per lane.  A choice is the warp's maximum of the lanes' best keys
-// (as order-preserving integers), the lowest lane holding it, and a new best of
-// that lane.  Traffic is one read of the logits and 12 bytes per choice.
+// (as order-preserving integers) at the lowest lane holding it.  Traffic is one
+// read of the logits and 12 bytes per choice; what bounds large batches is the
+// issue of some hundred instructions a token, small ones the chain of k choices.
 #include "kernels.cuh"
 
 namespace w8a8 {
@@ -37,7 +38,7 @@ constexpr float kNegInf = -INFINITY;
 // Order-preserving map of binary32 (no NaN) to unsigned: larger values get larger integers; 0 is below all.
 __device__ __forceinline__ uint32_t ordered(float f) {
   const uint32_t u = __float_as_uint(f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
@@ -48,6 +49,35 @@ template <bool BF16>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
   if constexpr (BF16) return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
   else return static_cast<const float*>(p)[i];
+}
+
+// P consecutive values of a row from i0, by 16-byte loads (the caller checks the alignment).
+template <int P, bool BF16>
+__device__ __forceinline__ void load_row(const void* p, int64_t i0, float (&l)[P]) {
+  if constexpr (BF16 && P % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < P; i += 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i0 + i);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        l[i + 2 * j] = __uint_as_float(w[j] << 16);
+        l[i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    }
+  } else if constexpr (!BF16 && P % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < P; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i0 + i);
+      l[i] = v.x;
+      l[i + 1] = v.y;
+      l[i + 2] = v.z;
+      l[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) l[i] = load_logit<BF16>(p, i0 + i);
+  }
 }
 
 __device__ __forceinline__ float sigmoid_rn(float x) { return __frcp_rn(__fadd_rn(1.0f, expf(-x))); }
@@ -66,6 +96,7 @@ __device__ __forceinline__ uint32_t group_key(uint32_t k1, uint32_t k2, bool top
 }
 
 struct GateArgs {
+  int full;  // E = 32 P, and logits and bias allow 16-byte loads
   const void* logits;
   const float* bias;
   int64_t T;
@@ -87,21 +118,28 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
   if (t >= a.T) return;
   const int E = a.E;
   const int64_t row = t * E;
-  float l[P];
+  float l[P], bias[P];
+  if (a.full) {
+    load_row<P, BF16>(a.logits, row + lane * P, l);
+    if (a.bias != nullptr) load_row<P, false>(a.bias, lane * P, bias);
+  } else {
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int e = lane * P + i;
-    l[i] = e < E ? load_logit<BF16>(a.logits, row + e) : kNegInf;
-    if (!(l[i] > kNegInf)) l[i] = kNegInf;  // NaN
+    for (int i = 0; i < P; ++i) {
+      const int e = lane * P + i;
+      l[i] = e < E ? load_logit<BF16>(a.logits, row + e) : kNegInf;
+      if (a.bias != nullptr) bias[i] = e < E ? a.bias[e] : 0.0f;
+    }
   }
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (!(l[i] > kNegInf)) l[i] = kNegInf;  // NaN
   float m = kNegInf, S = 0.0f;
   uint32_t key[P];
   if constexpr (SIGMOID) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int e = lane * P + i;
       float s = sigmoid_rn(l[i]);
-      if (a.bias != nullptr && e < E) s = __fadd_rn(s, a.bias[e]);
+      if (a.bias != nullptr) s = __fadd_rn(s, bias[i]);
       key[i] = (l[i] > kNegInf && s > kNegInf) ? ordered(s) : kOrderedNegInf;
     }
   } else {
@@ -132,15 +170,16 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int e = lane * P + i;
       float s = ex[i];
-      if (a.bias != nullptr && e < E) s = __fadd_rn(__fdiv_rn(s, S), a.bias[e]);
+      if (a.bias != nullptr) s = __fadd_rn(__fdiv_rn(s, S), bias[i]);
       key[i] = (l[i] > kNegInf && s > kNegInf) ? ordered(s) : kOrderedNegInf;
     }
   }
+  if (!a.full) {
 #pragma unroll
-  for (int i = 0; i < P; ++i)
-    if (lane * P + i >= E) key[i] = 0u;
+    for (int i = 0; i < P; ++i)
+      if (lane * P + i >= E) key[i] = 0u;
+  }
 
   if (a.topk_group < a.n_group) {
     const int gs = E / a.n_group;
@@ -200,38 +239,41 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
     }
   }
 
-  // the k largest keys; lane j keeps choice j
-  uint32_t best = 0u;
-  int at = 0;
-  auto local_best = [&]() {  // a tree for the key, then its first place
-    uint32_t t[P];
+  // The k largest keys; lane j keeps choice j.  A lane knows its two best (keys and places); the warp's maximum of
+  // the best, at its lowest lane, is the next choice, and that lane moves its second up.  Only a lane that gave both
+  // looks through its keys again.
+  uint32_t b1, b2, taken = 0u;
+  int a1, a2;
+  auto two_best = [&]() {
+    b1 = b2 = 0u;
+    a1 = a2 = 0;
 #pragma unroll
-    for (int i = 0; i < P; ++i) t[i] = key[i];
-#pragma unroll
-    for (int n = P / 2; n > 0; n /= 2)
-#pragma unroll
-      for (int i = 0; i < n; ++i) t[i] = max(t[i], t[i + n]);
-    best = t[0];
-    at = P - 1;
-#pragma unroll
-    for (int i = P - 2; i >= 0; --i) at = key[i] == best ? i : at;
+    for (int i = 0; i < P; ++i) {
+      const uint32_t v = (taken >> i) & 1u ? 0u : key[i];
+      const bool first = v > b1, second = v > b2;  // places in rising order: ties stay with the lower
+      b2 = first ? b1 : second ? v : b2;
+      a2 = first ? a1 : second ? i : a2;
+      b1 = first ? v : b1;
+      a1 = first ? i : a1;
+    }
   };
-  local_best();
+  two_best();
   int my_id = 0;
   uint32_t my_key = 0u;
   for (int j = 0; j < a.k; ++j) {
-    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    const int w = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-    const int id = __shfl_sync(0xffffffffu, lane * P + at, w);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, b1);
+    const int w = __ffs(__ballot_sync(0xffffffffu, b1 == top)) - 1;
+    const int id = __shfl_sync(0xffffffffu, lane * P + a1, w);
     if (lane == j) {
       my_id = id;
       my_key = top;
     }
     if (lane == w) {
-#pragma unroll
-      for (int i = 0; i < P; ++i)
-        if (i == at) key[i] = 0u;
-      local_best();
+      taken |= 1u << a1;
+      b1 = b2;
+      a1 = a2;
+      b2 = 0u;
+      if (b1 == 0u) two_best();
     }
   }
   float wgt = 0.0f;
@@ -255,8 +297,10 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
 }
 
 template <int P>
-cudaError_t launch_p(const GateArgs& a, bool bf16, bool sigmoid, cudaStream_t stream) {
+cudaError_t launch_p(GateArgs a, bool bf16, bool sigmoid, cudaStream_t stream) {
   const dim3 g(static_cast<unsigned>((a.T + kGateWarps - 1) / kGateWarps)), b(32 * kGateWarps);
+  const auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0u; };
+  a.full = a.E == 32 * P && aligned(a.logits) && aligned(a.bias) ? 1 : 0;
   if (bf16) {
     return sigmoid ? launch_pdl(gate_kernel<P, true, true>, g, b, 0, stream, a)
                    : launch_pdl(gate_kernel<P, true, false>, g, b, 0, stream, a);
@@ -271,12 +315,19 @@ cudaError_t launch_gate(const void* logits, bool bf16, int64_t T, int E, const f
                         int topk_group, bool top2, int k, bool renorm, float scale, int64_t* ids, float* weights,
                         cudaStream_t stream) {
   if (T == 0) return cudaSuccess;
-  const GateArgs a{logits, bias, T, E, k, n_group, topk_group, top2, renorm, scale, ids, weights};
-  if (E <= 32) return launch_p<1>(a, bf16, sigmoid, stream);
-  if (E <= 64) return launch_p<2>(a, bf16, sigmoid, stream);
-  if (E <= 128) return launch_p<4>(a, bf16, sigmoid, stream);
-  if (E <= 256) return launch_p<8>(a, bf16, sigmoid, stream);
-  if (E <= 512) return launch_p<16>(a, bf16, sigmoid, stream);
+  const GateArgs a{0, logits, bias, T, E, k, n_group, topk_group, top2, renorm, scale, ids, weights};
+  // experts per lane: as few as hold E, so that common counts (96, 160, 192, 384 and the powers of two) fill every lane
+  // and their groups are whole lanes
+  const int P = (E + 31) / 32;
+  if (P <= 1) return launch_p<1>(a, bf16, sigmoid, stream);
+  if (P <= 2) return launch_p<2>(a, bf16, sigmoid, stream);
+  if (P <= 3) return launch_p<3>(a, bf16, sigmoid, stream);
+  if (P <= 4) return launch_p<4>(a, bf16, sigmoid, stream);
+  if (P <= 5) return launch_p<5>(a, bf16, sigmoid, stream);
+  if (P <= 6) return launch_p<6>(a, bf16, sigmoid, stream);
+  if (P <= 8) return launch_p<8>(a, bf16, sigmoid, stream);
+  if (P <= 12) return launch_p<12>(a, bf16, sigmoid, stream);
+  if (P <= 16) return launch_p<16>(a, bf16, sigmoid, stream);
   return launch_p<32>(a, bf16, sigmoid, stream);
 }
 
