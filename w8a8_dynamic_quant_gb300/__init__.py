@@ -467,13 +467,17 @@ def moe_layer(x: torch.Tensor, x_scale: Optional[torch.Tensor], topk_ids: torch.
     return y
 
 
-# The calls below run a few microseconds of GPU work at decode sizes, so their host side is kept short: one pass of
-# plain attribute tests per tensor (the full _need only to say what is wrong), no device guard where the tensors'
+# The calls below run a few microseconds of GPU work at decode sizes, so their host side is kept short: plain attribute
+# tests of a tensor in one expression (the full _need only to say what is wrong), no device guard where the tensors'
 # device is already current, and the library's functions looked up once.  On the GPU host (aarch64) a quantisation
-# call takes 6 us this way, 16 us with a guard, _stream and _need for every tensor.
+# call takes about 9 us this way, 16 us with a guard, _stream and _need for every tensor; its two allocations
+# and the launch are 5 of them.
 
 _bound = {}
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_get_device = torch._C._cuda_getDevice
+_empty, _Tensor = torch.empty, torch.Tensor
+_BF16, _F32, _I64, _E4M3 = torch.bfloat16, torch.float32, torch.int64, torch.float8_e4m3fn
 
 
 def _call(name: str, index: int, *args):
@@ -481,7 +485,7 @@ def _call(name: str, index: int, *args):
     fn = _bound.get(name)
     if fn is None:
         fn = _bound[name] = getattr(_capi.lib(), name)
-    if torch.cuda.current_device() == index:
+    if _get_device() == index:
         code = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -542,11 +546,12 @@ def moe_gate_topk(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = N
     logit is -inf or NaN is chosen only when no other is left, with weight 0."""
     T, E = _dims(logits, "logits", 2)
     dtype, dev = logits.dtype, logits.get_device()
-    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+    if dtype is not _F32 and dtype is not _BF16:
         raise TypeError(f"logits must be torch.float32 or torch.bfloat16, got {dtype}")
-    _check(logits, "logits", dtype, (T, E), dev)
+    if not (dev >= 0 and logits.is_contiguous()):
+        _check(logits, "logits", dtype, (T, E), dev)
     if bias is not None:
-        _check(bias, "bias", torch.float32, (E,), dev)
+        _check(bias, "bias", _F32, (E,), dev)
     if scoring == "sigmoid":
         flags = _capi.GATE_SIGMOID
     elif scoring == "softmax":
@@ -564,11 +569,11 @@ def moe_gate_topk(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = N
     if dtype is torch.bfloat16:
         flags |= _capi.GATE_BF16
     if ids is None:
-        ids = torch.empty((T, max(k, 0)), dtype=torch.int64, device=logits.device)
+        ids = _empty((T, max(k, 0)), dtype=_I64, device=logits.device)
     else:
         _check(ids, "ids", torch.int64, (T, k), dev)
     if weights is None:
-        weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
+        weights = _empty((T, max(k, 0)), dtype=_F32, device=logits.device)
     else:
         _check(weights, "weights", torch.float32, (T, k), dev)
     _call("moe_gate_topk", dev, logits.data_ptr(), T, E, None if bias is None else bias.data_ptr(), n_group, topk_group,
@@ -576,26 +581,31 @@ def moe_gate_topk(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = N
     return ids, weights
 
 
-def _quant_out(q, scale, rows: int, K: int, device, dev: int):
-    kb = _blocks(K)
-    if q is None:
-        q = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=device)
-    else:
-        _check_e4m3(q, "q", (rows, K), dev)
-    if scale is None:
-        scale = torch.empty((rows, kb), dtype=torch.float32, device=device)
-    else:
-        _check(scale, "scale", torch.float32, (rows, kb), dev)
-    return q, scale
+def _quant_checks(x, name: str, columns: int, q, scale):
+    """The quantisers' tensors where one is not as the common call has it: [M, columns * K] bf16 and given outputs."""
+    M, width = _dims(x, name, 2)
+    dev = x.get_device()
+    _check(x, name, _BF16, (M, width), dev)
+    if width % columns:
+        raise ValueError(f"{name} must be [R,{columns}I]")
+    K = width // columns
+    if q is not None:
+        _check_e4m3(q, "q", (M, K), dev)
+    if scale is not None:
+        _check(scale, "scale", _F32, (M, _blocks(K)), dev)
 
 
 def w8a8_fp8_quant(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None):
     """BF16 x [M,K] (K % 16 == 0) -> (float8_e4m3fn q [M,K], float32 scale [M, ceil(K/128)])."""
-    M, K = _dims(x, "x", 2)
+    if not (q is None and scale is None and type(x) is _Tensor and x.dtype is _BF16 and x.dim() == 2 and x.is_cuda
+            and x.is_contiguous()):
+        _quant_checks(x, "x", 1, q, scale)
+    M, K = x.shape
     dev = x.get_device()
-    if not (x.dtype is torch.bfloat16 and dev >= 0 and x.is_contiguous()):
-        _check(x, "x", torch.bfloat16, (M, K), dev)
-    q, scale = _quant_out(q, scale, M, K, x.device, dev)
+    if q is None:
+        q = _empty((M, K), dtype=_E4M3, device=x.device)
+    if scale is None:
+        scale = _empty((M, (K + 127) // 128), dtype=_F32, device=x.device)
     _call("w8a8_fp8_quant", dev, x.data_ptr(), M, K, q.data_ptr(), scale.data_ptr())
     return q, scale
 
@@ -604,13 +614,16 @@ def w8a8_fp8_swiglu_quant(y13: torch.Tensor, q: Optional[torch.Tensor] = None,
                           scale: Optional[torch.Tensor] = None):
     """BF16 y13 [R,2I] (gate half, up half) -> SwiGLU, quantised: (float8_e4m3fn q [R,I], float32 scale
     [R, ceil(I/128)])."""
-    R, two = _dims(y13, "y13", 2)
-    if two % 2:
-        raise ValueError("y13 must be [R,2I]")
-    dev = y13.get_device()
-    _check(y13, "y13", torch.bfloat16, (R, two), dev)
-    q, scale = _quant_out(q, scale, R, two // 2, y13.device, dev)
-    _call("w8a8_fp8_swiglu_quant", dev, y13.data_ptr(), R, two // 2, q.data_ptr(), scale.data_ptr())
+    if not (q is None and scale is None and type(y13) is _Tensor and y13.dtype is _BF16 and y13.dim() == 2
+            and y13.is_cuda and y13.is_contiguous() and y13.shape[1] % 2 == 0):
+        _quant_checks(y13, "y13", 2, q, scale)
+    R, two = y13.shape
+    I, dev = two // 2, y13.get_device()
+    if q is None:
+        q = _empty((R, I), dtype=_E4M3, device=y13.device)
+    if scale is None:
+        scale = _empty((R, (I + 127) // 128), dtype=_F32, device=y13.device)
+    _call("w8a8_fp8_swiglu_quant", dev, y13.data_ptr(), R, I, q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -626,17 +639,22 @@ def w8a8_fp8_matmul(q: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_s
     M, K = _dims(q, "q", 2)
     N = _dims(w, "w", 2)[0]
     dev, kb = q.get_device(), (K + 127) // 128
-    _check_e4m3(q, "q", (M, K), dev)
-    _check_e4m3(w, "w", (N, K), dev)
-    _check(x_scale, "x_scale", torch.float32, (M, kb), dev)
-    _check(w_scale, "w_scale", torch.float32, ((N + 127) // 128, kb), dev)
+    if not (dev >= 0 and q.dtype is _E4M3 and w.dtype is _E4M3 and type(x_scale) is _Tensor and type(w_scale) is _Tensor
+            and x_scale.dtype is _F32 and w_scale.dtype is _F32 and w.get_device() == dev
+            and x_scale.get_device() == dev and w_scale.get_device() == dev and w.shape[1] == K
+            and x_scale.shape == (M, kb) and w_scale.shape == ((N + 127) // 128, kb) and q.is_contiguous()
+            and w.is_contiguous() and x_scale.is_contiguous() and w_scale.is_contiguous()):
+        _check_e4m3(q, "q", (M, K), dev)
+        _check_e4m3(w, "w", (N, K), dev)
+        _check(x_scale, "x_scale", _F32, (M, kb), dev)
+        _check(w_scale, "w_scale", _F32, (_blocks(N), kb), dev)
     if bias is not None:
         _check(bias, "bias", torch.bfloat16, (N,), dev)
     ws = _check_ws(ws, lambda: fp8_matmul_workspace_bytes(M, N, K), dev)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=q.device)
+        y = _empty((M, N), dtype=_BF16, device=q.device)
     else:
-        _check(y, "y", torch.bfloat16, (M, N), dev)
+        _check(y, "y", _BF16, (M, N), dev)
     _call("w8a8_fp8_matmul", dev, q.data_ptr(), x_scale.data_ptr(), M, K, w.data_ptr(), w_scale.data_ptr(), N,
           None if bias is None else bias.data_ptr(), y.data_ptr(), ws.data_ptr(), ws.numel())
     return y
@@ -652,18 +670,25 @@ def w8a8_fp8_grouped_matmul(q: torch.Tensor, x_scale: torch.Tensor, group_list: 
     """E4M3 q [R,K] (rows grouped by expert) with x_scale [R, ceil(K/128)] x E4M3 w [E,N,K] with w_scale
     [E, ceil(N/128), ceil(K/128)] -> bf16 y [R,N]."""
     R, K = _dims(q, "q", 2)
-    E, N, _ = _dims(w, "w", 3)
-    dev, kb = q.get_device(), _blocks(K)
-    _check_e4m3(q, "q", (R, K), dev)
-    _check_e4m3(w, "w", (E, N, K), dev)
-    _check(group_list, "group_list", torch.int64, (E,), dev)
-    _check(x_scale, "x_scale", torch.float32, (R, kb), dev)
-    _check(w_scale, "w_scale", torch.float32, (E, _blocks(N), kb), dev)
+    E, N, K2 = _dims(w, "w", 3)
+    dev, kb = q.get_device(), (K + 127) // 128
+    if not (dev >= 0 and q.dtype is _E4M3 and w.dtype is _E4M3 and type(x_scale) is _Tensor and type(w_scale) is _Tensor
+            and type(group_list) is _Tensor and x_scale.dtype is _F32 and w_scale.dtype is _F32
+            and group_list.dtype is _I64 and w.get_device() == dev and x_scale.get_device() == dev
+            and w_scale.get_device() == dev and group_list.get_device() == dev and K2 == K
+            and x_scale.shape == (R, kb) and w_scale.shape == (E, (N + 127) // 128, kb) and group_list.shape == (E,)
+            and q.is_contiguous() and w.is_contiguous() and x_scale.is_contiguous() and w_scale.is_contiguous()
+            and group_list.is_contiguous()):
+        _check_e4m3(q, "q", (R, K), dev)
+        _check_e4m3(w, "w", (E, N, K), dev)
+        _check(group_list, "group_list", _I64, (E,), dev)
+        _check(x_scale, "x_scale", _F32, (R, kb), dev)
+        _check(w_scale, "w_scale", _F32, (E, _blocks(N), kb), dev)
     ws = _check_ws(ws, lambda: fp8_grouped_matmul_workspace_bytes(E, R, N, K), dev)
     if y is None:
-        y = torch.empty((R, N), dtype=torch.bfloat16, device=q.device)
+        y = _empty((R, N), dtype=_BF16, device=q.device)
     else:
-        _check(y, "y", torch.bfloat16, (R, N), dev)
+        _check(y, "y", _BF16, (R, N), dev)
     _call("w8a8_fp8_grouped_matmul", dev, q.data_ptr(), x_scale.data_ptr(), group_list.data_ptr(), E, R, K,
           w.data_ptr(), w_scale.data_ptr(), N, y.data_ptr(), ws.data_ptr(), ws.numel())
     return y
