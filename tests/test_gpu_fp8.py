@@ -165,7 +165,8 @@ def test_dense(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(64, 2048, 7168), (1, 4096, 7168), (8, 129, 16384), (300, 520, 4096),
-                                   (2100, 1111, 1040), (4096, 2048, 512), (1024, 1024, 65536)])
+                                   (2100, 1111, 1040), (400, 1002, 528), (4096, 2048, 512),
+                                   (1024, 1024, 65536)])
 def test_dense_large(M, N, K):
     check_dense(M, N, K, bias=True)
 

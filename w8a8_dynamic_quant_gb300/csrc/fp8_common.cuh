@@ -150,6 +150,21 @@ __device__ __forceinline__ void tmem_ready(uint32_t (&v)[C]) {
   for (int i = 0; i < C; ++i) asm volatile("" : "+r"(v[i]));  // no use of a value moves before the wait
 }
 
+// Arrival of lane 0 on a cluster-window mbarrier, without a branch.
+__device__ __forceinline__ void arrive_lane0(uint32_t bar, int lane) {
+  asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cluster.b64 _, [%0];\n}\n" ::"r"(bar), "r"(lane)
+               : "memory");
+}
+__device__ __forceinline__ void arrive_lane0_cta(uint32_t bar, int lane) {
+  asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar), "r"(lane)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint32_t a, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(a), "r"(parity) : "memory");
+  return ok != 0u;
+}
+
 // The sequence of segments of one pair.  Every role walks it on its own.
 struct Walk {
   int64_t x, end;  // cut: block position; else: unit number

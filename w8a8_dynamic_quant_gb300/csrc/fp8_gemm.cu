@@ -65,30 +65,36 @@ struct Cfg {
   static constexpr size_t kPiece = static_cast<size_t>(F_EPI_WARPS) * kCols * 32;  // floats of one CTA's partial sums
 };
 
-// acc[c] += accumulator column c * sc[c], c < cols (rounded up to 16).  The warp's columns come in one load, and once
-// it is complete the accumulator is released (arrival on `release`), before the sums.
+// acc[c] += accumulator column c * sc[c], c < cols (rounded up to 16), two columns an instruction.  The warp's columns
+// come in one load; once it is complete the accumulator is released (arrival on `release`) and the next one's barrier
+// probed, before the sums.
 template <int COLS>
-__device__ __forceinline__ void drain(uint32_t taddr, const float* sc, int cols, uint32_t release, int lane,
-                                      float (&acc)[COLS]) {
+__device__ __forceinline__ bool drain(uint32_t taddr, const float* sc, int cols, uint32_t release, int lane,
+                                      uint32_t next_bar, uint32_t next_parity, float (&acc)[COLS]) {
   uint32_t v[COLS];
   tmem_fetch(taddr, v);
   tmem_ready(v);
   tc_fence_before();
-  __syncwarp();
-  if (lane == 0) mbar_arrive_cluster(release);
+  arrive_lane0(release, lane);
+  const bool next = mbar_test(next_bar, next_parity);
 #pragma unroll
   for (int j = 0; j < COLS; j += 16) {
     if (j < cols) {
 #pragma unroll
       for (int i = j; i < j + 16; i += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(sc + i);
-        acc[i] = fmaf(__uint_as_float(v[i]), f.x, acc[i]);
-        acc[i + 1] = fmaf(__uint_as_float(v[i + 1]), f.y, acc[i + 1]);
-        acc[i + 2] = fmaf(__uint_as_float(v[i + 2]), f.z, acc[i + 2]);
-        acc[i + 3] = fmaf(__uint_as_float(v[i + 3]), f.w, acc[i + 3]);
+        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(sc + i);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint64_t a, x;
+          asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(acc[i + 2 * h]), "f"(acc[i + 2 * h + 1]));
+          asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(v[i + 2 * h]), "r"(v[i + 2 * h + 1]));
+          asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(x), "l"(h == 0 ? f.x : f.y));
+          asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[i + 2 * h]), "=f"(acc[i + 2 * h + 1]) : "l"(a));
+        }
       }
     }
   }
+  return next;
 }
 
 // One run of blocks of a unit: the tile and its K range.
@@ -354,6 +360,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     uint16_t* stg = s_out + ew * 16 * 32;
     int buf = 0, slot = 0;
     uint32_t bphase = 0, sphase = 0;
+    bool probed = false;  // the next accumulator was seen complete
+    const uint32_t accf0 = smem_u32(&bar_accf[0]);
     Walk w = walk0;
     Seg s;
     bool ok = true;
@@ -369,18 +377,19 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       for (int kb = kb0; kb < kb1; ++kb) {
         if (kb == kb0 || (kb & (F_SG - 1)) == 0)
           ok = wait_all(smem_u32(&bar_scf[slot]), sphase, &s_abort, a.status, 6u);
-        ok = ok && wait_all(smem_u32(&bar_accf[buf]), bphase, &s_abort, a.status, 4u);
+        if (!probed) ok = ok && wait_all(accf0 + 8 * buf, bphase, &s_abort, a.status, 4u);
         if (!ok) break;
         tc_fence_after();
-        drain<C::kCols>(lane_addr + buf * NT + c0, s_scale + (slot * F_SG + (kb & (F_SG - 1))) * NT + c0, cols,
-                        acce_even + 8u * buf, lane, acc);
+        const uint32_t here = lane_addr + buf * NT + c0, release = acce_even + 8u * buf;
         if (++buf == C::kAcc) {
           buf = 0;
           bphase ^= 1u;
         }
+        probed = __all_sync(0xffffffffu, drain<C::kCols>(here, s_scale + (slot * F_SG + (kb & (F_SG - 1))) * NT + c0, cols,
+                                                         release, lane, accf0 + 8 * buf, bphase, acc));
         if ((kb & (F_SG - 1)) == F_SG - 1 || kb == kb1 - 1) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bar_sce[slot]));
+          arrive_lane0_cta(smem_u32(&bar_sce[0]) + 8 * slot, lane);
           if (++slot == F_SRING) {
             slot = 0;
             sphase ^= 1u;

@@ -87,21 +87,6 @@ __device__ __forceinline__ void fma_scaled(float* acc, const uint32_t* v, float 
   }
 }
 
-// Arrival of lane 0 on a cluster-window mbarrier, without a branch.
-__device__ __forceinline__ void arrive_lane0(uint32_t bar, int lane) {
-  asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cluster.b64 _, [%0];\n}\n" ::"r"(bar), "r"(lane)
-               : "memory");
-}
-__device__ __forceinline__ void arrive_lane0_cta(uint32_t bar, int lane) {
-  asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar), "r"(lane)
-               : "memory");
-}
-__device__ __forceinline__ bool mbar_test(uint32_t a, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(a), "r"(parity) : "memory");
-  return ok != 0u;
-}
-
 // acc += s * the warp's 128 accumulator columns, 32 at a time through two buffers: while one is added the other's load
 // runs.  The accumulator is released once its last load is complete, and the next one's barrier probed while the last
 // sums run.
@@ -147,22 +132,32 @@ __device__ __forceinline__ void stage_chunk(uint8_t* stg, int c, int lane, const
   *reinterpret_cast<uint4*>(stg + stg_at(lane, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// The staged rows to y rows row0 + r < row0 + rows, channels n0 .. (16-byte chunks [c_lo, c_hi) of them)
+// The staged rows to y rows row0 + r < row0 + rows, channels n0 .. (16-byte chunks [c_lo, c_hi) of them).  Rows of y
+// that do not start on 16-byte boundaries take a row an instruction in words of two channels, or of one where N is odd.
 __device__ __forceinline__ void store_wide(const uint8_t* stg, uint16_t* y, int64_t row0, int rows, int64_t N,
-                                           int64_t n0, bool vec, int lane, int c_lo = 0, int c_hi = 8) {
-  const int c = lane & 7;
-  if (c < c_lo || c >= c_hi) return;
+                                           int64_t n0, int lane, int c_lo = 0, int c_hi = 8) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(y);
+  if ((N & 7) == 0 && (at & 15u) == 0u) {
+    const int c = lane & 7;
+    if (c < c_lo || c >= c_hi || n0 + 8 * c >= N) return;
 #pragma unroll 1
-  for (int r = lane >> 3; r < rows; r += 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(stg + stg_at(r, c));
-    uint16_t* d = y + (row0 + r) * N + n0 + 8 * c;
-    if (vec && n0 + 8 * c + 8 <= N) {
-      *reinterpret_cast<uint4*>(d) = v;
-    } else {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int r = lane >> 3; r < rows; r += 4)
+      *reinterpret_cast<uint4*>(y + (row0 + r) * N + n0 + 8 * c) = *reinterpret_cast<const uint4*>(stg + stg_at(r, c));
+  } else if ((N & 1) == 0 && (at & 3u) == 0u) {
+    const int c = lane >> 2;
+    if (c < c_lo || c >= c_hi || n0 + 2 * lane >= N) return;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r)
+      *reinterpret_cast<uint32_t*>(y + (row0 + r) * N + n0 + 2 * lane) =
+          *reinterpret_cast<const uint32_t*>(stg + stg_at(r, c) + 4 * (lane & 3));
+  } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (n0 + 8 * c + k < N) d[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+    for (int k = 0; k < 64; k += 32) {
+      const int n = lane + k, c = n >> 3;
+      if (c < c_lo || c >= c_hi || n0 + n >= N) continue;
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r)
+        y[(row0 + r) * N + n0 + n] = *reinterpret_cast<const uint16_t*>(stg + stg_at(r, c) + 2 * (n & 7));
     }
   }
 }
@@ -463,7 +458,6 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       const int rows = min(32, s.tvalid - rbase);
       if (n0 >= N || rows <= 0) continue;
       const int64_t row0 = static_cast<int64_t>(s.row0) + rbase;
-      const bool vec = (N & 7) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0u;
       auto stage8 = [&](int c, const float (&f)[8]) { stage_chunk(stg, c, lane, f, a.bias, n0, N); };
       if (s.kb0 == 0 && s.kb1 == KB) {
 #pragma unroll
@@ -481,7 +475,7 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             tma_store_rows(&tmY, smem_u32(stg), static_cast<int>(n0) + half * 64, static_cast<int>(row0));
           } else {
             __syncwarp();
-            store_wide(stg, a.y, row0, rows, N, n0 + half * 64, vec, lane);
+            store_wide(stg, a.y, row0, rows, N, n0 + half * 64, lane);
           }
         }
       } else if (a.split > 1) {  // a part of K of the cluster's unit
@@ -532,7 +526,7 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
               stage8(half * 8 + c + 1, f[1]);
             }
             __syncwarp();
-            store_wide(stg, a.y, row0, rows, N, n0 + half * 64, vec, lane);
+            store_wide(stg, a.y, row0, rows, N, n0 + half * 64, lane);
           }
         }
       }
@@ -551,7 +545,6 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       const int rbase = static_cast<int>(rank) * G_HALF + 32 * (warp & 3);
       const int rows = min(32, s.tvalid - rbase);
       if (n0 < N && rows > 0) {
-        const bool vec = (N & 7) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0u;
         const int share = G_PART / 8 / a.split, lo = share * static_cast<int>(crank >> 1);  // 8-channel chunks
         const uint32_t src = smem_u32(s_part + ew * G_PART * 32 + lane);
         uint8_t* stg = s_out + ew * G_STG_WARP;
@@ -565,7 +558,7 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
           stage_chunk(stg, c, lane, f, a.bias, n0, N);
         }
         __syncwarp();
-        store_wide(stg, a.y, static_cast<int64_t>(s.row0) + rbase, rows, N, n0 + (lo >> 3) * 64, vec, lane, lo & 7,
+        store_wide(stg, a.y, static_cast<int64_t>(s.row0) + rbase, rows, N, n0 + (lo >> 3) * 64, lane, lo & 7,
                    (lo & 7) + share);
       }
     }
