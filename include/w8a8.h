@@ -388,6 +388,9 @@ W8A8_API w8a8_status moe_gate_topk(const void* logits, int64_t T, int64_t E, con
 /* output channels).  The last block of a row or of a weight's channels may  */
 /* be shorter: ceil(K/128) scales a row, ceil(N/128) x ceil(K/128) a weight. */
 /* Weights are used as they lie in a checkpoint; there is nothing to pack.   */
+/* One workspace may serve FP8 calls of different sizes in turn, but not the */
+/* other calls as well (they lay theirs out differently).  After a device    */
+/* timeout zero-fill it again.  w8a8_last_engine() is W8A8_ENGINE_TC.        */
 /* ------------------------------------------------------------------------ */
 
 /* x [M,K] bf16 -> q [M,K] E4M3 bytes, scale [M, ceil(K/128)] fp32: per block

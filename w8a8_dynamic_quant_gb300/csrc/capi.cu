@@ -787,11 +787,11 @@ static w8a8_status fp8_common(const Fp8GemmArgs& in, void* ws, size_t ws_bytes, 
   const size_t need = kStatusBytes + fp8_gemm_ws_bytes(a.E, a.R, a.N, a.K, a.group_list != nullptr);
   if (ws_bytes < need || !aligned16(ws)) return W8A8_ERR_WORKSPACE;
   int sms = 0;
-  if (w8a8_status s = device_info(sms)) return s;
+  if (w8a8_status s = device_info(sms)) return s;  // refuses a device of another kind
   a.status = static_cast<DeviceStatus*>(ws);
   t_last_engine = W8A8_ENGINE_TC;
   return cuda_status(
-      launch_fp8_gemm(a, static_cast<uint8_t*>(ws) + kStatusBytes, sms, reinterpret_cast<cudaStream_t>(stream)));
+      launch_fp8_gemm(a, static_cast<uint8_t*>(ws) + kStatusBytes, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 w8a8_status w8a8_fp8_matmul(const uint8_t* q, const float* x_scale, int64_t M, int64_t K, const uint8_t* w,
@@ -909,7 +909,7 @@ w8a8_status moe_fp8_layer(const uint16_t* x, const int64_t* topk_ids, const floa
   a.w_scale = w13_scale;
   a.y = y13;
   a.status = status;
-  if (w8a8_status e = cuda_status(launch_fp8_gemm(a, b + L.gemm, sms, st))) return e;
+  if (w8a8_status e = cuda_status(launch_fp8_gemm(a, b + L.gemm, st))) return e;
   if (w8a8_status e = cuda_status(launch_fp8_swiglu_quant(y13, R, I, b + L.hq, hs, st, sms))) return e;
   a.q = b + L.hq;
   a.x_scale = hs;
@@ -918,7 +918,7 @@ w8a8_status moe_fp8_layer(const uint16_t* x, const int64_t* topk_ids, const floa
   a.w = w2;
   a.w_scale = w2_scale;
   a.y = yr;
-  if (w8a8_status e = cuda_status(launch_fp8_gemm(a, b + L.gemm, sms, st))) return e;
+  if (w8a8_status e = cuda_status(launch_fp8_gemm(a, b + L.gemm, st))) return e;
   t_last_engine = W8A8_ENGINE_TC;
   return cuda_status(launch_combine(yr, pos, topk_weights, T, kk, H, y, status, st, sms));
 }

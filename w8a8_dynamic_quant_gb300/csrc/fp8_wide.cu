@@ -13,13 +13,14 @@
 // What bounds it.  Per 128-deep block a pair's MMAs take 512 cycles; an epilogue
 // warp's round -- barrier, two tensor-memory loads of 64 columns, 128 sums,
 // release -- takes about 750, most of it latency that does not grow with the
-// columns.  So few, wide rounds win: measured on 8192 x 14336 x 4096 (at one
-// stage of the work), 2 x 128 channels a tile 392 us, 2 x 96 452 us, one part of 160
-// with three accumulators 486 us; without the drain the pipeline took 261 us, near
-// the MMAs' own time.  Each part has its own issuing warp and its own four
-// epilogue warps.  The scales of four blocks are read at once and the block loop is
-// unrolled by them (388 -> 357 us), and the accumulator's columns come in four
-// overlapping loads (349 us, 2.76 PFLOP/s, 0.72 of twice the measured BF16 burst).
+// columns.  So few, wide rounds win: measured on 8192 x 14336 x 4096 before the two
+// steps below, 2 x 128 channels a tile 392 us, 2 x 96 452 us, one part of 160 with
+// three accumulators 486 us; without the drain the pipeline took 261 us, near the
+// MMAs' own time.  Each part has its own issuing warp (one for both: 437 against
+// 418 us) and its own four epilogue warps.  The scales of four blocks are read at
+// once and the block loop is unrolled by them (388 -> 357 us), and the accumulator's
+// columns come in four overlapping loads (349 us, 2.76 PFLOP/s, 0.72 of twice the
+// measured BF16 burst; called without a pause, under the power cap, 380 to 390 us).
 // One barrier for two blocks was slower (410 us): it lengthens the way above.
 //
 // Warp roles (384 threads, one CTA per SM):

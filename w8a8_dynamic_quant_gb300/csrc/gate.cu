@@ -25,7 +25,11 @@
 // experts per lane.  A choice is the warp's maximum of the lanes' best keys
 // (as order-preserving integers) at the lowest lane holding it.  Traffic is one
 // read of the logits and 12 bytes per choice; what bounds large batches is the
-// issue of some hundred instructions a token, small ones the chain of k choices.
+// issue of some hundred instructions a token, small ones the chain of k choices
+// (128 tokens, 256 experts in 8 groups of which 4 stay, top-8: 3.2 us a launch;
+// 16384 tokens, 64 experts, top-8: 9.6 us, where the reads alone would take 0.5).
+// A lane keeps its two best keys, so that it rescans its experts only at its third
+// choice.
 #include "kernels.cuh"
 
 namespace w8a8 {

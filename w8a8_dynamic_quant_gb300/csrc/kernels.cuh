@@ -93,7 +93,7 @@ struct Fp8GemmArgs {
 };
 // Scratch of the contraction (zero-filled once) for R rows, in E groups when grouped.
 size_t fp8_gemm_ws_bytes(int64_t E, int64_t R, int64_t N, int64_t K, bool grouped);
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, void* ws, int num_sms, cudaStream_t stream);
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, void* ws, cudaStream_t stream);
 
 // Expert router (gate.cu): logits [T,E] fp32 or bf16 -> ids [T,k], weights [T,k].  n_group <= 32, k <= 32.
 cudaError_t launch_gate(const void* logits, bool bf16, int64_t T, int E, const float* bias, bool sigmoid, int n_group,
