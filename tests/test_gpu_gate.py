@@ -127,6 +127,34 @@ def test_softmax_sum_order_does_not_matter():
     assert torch.equal(ids, key.sort(dim=1, descending=True, stable=True).indices[:, :8])
 
 
+@pytest.mark.parametrize("T,E,k,n_group,topk_group", [
+    (2050, 64, 8, 1, 1), (2049, 32, 8, 8, 3), (2051, 60, 5, 1, 1), (2048, 8, 2, 1, 1), (2061, 64, 6, 4, 2),
+    (2053, 60, 6, 4, 2), (8193, 128, 16, 16, 9), (8200, 100, 8, 1, 1), (8192, 72, 9, 1, 1)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_many_tokens(T, E, k, n_group, topk_group, scoring):
+    """Batches of many tokens: the first and last rows against the plain implementation, every row against the same
+    rows in calls of few tokens (the choice exactly, the weight within a few of its own roundings)."""
+    rng = np.random.default_rng(T)
+    x = logits(rng, T, E, True)
+    x[-1] = -np.inf
+    x[-2, : E // 2] = np.nan
+    bias = (rng.integers(-400, 401, E) / 4096.0).astype(np.float32) if T % 2 else None
+    args = dict(scoring=scoring, n_group=n_group, topk_group=topk_group, group_score="top2", renormalize=k % 2 == 0,
+                routed_scale=2.5)
+    for dtype in (torch.float32, torch.bfloat16):
+        xt = torch.from_numpy(x).cuda().to(dtype)
+        bt = None if bias is None else torch.from_numpy(bias).cuda()
+        ids, w = W.moe_gate_topk(xt, k, bias=bt, **args)
+        some = [W.moe_gate_topk(c.contiguous(), k, bias=bt, **args) for c in xt.split(500)]
+        assert torch.equal(ids, torch.cat([s[0] for s in some]))
+        np.testing.assert_allclose(w.cpu().numpy(), torch.cat([s[1] for s in some]).cpu().numpy(),
+                                   rtol=64 * 2.0 ** -24, atol=0)
+        rows = np.r_[0:40, T - 40:T]
+        ri, rw = reference(xt.float().cpu().numpy()[rows], k, bias, scoring, n_group, topk_group, "top2", k % 2 == 0, 2.5)
+        np.testing.assert_array_equal(ids.cpu().numpy()[rows], ri)
+        np.testing.assert_allclose(w.cpu().numpy()[rows], rw, rtol=64 * 2.0 ** -24, atol=0)
+
+
 def test_empty_and_other_stream():
     ids, w = W.moe_gate_topk(torch.empty(0, 16, device="cuda"), 4)
     assert ids.shape == (0, 4) and w.shape == (0, 4)

@@ -21,15 +21,14 @@
 // bit for bit.  S is summed with the rounding errors carried along (Knuth's
 // two-sum), so that its last bit does not depend on the order of the sum.
 //
-// One warp per token; lane l holds the experts [l * P, l * P + P), P = the
-// experts per lane.  A choice is the warp's maximum of the lanes' best keys
-// (as order-preserving integers) at the lowest lane holding it.  Traffic is one
-// read of the logits and 12 bytes per choice; what bounds large batches is the
-// issue of some hundred instructions a token, small ones the chain of k choices
-// (128 tokens, 256 experts in 8 groups of which 4 stay, top-8: 3.2 us a launch;
-// 16384 tokens, 64 experts, top-8: 9.6 us, where the reads alone would take 0.5).
-// A lane keeps its two best keys, so that it rescans its experts only at its third
-// choice.
+// L lanes per token (32; 8 or 16 for many tokens of few experts); lane l holds
+// the experts [l * P, l * P + P), P = the experts per lane.  A choice is the
+// maximum of the lanes' best keys (as order-preserving integers) at the lowest
+// lane holding it.  Traffic is one read of the logits and 12 bytes per choice;
+// what bounds large batches is the issue of some hundred instructions a token,
+// small ones the chain of k choices (128 tokens, 256 experts in 8 groups of which
+// 4 stay, top-8: 3.3 us a launch; 16384 tokens, 64 experts, top-8: 5.8 us, where
+// the reads and writes alone would take 0.5).
 #include "kernels.cuh"
 
 namespace w8a8 {
@@ -100,7 +99,7 @@ __device__ __forceinline__ uint32_t group_key(uint32_t k1, uint32_t k2, bool top
 }
 
 struct GateArgs {
-  int full;  // E = 32 P, and logits and bias allow 16-byte loads
+  int full;  // P divides E, and logits and bias allow 16-byte loads
   const void* logits;
   const float* bias;
   int64_t T;
@@ -111,19 +110,23 @@ struct GateArgs {
   float* weights;
 };
 
-template <int P, bool BF16, bool SIGMOID>
+// L lanes a token, P experts a lane.
+template <int L, int P, bool BF16, bool SIGMOID>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a) {
   pdl_trigger();
   pdl_wait();
-  __shared__ uint32_t s_gkey[kGateWarps][W8A8_MAX_EXPERTS];
-  const int lane = threadIdx.x & 31;
-  const int warp = threadIdx.x >> 5;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
+  constexpr int kTokens = 32 / L;  // of a warp
+  const int lane = threadIdx.x % L;           // within the token's lanes
+  const int first = threadIdx.x % 32 - lane;  // the token's first lane
+  int64_t t = (static_cast<int64_t>(blockIdx.x) * kGateWarps + threadIdx.x / 32) * kTokens;
   if (t >= a.T) return;
+  t += first / L;
+  const bool live = t < a.T;  // a warp's last tokens may not be there: they repeat the last one and store nothing
+  if (!live) t = a.T - 1;
   const int E = a.E;
   const int64_t row = t * E;
   float l[P], bias[P];
-  if (a.full) {
+  if (a.full && lane * P < E) {
     load_row<P, BF16>(a.logits, row + lane * P, l);
     if (a.bias != nullptr) load_row<P, false>(a.bias, lane * P, bias);
   } else {
@@ -150,11 +153,13 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
 #pragma unroll
     for (int i = 0; i < P; ++i) m = fmaxf(m, l[i]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float ex[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-      ex[i] = !(l[i] > kNegInf) ? 0.0f : l[i] == m ? 1.0f : expf(__fsub_rn(l[i], m));
+    for (int i = 0; i < P; ++i) {
+      const float x = expf(l[i] == m ? 0.0f : __fsub_rn(l[i], m));
+      ex[i] = l[i] > kNegInf ? x : 0.0f;
+    }
     if (a.bias != nullptr || !a.renorm) {
       float err = 0.0f;
 #pragma unroll
@@ -164,7 +169,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
         err += e;
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
+      for (int o = L / 2; o > 0; o >>= 1) {
         const float S2 = __shfl_xor_sync(0xffffffffu, S, o), err2 = __shfl_xor_sync(0xffffffffu, err, o);
         float e;
         two_sum(S, S2, S, e);
@@ -179,7 +184,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
       key[i] = (l[i] > kNegInf && s > kNegInf) ? ordered(s) : kOrderedNegInf;
     }
   }
-  if (!a.full) {
+  if (E != L * P) {
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (lane * P + i >= E) key[i] = 0u;
@@ -206,15 +211,16 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
       const int mine = lane / lanes;
       int above = 0;
       for (int g = 0; g < a.n_group; ++g) {
-        const uint32_t other = __shfl_sync(0xffffffffu, gk, g * lanes);
+        const uint32_t other = __shfl_sync(0xffffffffu, gk, first + g * lanes);
         above += other > gk || (other == gk && g < mine) ? 1 : 0;
       }
       if (above >= a.topk_group) {
 #pragma unroll
         for (int i = 0; i < P; ++i) key[i] = 0u;
       }
-    } else {  // through shared memory: lane g scans group g's keys (n_group <= 32)
-      uint32_t* sk = s_gkey[warp];
+    } else if constexpr (L == 32) {  // through shared memory: lane g scans group g's keys (n_group <= 32)
+      __shared__ uint32_t s_gkey[kGateWarps][32 * P];
+      uint32_t* sk = s_gkey[threadIdx.x / 32];
 #pragma unroll
       for (int i = 0; i < P; ++i)
         if (lane * P + i < E) sk[lane * P + i] = key[i];
@@ -243,41 +249,81 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
     }
   }
 
-  // The k largest keys; lane j keeps choice j.  A lane knows its two best (keys and places); the warp's maximum of
-  // the best, at its lowest lane, is the next choice, and that lane moves its second up.  Only a lane that gave both
-  // looks through its keys again.
-  uint32_t b1, b2, taken = 0u;
-  int a1, a2;
-  auto two_best = [&]() {
-    b1 = b2 = 0u;
-    a1 = a2 = 0;
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const uint32_t v = (taken >> i) & 1u ? 0u : key[i];
-      const bool first = v > b1, second = v > b2;  // places in rising order: ties stay with the lower
-      b2 = first ? b1 : second ? v : b2;
-      a2 = first ? a1 : second ? i : a2;
-      b1 = first ? v : b1;
-      a1 = first ? i : a1;
-    }
-  };
-  two_best();
+  // The k <= L largest keys; lane j keeps choice j: the maximum of the lanes' best keys, at its lowest lane.
   int my_id = 0;
   uint32_t my_key = 0u;
-  for (int j = 0; j < a.k; ++j) {
-    const uint32_t top = __reduce_max_sync(0xffffffffu, b1);
-    const int w = __ffs(__ballot_sync(0xffffffffu, b1 == top)) - 1;
-    const int id = __shfl_sync(0xffffffffu, lane * P + a1, w);
-    if (lane == j) {
-      my_id = id;
-      my_key = top;
+  if constexpr (L == 32) {
+    // A lane knows its two best (keys and places) and moves the second up when its best is taken.  Only a lane that
+    // gave both looks through its keys again.
+    uint32_t b1, b2, taken = 0u;
+    int a1, a2;
+    auto two_best = [&]() {
+      b1 = b2 = 0u;
+      a1 = a2 = 0;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const uint32_t v = (taken >> i) & 1u ? 0u : key[i];
+        const bool best = v > b1, second = v > b2;  // places in rising order: ties stay with the lower
+        b2 = best ? b1 : second ? v : b2;
+        a2 = best ? a1 : second ? i : a2;
+        b1 = best ? v : b1;
+        a1 = best ? i : a1;
+      }
+    };
+    two_best();
+    for (int j = 0; j < a.k; ++j) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, b1);
+      const int w = __ffs(__ballot_sync(0xffffffffu, b1 == top)) - 1;
+      const int id = __shfl_sync(0xffffffffu, lane * P + a1, w);
+      if (lane == j) {
+        my_id = id;
+        my_key = top;
+      }
+      if (lane == w) {
+        taken |= 1u << a1;
+        b1 = b2;
+        a1 = a2;
+        b2 = 0u;
+        if (b1 == 0u) two_best();
+      }
     }
-    if (lane == w) {
-      taken |= 1u << a1;
-      b1 = b2;
-      a1 = a2;
-      b2 = 0u;
-      if (b1 == 0u) two_best();
+  } else {
+    // A lane sorts its keys once, so that a choice costs the warp's tokens the same few steps.  Neighbours change
+    // places only where the later key is larger: equal keys stay in the order of their places.
+    uint32_t place[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) place[i] = i;
+#pragma unroll
+    for (int r = 0; r < P; ++r)
+#pragma unroll
+      for (int i = r & 1; i + 1 < P; i += 2) {
+        const bool swap = key[i + 1] > key[i];
+        const uint32_t k0 = key[i], p0 = place[i];
+        key[i] = swap ? key[i + 1] : k0;
+        place[i] = swap ? place[i + 1] : p0;
+        key[i + 1] = swap ? k0 : key[i + 1];
+        place[i + 1] = swap ? p0 : place[i + 1];
+      }
+    uint32_t places = 0u;  // four bits each, the best lowest
+#pragma unroll
+    for (int i = 0; i < P; ++i) places |= place[i] << (4 * i);
+    for (int j = 0; j < a.k; ++j) {
+      uint32_t top = key[0];
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const uint32_t at = __ballot_sync(0xffffffffu, key[0] == top) >> first;
+      const int w = __ffs(at) - 1;  // below L: one of the token's own lanes holds it
+      const int id = __shfl_sync(0xffffffffu, lane * P + static_cast<int>(places & 15u), first + w);
+      if (lane == j) {
+        my_id = id;
+        my_key = top;
+      }
+      if (lane == w) {
+#pragma unroll
+        for (int i = 0; i + 1 < P; ++i) key[i] = key[i + 1];
+        key[P - 1] = 0u;
+        places >>= 4;
+      }
     }
   }
   float wgt = 0.0f;
@@ -289,28 +335,29 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
   if (a.renorm) {
     float d = wgt;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    for (int o = L / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
     wgt = d > 0.0f ? __fdiv_rn(wgt, d) : 0.0f;
   } else if constexpr (!SIGMOID) {
     wgt = S > 0.0f ? __fdiv_rn(wgt, S) : 0.0f;
   }
-  if (lane < a.k) {
+  if (live && lane < a.k) {
     a.ids[t * a.k + lane] = my_id;
     a.weights[t * a.k + lane] = wgt * a.scale;
   }
 }
 
-template <int P>
+template <int L, int P>
 cudaError_t launch_p(GateArgs a, bool bf16, bool sigmoid, cudaStream_t stream) {
-  const dim3 g(static_cast<unsigned>((a.T + kGateWarps - 1) / kGateWarps)), b(32 * kGateWarps);
+  constexpr int per = kGateWarps * 32 / L;  // tokens of a CTA
+  const dim3 g(static_cast<unsigned>((a.T + per - 1) / per)), b(32 * kGateWarps);
   const auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0u; };
-  a.full = a.E == 32 * P && aligned(a.logits) && aligned(a.bias) ? 1 : 0;
+  a.full = a.E % P == 0 && aligned(a.logits) && aligned(a.bias) ? 1 : 0;
   if (bf16) {
-    return sigmoid ? launch_pdl(gate_kernel<P, true, true>, g, b, 0, stream, a)
-                   : launch_pdl(gate_kernel<P, true, false>, g, b, 0, stream, a);
+    return sigmoid ? launch_pdl(gate_kernel<L, P, true, true>, g, b, 0, stream, a)
+                   : launch_pdl(gate_kernel<L, P, true, false>, g, b, 0, stream, a);
   }
-  return sigmoid ? launch_pdl(gate_kernel<P, false, true>, g, b, 0, stream, a)
-                 : launch_pdl(gate_kernel<P, false, false>, g, b, 0, stream, a);
+  return sigmoid ? launch_pdl(gate_kernel<L, P, false, true>, g, b, 0, stream, a)
+                 : launch_pdl(gate_kernel<L, P, false, false>, g, b, 0, stream, a);
 }
 
 }  // namespace
@@ -320,19 +367,30 @@ cudaError_t launch_gate(const void* logits, bool bf16, int64_t T, int E, const f
                         cudaStream_t stream) {
   if (T == 0) return cudaSuccess;
   const GateArgs a{0, logits, bias, T, E, k, n_group, topk_group, top2, renorm, scale, ids, weights};
+  // Many tokens of few experts: 8 or 16 lanes a token, so that the steps of a choice serve four or two tokens.  Softmax,
+  // top-8, without groups, against a warp a token: E = 64 at 1024 tokens 2.6 us both, 2048 2.8 against 4.4, 16384 5.8
+  // against 8.3, 65536 14.1 against 28.6; E = 128 at 4096 tokens 5.7 against 5.3, 16384 8.7 against 10.0, 65536 28.5
+  // against 34.6.  (E = 256 in 16 lanes of 16: 57.8 us at 65536, against 47.)  Groups have to be whole lanes.
+  const auto whole = [=](int P) {
+    const int gs = E / n_group, lanes = gs / P;
+    return topk_group == n_group || (lanes * P == gs && (lanes & (lanes - 1)) == 0);
+  };
+  if (T >= 2048 && E <= 32 && k <= 8 && whole(4)) return launch_p<8, 4>(a, bf16, sigmoid, stream);
+  if (T >= 2048 && E > 32 && E <= 64 && k <= 8 && whole(8)) return launch_p<8, 8>(a, bf16, sigmoid, stream);
+  if (T >= 8192 && E > 64 && E <= 128 && k <= 16 && whole(8)) return launch_p<16, 8>(a, bf16, sigmoid, stream);
   // experts per lane: as few as hold E, so that common counts (96, 160, 192, 384 and the powers of two) fill every lane
   // and their groups are whole lanes
   const int P = (E + 31) / 32;
-  if (P <= 1) return launch_p<1>(a, bf16, sigmoid, stream);
-  if (P <= 2) return launch_p<2>(a, bf16, sigmoid, stream);
-  if (P <= 3) return launch_p<3>(a, bf16, sigmoid, stream);
-  if (P <= 4) return launch_p<4>(a, bf16, sigmoid, stream);
-  if (P <= 5) return launch_p<5>(a, bf16, sigmoid, stream);
-  if (P <= 6) return launch_p<6>(a, bf16, sigmoid, stream);
-  if (P <= 8) return launch_p<8>(a, bf16, sigmoid, stream);
-  if (P <= 12) return launch_p<12>(a, bf16, sigmoid, stream);
-  if (P <= 16) return launch_p<16>(a, bf16, sigmoid, stream);
-  return launch_p<32>(a, bf16, sigmoid, stream);
+  if (P <= 1) return launch_p<32, 1>(a, bf16, sigmoid, stream);
+  if (P <= 2) return launch_p<32, 2>(a, bf16, sigmoid, stream);
+  if (P <= 3) return launch_p<32, 3>(a, bf16, sigmoid, stream);
+  if (P <= 4) return launch_p<32, 4>(a, bf16, sigmoid, stream);
+  if (P <= 5) return launch_p<32, 5>(a, bf16, sigmoid, stream);
+  if (P <= 6) return launch_p<32, 6>(a, bf16, sigmoid, stream);
+  if (P <= 8) return launch_p<32, 8>(a, bf16, sigmoid, stream);
+  if (P <= 12) return launch_p<32, 12>(a, bf16, sigmoid, stream);
+  if (P <= 16) return launch_p<32, 16>(a, bf16, sigmoid, stream);
+  return launch_p<32, 32>(a, bf16, sigmoid, stream);
 }
 
 }  // namespace w8a8
