@@ -11,17 +11,21 @@
 // has its own scale, which comes from shared memory: four values a 16-byte load.)
 //
 // What bounds it.  Per 128-deep block a pair's MMAs take 512 cycles; an epilogue
-// warp's round -- barrier, two tensor-memory loads of 64 columns, 128 sums,
-// release -- takes about 750, most of it latency that does not grow with the
-// columns.  So few, wide rounds win: measured on 8192 x 14336 x 4096 before the two
-// steps below, 2 x 128 channels a tile 392 us, 2 x 96 452 us, one part of 160 with
-// three accumulators 486 us; without the drain the pipeline took 261 us, near the
-// MMAs' own time.  Each part has its own issuing warp (one for both: 437 against
-// 418 us) and its own four epilogue warps.  The scales of four blocks are read at
-// once and the block loop is unrolled by them (388 -> 357 us), and the accumulator's
-// columns come in four overlapping loads (349 us, 2.76 PFLOP/s, 0.72 of twice the
-// measured BF16 burst; called without a pause, under the power cap, 380 to 390 us).
-// One barrier for two blocks was slower (410 us): it lengthens the way above.
+// warp's round -- barrier, tensor-memory loads of 128 columns, 128 sums, release --
+// takes about 660, and the end of a tile about 2200 (sums to bf16, shared memory, TMA)
+// in which the MMAs are at most two blocks ahead.  On 8192 x 14336 x 4096, 338 us
+// (2.85 PFLOP/s, 0.75 of twice the measured BF16 burst; called without a pause, under
+// the power cap, 368):
+//   - few, wide rounds: 2 x 128 channels a tile 392 us, 2 x 96 452 us, one part of
+//     160 with three accumulators 486 us (before the steps below); sixteen epilogue
+//     warps of 64 channels 365 us against 357; one barrier for two blocks 410 us: it
+//     lengthens the way above.  Without the drain the pipeline took 261 us;
+//   - an issuing warp (437 -> 418 us) and four epilogue warps per part;
+//   - scales of four blocks read at once, the loop unrolled by them (388 -> 357 us);
+//   - overlapping accumulator loads (357 -> 349 us);
+//   - registers: the segment comes with its first scales from the warp that walks
+//     ahead, the walk is worked out again where it is seldom needed, and both halves
+//     of a tile are staged at once at the price of the fifth stage (355 -> 338 us).
 //
 // Warp roles (384 threads, one CTA per SM):
 //   warp 0       TMA producer
@@ -43,12 +47,14 @@ constexpr int G_CH = 256;     // channels per tile
 constexpr int G_PART = 128;   // channels per part (MMA N)
 constexpr int G_THREADS = 384;
 constexpr int G_EPI0 = 4;
-constexpr int G_STAGES = 5;
+constexpr int G_STAGES = 4;
+constexpr int G_SEGS = 4;  // the scales are at most two groups, so two segments, ahead of an epilogue warp
 constexpr uint32_t G_X_BYTES = G_HALF * F_BK;       // 16 KB: the CTA's token rows
 constexpr uint32_t G_P_BYTES = G_PART / 2 * F_BK;   // 8 KB: its weight rows of a part
 constexpr uint32_t G_STAGE_BYTES = G_X_BYTES + 2 * G_P_BYTES;
 constexpr uint32_t G_SCALE_BYTES = F_SRING * F_SG * 2 * G_HALF * 4;
-constexpr uint32_t G_STG_WARP = 32 * 128;            // output staging: [32 tokens][64 channels] bf16 per warp
+constexpr uint32_t G_STG_HALF = 32 * 128;            // output staging of a warp: two of [32 tokens][64 channels] bf16
+constexpr uint32_t G_STG_WARP = 2 * G_STG_HALF;
 constexpr uint32_t G_STG_BYTES = F_EPI_WARPS * G_STG_WARP;
 constexpr size_t kWideSmem = static_cast<size_t>(G_STAGES) * G_STAGE_BYTES + G_SCALE_BYTES + G_STG_BYTES + 1024;
 constexpr size_t kWidePiece = static_cast<size_t>(F_EPI_WARPS) * G_PART * 32;  // floats of one CTA's partial sums
@@ -59,7 +65,7 @@ struct WSeg {
   int row0;      // first token row (of all R)
   int tvalid;    // tokens
   int kb0, kb1;  // blocks [kb0, kb1)
-  int unit;
+  int unit;      // < 0: no more segments
 };
 
 __device__ __forceinline__ int wide_blocks(int c) { return (c + G_TOK - 1) / G_TOK; }
@@ -88,27 +94,30 @@ __device__ __forceinline__ void fma_scaled(float* acc, const uint32_t* v, float 
   }
 }
 
-// acc += s * the warp's 128 accumulator columns, 32 at a time through two buffers: while one is added the other's load
-// runs.  The accumulator is released once its last load is complete, and the next one's barrier probed while the last
-// sums run.
+// acc += s * the warp's 128 accumulator columns, through buffers of 32 and 16: while one is added the other's load runs.
+// (With 32 and 32 the block loop spilled.)  The accumulator is released once its last load is complete, and the next
+// one's barrier probed while the last sums run.
 __device__ __forceinline__ bool drain_wide(uint32_t taddr, float s, uint32_t release, int lane, uint32_t next_bar,
                                            uint32_t next_parity, float (&acc)[G_PART]) {
-  uint32_t u[32], v[32];
+  uint32_t u[32], v[16];
   tmem_fetch(taddr, u);
   tmem_fetch(taddr + 32, v);
   tmem_ready(u);
   tmem_ready(v);
   fma_scaled<32>(acc, u, s);
-  tmem_fetch(taddr + 64, u);
-  fma_scaled<32>(acc + 32, v, s);
+  tmem_fetch(taddr + 48, u);
+  fma_scaled<16>(acc + 32, v, s);
   tmem_ready(u);
-  tmem_fetch(taddr + 96, v);
-  fma_scaled<32>(acc + 64, u, s);
+  tmem_fetch(taddr + 80, v);
+  fma_scaled<32>(acc + 48, u, s);
   tmem_ready(v);
+  tmem_fetch(taddr + 96, u);
+  fma_scaled<16>(acc + 80, v, s);
+  tmem_ready(u);
   tc_fence_before();
   arrive_lane0(release, lane);
   const bool next = mbar_test(next_bar, next_parity);
-  fma_scaled<32>(acc + 96, v, s);
+  fma_scaled<32>(acc + 96, u, s);
   return next;
 }
 
@@ -116,21 +125,17 @@ __device__ __forceinline__ bool drain_wide(uint32_t taddr, float s, uint32_t rel
 // c of row r at c ^ (r & 7), so neither the row-wise writes nor the reads conflict.
 __device__ __forceinline__ uint32_t stg_at(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// 8 channels n0 + 8c .. (16 bytes; + bias) of the lane's row into the staging buffer.
-__device__ __forceinline__ void stage_chunk(uint8_t* stg, int c, int lane, const float (&f)[8], const uint16_t* bias,
-                                            int64_t n0, int64_t N) {
-  uint32_t o[4];
+// 8 channels (chunk c, 16 bytes) of the lane's row into the staging buffers.
+__device__ __forceinline__ void stage_chunk(uint8_t* stg, int c, int lane, const float* f) {
+  *reinterpret_cast<uint4*>(stg + (c >> 3) * G_STG_HALF + stg_at(lane, c & 7)) =
+      make_uint4(f32x2_to_bf16x2_bits(f[0], f[1]), f32x2_to_bf16x2_bits(f[2], f[3]), f32x2_to_bf16x2_bits(f[4], f[5]),
+                 f32x2_to_bf16x2_bits(f[6], f[7]));
+}
+// f[i] += bias[n + i] inside N.
+template <int C>
+__device__ __forceinline__ void add_bias(float* f, const uint16_t* bias, int64_t n, int64_t N) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float lo = f[2 * k], hi = f[2 * k + 1];
-    if (bias != nullptr) {
-      const int64_t n = n0 + 8 * c + 2 * k;
-      lo += n < N ? bf16_bits_to_f32(bias[n]) : 0.0f;
-      hi += n + 1 < N ? bf16_bits_to_f32(bias[n + 1]) : 0.0f;
-    }
-    o[k] = f32x2_to_bf16x2_bits(lo, hi);
-  }
-  *reinterpret_cast<uint4*>(stg + stg_at(lane, c & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+  for (int i = 0; i < C; ++i) f[i] += n + i < N ? bf16_bits_to_f32(bias[n + i]) : 0.0f;
 }
 
 // The staged rows to y rows row0 + r < row0 + rows, channels n0 .. (16-byte chunks [c_lo, c_hi) of them).  Rows of y
@@ -163,11 +168,9 @@ __device__ __forceinline__ void store_wide(const uint8_t* stg, uint16_t* y, int6
   }
 }
 
-// The same by TMA (32 whole rows; columns past N are cut off by the map), asynchronously: stg_free() before the
-// buffer is written again.
+// The same by TMA (32 whole rows; columns past N are cut off by the map), asynchronously: the writes are fenced for it
+// before, and stg_free() comes before the buffer is written again.
 __device__ __forceinline__ void tma_store_rows(const CUtensorMap* map, uint32_t stg, int x, int y) {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  __syncwarp();
   asm volatile(
       "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
       " @e cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n"
@@ -178,6 +181,16 @@ __device__ __forceinline__ void tma_store_rows(const CUtensorMap* map, uint32_t 
 __device__ __forceinline__ void stg_free() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncwarp();
+}
+
+// This CTA's pair among all, its clusters, and the pair's walk over `units` units.
+__device__ __forceinline__ Walk pair_walk(const KArgs& a, int units, int KB, int& me, int64_t& total, int& runs) {
+  uint32_t crank, cluster_id, nclusters;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
+  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(cluster_id));
+  asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(nclusters));
+  me = static_cast<int>(cluster_id) * a.split + static_cast<int>(crank >> 1);
+  return start_walk(a, units, KB, static_cast<int>(nclusters), me, true, total, runs);
 }
 
 __global__ void __launch_bounds__(G_THREADS, 1)
@@ -196,8 +209,7 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   __shared__ int s_prefix[F_MAX_E + 1];
   __shared__ int s_off[F_MAX_E + 1];
   __shared__ int s_warp[G_THREADS / 32];
-  __shared__ WSeg s_seg[F_EPI_WARPS];   // the epilogue warps' segment and place in the walk: 128 sums a thread leave
-  __shared__ Walk s_walk[F_EPI_WARPS];  // no registers to hold them through the block loop
+  __shared__ WSeg s_seg[G_SEGS];         // the segments in turn, from the scales warp to the epilogue
   __shared__ unsigned long long s_rows;
 
   const int tid = threadIdx.x;
@@ -214,10 +226,8 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   float* s_part = reinterpret_cast<float*>(stages);  // [epilogue warp][channel][token], after the last block
   uint8_t* s_out = stages + G_STAGES * G_STAGE_BYTES + G_SCALE_BYTES;
   // CTAs 2i and 2i + 1 of a cluster are a pair; rank: the CTA's place in it
-  uint32_t crank, cluster_id, nclusters;
+  uint32_t crank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
-  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(cluster_id));
-  asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(nclusters));
   const uint32_t rank = crank & 1u, even = crank & ~1u;
   const uint16_t pair_mask = static_cast<uint16_t>(3u << even);
 
@@ -261,14 +271,12 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     if (tid == 0 && blockIdx.x == 0) set_status(a.status, W8A8_ERR_GROUP_LIST, 0u);
     units = 0;
   }
-  const int me = static_cast<int>(cluster_id) * a.split + static_cast<int>(crank >> 1);
-  int64_t total;
-  int runs;
-  const Walk walk0 = start_walk(a, units, KB, static_cast<int>(nclusters), me, true, total, runs);
-
   if (warp < G_EPI0) {
-    // the epilogue's 128 sums a thread take registers from these warps (384 x 168 at launch = 128 x 88 + 256 x 208)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    // the epilogue's 128 sums a thread take registers from these warps (384 x 168 at launch = 128 x 72 + 256 x 216)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    int me, runs;
+    int64_t total;
+    const Walk walk0 = pair_walk(a, units, KB, me, total, runs);
     if (warp == 0) {
       // ---------------------------------------------------------- TMA producer (both CTAs)
       const uint32_t full_even0 = smem_cluster_addr(smem_u32(&bar_full[0]), even);
@@ -347,12 +355,12 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       // ----------------------------------------------------------- scales (both CTAs)
       const int NB = static_cast<int>((N + 127) / 128);
       const bool vec = (KB & 3) == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 15u) == 0u;
-      int slot = 0;
+      int slot = 0, seg = 0;
       uint32_t phase = 0;
       Walk w = walk0;
       WSeg s;
       bool ok = true;
-      while (ok && uni(next_wide(w, E, WB, s_prefix, s_off, s))) {
+      for (; ok && uni(next_wide(w, E, WB, s_prefix, s_off, s)); ++seg) {
         const int nb = 2 * s.wb;
         const float* w0 = a.wsc + (static_cast<int64_t>(s.e) * NB + nb) * KB;
         const bool two = nb + 1 < NB;
@@ -387,6 +395,7 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             for (int p = 0; p < 2; ++p)
 #pragma unroll
               for (int i = 0; i < 4; ++i) d[(j * 2 + p) * G_HALF + 32 * i] = v[i][j] * wv[p][j];
+          if (lane == 0 && k0 <= s.kb0) s_seg[seg % G_SEGS] = s;  // with its first group
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bar_scf[slot]));
           if (++slot == F_SRING) {
@@ -395,10 +404,15 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
           }
         }
       }
+      if (ok && wait_all(smem_u32(&bar_sce[slot]), phase ^ 1u, &s_abort, a.status, 12u)) {  // the end, as a group
+        if (lane == 0) s_seg[seg % G_SEGS].unit = -1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_scf[slot]));
+      }
     }
   } else {
     // ---------------------------------------------------------------- epilogue (both CTAs)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int ew = warp - G_EPI0;
     const int q = warp & 3;
     const int p = ew >> 2;
@@ -409,26 +423,15 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     bool probed = false;        // the next accumulator was seen complete
     const uint32_t accf0 = smem_u32(&bar_accf[2 * p]);
     const float* my_scale = s_scale + p * G_HALF + 32 * q + lane;
-    s_walk[ew] = walk0;
+    const bool shares = a.split > 1;  // one segment, whose sums meet the cluster's others
     bool ok = true;
-    while (ok) {
-      __syncwarp();
-      {
-        Walk w = s_walk[ew];
-        WSeg s;
-        if (!uni(next_wide(w, E, WB, s_prefix, s_off, s))) break;
-        __syncwarp();
-        if (lane == 0) {
-          s_walk[ew] = w;
-          s_seg[ew] = s;
-        }
-        __syncwarp();
-      }
-      const int kb1 = uni(s_seg[ew].kb1);
+    for (int seg = 0; ok && (seg == 0 || !shares); seg = (seg + 1) % G_SEGS) {
+      ok = wait_all(smem_u32(&bar_scf[0]) + 8 * (grp & 1u), (grp >> 1) & 1u, &s_abort, a.status, 6u);
+      if (ok && uni(s_seg[seg].unit) < 0) break;
+      const int kb0 = ok ? uni(s_seg[seg].kb0) : 0, kb1 = ok ? uni(s_seg[seg].kb1) : 0;
       float acc[G_PART];
 #pragma unroll
       for (int i = 0; i < G_PART; ++i) acc[i] = 0.0f;
-      const int kb0 = uni(s_seg[ew].kb0);
       for (int k4 = kb0 & ~(F_SG - 1); ok && k4 < kb1; k4 += F_SG) {
         ok = wait_all(smem_u32(&bar_scf[0]) + 8 * (grp & 1u), (grp >> 1) & 1u, &s_abort, a.status, 6u);
         if (!ok) break;
@@ -451,40 +454,39 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
         }
       }
       // every part's MMAs are done with the ring before it takes the sums of a shared unit
-      if (a.split > 1) asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (shares) asm volatile("bar.sync 1, 256;" ::: "memory");
       if (!ok) break;
-      const WSeg s = s_seg[ew];
+      const WSeg s = s_seg[seg];
       const int64_t n0 = static_cast<int64_t>(s.wb) * G_CH + p * G_PART;
       const int rbase = static_cast<int>(rank) * G_HALF + 32 * q;  // first token of the warp inside the tile
       const int rows = min(32, s.tvalid - rbase);
       if (n0 >= N || rows <= 0) continue;
       const int64_t row0 = static_cast<int64_t>(s.row0) + rbase;
-      auto stage8 = [&](int c, const float (&f)[8]) { stage_chunk(stg, c, lane, f, a.bias, n0, N); };
       if (s.kb0 == 0 && s.kb1 == KB) {
+        if (a.bias != nullptr) add_bias<G_PART>(acc, a.bias, n0, N);
+        stg_free();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (n0 + half * 64 >= N) break;
-          stg_free();
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            float f[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = acc[(half * 8 + c) * 8 + k];
-            stage8(half * 8 + c, f);
-          }
-          if (y_tma != 0 && rows == 32) {
-            tma_store_rows(&tmY, smem_u32(stg), static_cast<int>(n0) + half * 64, static_cast<int>(row0));
-          } else {
-            __syncwarp();
-            store_wide(stg, a.y, row0, rows, N, n0 + half * 64, lane);
-          }
+        for (int c = 0; c < G_PART / 8; ++c) stage_chunk(stg, c, lane, acc + 8 * c);
+        const bool two = n0 + 64 < N;
+        if (y_tma != 0 && rows == 32) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          tma_store_rows(&tmY, smem_u32(stg), static_cast<int>(n0), static_cast<int>(row0));
+          if (two) tma_store_rows(&tmY, smem_u32(stg + G_STG_HALF), static_cast<int>(n0) + 64, static_cast<int>(row0));
+        } else {
+          __syncwarp();
+          store_wide(stg, a.y, row0, rows, N, n0, lane);
+          if (two) store_wide(stg + G_STG_HALF, a.y, row0, rows, N, n0 + 64, lane);
         }
-      } else if (a.split > 1) {  // a part of K of the cluster's unit
+      } else if (shares) {  // a part of K of the cluster's unit
         float* d = s_part + ew * G_PART * 32 + lane;
 #pragma unroll
         for (int i = 0; i < G_PART; ++i) d[i * 32] = acc[i];
       } else {
         // a piece of a cut unit (as in fp8_gemm.cu): [channel][token] partial sums
+        int me, runs;
+        int64_t total;
+        pair_walk(a, s_prefix[E], KB, me, total, runs);
         const int64_t u0 = static_cast<int64_t>(s.unit) * KB;
         const int first = run_owner(total, runs, u0), last = run_owner(total, runs, u0 + KB - 1);
         auto piece = [&](int c) {
@@ -523,11 +525,14 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                     for (int k = 0; k < 16; ++k) f[k >> 3][k & 7] += v[j][k];
                   }
               }
-              stage8(half * 8 + c, f[0]);
-              stage8(half * 8 + c + 1, f[1]);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                if (a.bias != nullptr) add_bias<8>(f[j], a.bias, n0 + (half * 8 + c + j) * 8, N);
+                stage_chunk(stg, half * 8 + c + j, lane, f[j]);
+              }
             }
             __syncwarp();
-            store_wide(stg, a.y, row0, rows, N, n0 + half * 64, lane);
+            store_wide(stg + half * G_STG_HALF, a.y, row0, rows, N, n0 + half * 64, lane);
           }
         }
       }
@@ -538,7 +543,9 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     // the parts' sums meet: every CTA adds its share of the channels over its peers' shared memory, in the order of K
     __syncwarp();
     cluster_sync_all();
-    Walk w = walk0;
+    int me, runs;
+    int64_t total;
+    Walk w = pair_walk(a, s_prefix[E], KB, me, total, runs);
     WSeg s;
     if (warp >= G_EPI0 && uni(next_wide(w, E, WB, s_prefix, s_off, s))) {
       const int ew = warp - G_EPI0;
@@ -556,10 +563,11 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
 #pragma unroll
             for (int k = 0; k < 8; ++k) f[k] += ld_cluster(p + k * 128);
           }
-          stage_chunk(stg, c, lane, f, a.bias, n0, N);
+          if (a.bias != nullptr) add_bias<8>(f, a.bias, n0 + 8 * c, N);
+          stage_chunk(stg, c, lane, f);
         }
         __syncwarp();
-        store_wide(stg, a.y, static_cast<int64_t>(s.row0) + rbase, rows, N, n0 + (lo >> 3) * 64, lane, lo & 7,
+        store_wide(stg + (lo >> 3) * G_STG_HALF, a.y, static_cast<int64_t>(s.row0) + rbase, rows, N, n0 + (lo >> 3) * 64, lane, lo & 7,
                    (lo & 7) + share);
       }
     }
