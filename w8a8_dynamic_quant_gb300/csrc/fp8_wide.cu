@@ -30,7 +30,8 @@
 // Warp roles (384 threads, one CTA per SM):
 //   warp 0       TMA producer
 //   warps 1, 2   issue the MMAs of part 0, 1 (even CTA); warp 1 owns the TMEM
-//   warp 3       scales: xs * ws, [block][part][token], four blocks at a time, into a shared-memory ring
+//   warp 3       scales: xs * ws, [block][part][token], four blocks at a time, into a shared-memory ring, with the
+//                segment that they belong to
 //   warps 4-11   epilogue: part (w - 4) / 4, TMEM lanes 32 * (w % 4) ..
 // Whole rows of 32 tokens leave through shared memory by TMA.  Work, cut units and bounded waits as in fp8_gemm.cu.
 #include "fp8_common.cuh"
