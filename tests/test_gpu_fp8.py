@@ -166,8 +166,15 @@ def test_dense(M, N, K):
 
 @pytest.mark.parametrize("M,N,K", [(64, 2048, 7168), (1, 4096, 7168), (8, 129, 16384), (300, 520, 4096),
                                    (2100, 1111, 1040), (400, 1002, 528), (4096, 2048, 512),
-                                   (1024, 1024, 65536)])
+                                   (1024, 1024, 65536), (129, 5000, 16400)])
 def test_dense_large(M, N, K):
+    check_dense(M, N, K, bias=True)
+
+
+@pytest.mark.parametrize("M,N,K", [(50, 9900, 8192), (2100, 1111, 16384)])
+def test_dense_cut_units(M, N, K):
+    """Few long units that are no whole number for the pairs: their pieces meet in the workspace."""
+    assert W.fp8_matmul_workspace_bytes(M, N, K) > 1 << 20  # room for pieces
     check_dense(M, N, K, bias=True)
 
 
@@ -215,6 +222,11 @@ def check_grouped(counts, N, K, seed=0):
 @pytest.mark.parametrize("N,K", [(128, 256), (200, 400), (577, 1040)])
 def test_grouped(counts, N, K):
     check_grouped(counts, N, K)
+
+
+@pytest.mark.parametrize("counts", [[3, 0, 17, 1, 64], [130, 1, 0, 257, 40, 2], [2, 1]])
+def test_grouped_cut_units(counts):
+    check_grouped(counts, 577, 16384)
 
 
 def test_grouped_large():

@@ -238,16 +238,18 @@ __device__ __forceinline__ bool bad_list(const KArgs& a, int rows, int s_bad, un
          (a.group_list != nullptr && a.R > INT32_MAX / a.E && s_rows != static_cast<unsigned long long>(a.R));
 }
 
-// How the units' blocks are shared out over C pairs, from costs in eighths of a block's time (about 0.4 us).  Uncut:
-// whole units, every C-th one to a pair.  Cut: equal runs of blocks, aligned to units where there are fewer runs
-// than pairs; the pieces of a cut unit cost about 9 blocks (write, fence, arrival) and one or three blocks a piece
-// to add (measured: 64 x 7168 x 2048 7.1 us uncut, 10.9 us in two pieces, 64 x 2048 x 7168 13.1 us in seven).
+// How the units' blocks are shared out over C pairs, from costs in eighths of a block's time (about 0.25 us at 64
+// tokens a tile, 0.4 us at 256).  Uncut: whole units, every C-th one to a pair.  Cut: equal runs of blocks, aligned to
+// units where there are fewer runs than pairs; writing, fencing and adding the pieces costs about 22 blocks (30 for
+// 256 tokens, whose pieces are 128 KB a CTA) and one or three more a piece.  Measured, uncut against cut: 80 units of
+// 16 blocks and 64 tokens 15.2 and 17.3 us, 96 of 32 and 128 tokens 39.6 and 38.6; with 256 tokens, 112 units of 32
+// blocks 31.2 and 41.6, 336 71 and 83, 80 of 56 46.2 and 44.3.
 struct RunPlan {
   int runs;      // 0: uncut
   int64_t cost;
 };
 __host__ __device__ inline RunPlan plan_runs(int64_t units, int KB, int C, bool wide) {
-  const int64_t fixed = 72, per = wide ? 24 : 8;
+  const int64_t fixed = wide ? 240 : 180, per = wide ? 24 : 8;
   RunPlan p{0, (units + C - 1) / C * KB * 8};
   if (units <= 0) return p;
   const int64_t total = units * KB;

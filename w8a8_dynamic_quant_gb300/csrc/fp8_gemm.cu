@@ -38,13 +38,14 @@
 // piece of a cut unit leaves its partial sums in the workspace, and the warp
 // that arrives last at a unit adds the pieces in the order of K and writes the
 // result: no order of arrival changes a bit, and no warp waits for another.
-// The cluster's sum costs about 1.2 us, a cut unit's 3.5 to 6 (64 x 2048 x 7168 in
-// seven parts a unit: 10.1 us in clusters of 7 pairs, 13.1 us through the workspace).
+// The cluster's sum costs about 1.2 us, a cut unit's 5 and more (64 x 2048 x 7168:
+// 10.1 us in clusters of 6 pairs, 13.1 us in seven parts through the workspace), so
+// units are cut only where they are few and long.
 //
 // What bounds it.  Many experts with few rows: the weight stream (256 experts of
 // 4096 x 7168, four rows each: 1041 us, 7.2 TB/s).  One small layer: latency.
 // 64 x 2048 x 7168 could stream its weights in 2.3 us; launch and the first
-// tiles' way take about 4 (16 x 256 x 512: 4.3 us in all), seven blocks a pair
+// tiles' way take about 4 (16 x 256 x 512: 4.3 us in all), ten blocks a pair
 // in turn and the sum over the cluster the rest.
 //
 // Every mbarrier wait is bounded (2 s): on expiry the CTA sets
