@@ -561,9 +561,10 @@ struct Plan {
   int nt, pairs, split, runs;
 };
 // A dense problem of few tiles lets the pairs of a cluster share each tile's K (their sums meet in distributed shared
-// memory, about 3 or 7 blocks' time), as far as the clusters fit the GPU at once; else plan_runs.  The plan goes by the
-// sizes alone, so that the workspace's size and the launch agree on every device: no pair waits for a pair of another
-// cluster, so a GPU with fewer SMs runs the same grid in two waves.
+// memory: about 3 blocks' time, or 5 and 1.5 a part for 256 tokens, where 256 x 5000 x 2048 takes 11.9 us whole and 13.6
+// in two parts), as far as the clusters fit the GPU at once; else plan_runs.  The plan goes by the sizes alone, so that
+// the workspace's size and the launch agree on every device: no pair waits for a pair of another cluster, so a GPU with
+// fewer SMs runs the same grid in two waves.
 Plan make_plan(int64_t E, int64_t R, int64_t N, int64_t K, bool grouped) {
   constexpr int most = F_MAX_CLUSTERS;
   Plan p{tile_tokens(E, R, grouped), most, 1, -1};
@@ -578,9 +579,9 @@ Plan make_plan(int64_t E, int64_t R, int64_t N, int64_t K, bool grouped) {
   // clusters of 2 ks CTAs (one a SM) that are resident at once on 152 SMs, as the occupancy query gives them
   constexpr int kFit[F_MAX_SPLIT + 1] = {0, 76, 36, 23, 15, 13, 8, 7, 7};
   for (int ks = 2; ks <= F_MAX_SPLIT; ++ks) {
-    const int64_t cost = (KB + ks - 1) / ks * 8 + (wide ? 56 : 24);
+    const int64_t cost = (KB + ks - 1) / ks * 8 + (wide ? 40 + 12 * ks : 24);
     if (units > kFit[ks] || units * ks > most || 2 * ks > KB || cost >= best) continue;
-    if (wide && 16 % ks != 0) continue;  // equal shares of a part's sixteen 8-channel chunks
+    if (wide && 16 % ks != 0) continue;  // equal shares of a part's sixteen 8-channel chunks (three parts: slower)
     best = cost;
     p.split = ks;
     p.runs = 0;
