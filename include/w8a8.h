@@ -403,8 +403,9 @@ W8A8_API w8a8_status w8a8_fp8_quant(const uint16_t* x, int64_t M, int64_t K, uin
 
 /* y13 [R,2I] bf16 (gate channels [0,I), up channels [I,2I)) -> q [R,I] E4M3,
  * scale [R, ceil(I/128)]: the same quantisation of h = (g * sigmoid(g)) * u,
- * which stays binary32 (not rounded to bf16 first).  exp and the reciprocal
- * are within a few binary32 units in the last place. */
+ * which stays binary32 (not rounded to bf16 first).  Its exp is within
+ * 2 + 1.173 |g| binary32 units in the last place (for g < 0 units of h; for
+ * g >= 0 they count exp(-g) times), its other steps within 5 together. */
 W8A8_API w8a8_status w8a8_fp8_swiglu_quant(const uint16_t* y13, int64_t R, int64_t I, uint8_t* q, float* scale,
                                            w8a8_stream_t stream);
 

@@ -121,6 +121,28 @@ def test_swiglu_quant(R, I):
     assert bool((err <= torch.maximum(want.abs() * 2.0 ** -4, torch.full_like(want, 2.0 ** -10)) * (1 + 1e-4)).all())
 
 
+def test_swiglu_quant_far_gates():
+    """Blocks whose gates all lie far out: the sigmoid of a negative gate falls through binary32's smallest normal
+    value at -87.3 to its smallest at -103, and h with a large up value stays well above either."""
+    gates = [-16.0, -20.0, -60.0, -87.0, -87.5, -88.0, -88.5, -89.0, -95.0, 20.0, 60.0, 88.5, 100.0]
+    g = torch.tensor(gates, device="cuda").view(-1, 1).expand(-1, 256)
+    u = torch.randn(len(gates), 256, generator=gen(7), device="cuda") * 2.0 ** 30
+    y = torch.cat([g, u], 1).to(torch.bfloat16)
+    q, s = W.w8a8_fp8_swiglu_quant(y)
+    g, u = y[:, :256].double(), y[:, 256:].double()
+    t = torch.exp(-g.abs())
+    h = g * torch.where(g > 0, 1.0, t) / (1 + t) * u
+    # relative to h: exp within 2 + 1.173 |g| units of 2^-23 (for a positive gate they count t / (1 + t) < 1 times) and,
+    # below the normal values, 2 of 2^-149; the sum, the quotient and the products 4.5, and half of 2^-149 where one of
+    # them is below the normal values
+    rel = (2 + 1.173 * g.abs() + 4.5) * 2.0 ** -23 + torch.where(g > 0, 0.0, 2.5 * 2.0 ** -149 / t)
+    rs = h.view(len(gates), 2, 128).abs().amax(2) / 448.0
+    assert bool(((s.double() - rs).abs() <= rs * (rel[:, :1] + 2.0 ** -24)).all()), (s.double() / rs - 1).tolist()
+    want = h / spread(s, 256)
+    step = torch.maximum(want.abs() * 2.0 ** -4, torch.full_like(want, 2.0 ** -10))  # half a step of E4M3
+    assert bool(((q.double() - want).abs() <= step + want.abs() * (rel + 2.0 ** -24)).all())
+
+
 def bound(q, xs, w, ws, K, ref):
     """One bf16 rounding of the exact value, and the binary32 sums: 128 products and their sum inside a block by
     the tensor core (held to 2^-20 of the magnitude: its adder may cut a few bits below binary32) and one
