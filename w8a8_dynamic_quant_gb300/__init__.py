@@ -474,17 +474,23 @@ def moe_layer(x: torch.Tensor, x_scale: Optional[torch.Tensor], topk_ids: torch.
 # and the launch are 5 of them.
 
 _bound = {}
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_get_device = torch._C._cuda_getDevice
+_raw_stream = _get_device = None  # torch's own, looked up with the first function: a torch without CUDA lacks them
 _empty, _Tensor = torch.empty, torch.Tensor
 _BF16, _F32, _I64, _E4M3 = torch.bfloat16, torch.float32, torch.int64, torch.float8_e4m3fn
+
+
+def _bind(name: str):
+    global _raw_stream, _get_device
+    _raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    fn = _bound[name] = getattr(_capi.lib(), name)
+    return fn
 
 
 def _call(name: str, index: int, *args):
     """The library's `name` on the current stream of CUDA device `index` (the last argument)."""
     fn = _bound.get(name)
     if fn is None:
-        fn = _bound[name] = getattr(_capi.lib(), name)
+        fn = _bind(name)
     if _get_device() == index:
         code = fn(*args, _raw_stream(index))
     else:
