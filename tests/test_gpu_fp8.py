@@ -384,6 +384,23 @@ def test_dense_offsets_past_32_bits():
     assert bool((err <= bound(q[rows], xs[rows], w, ws, K, ref)).all())
 
 
+def test_dense_most_rows():
+    """The largest number of rows there may be: their last block of 256 ends at 2^31."""
+    M, N, K = 2 ** 31 - 1, 1, 16
+    w = torch.ones(N, K, device="cuda").to(torch.float8_e4m3fn)
+    ws = torch.ones(1, 1, device="cuda")
+    q = torch.zeros(M, K, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    xs = torch.zeros(M, 1, device="cuda")
+    y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0, 255, 256, M // 2, M - 256, M - 255, M - 2, M - 1], device="cuda")
+    q.view(torch.uint8)[rows] = 0x38  # 1.0
+    xs[rows, 0] = torch.arange(1, 9, device="cuda").float()
+    W.w8a8_fp8_matmul(q, xs, w, ws, y=y)
+    assert y[rows, 0].tolist() == [16.0 * (i + 1) for i in range(8)]  # 16 products of ones, times the row's scale
+    y[rows] = 0
+    assert not bool(y.any())
+
+
 @pytest.mark.parametrize("M,N,K", [(48, 1100, 4096), (300, 1100, 4096), (700, 2000, 1536)])
 def test_matmul_in_a_graph(M, N, K):
     """Captured and replayed on changed inputs: nothing of a call is left on the host, the workspace stays ready."""

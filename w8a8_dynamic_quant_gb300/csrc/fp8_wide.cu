@@ -69,7 +69,8 @@ struct WSeg {
   int unit;      // < 0: no more segments
 };
 
-__device__ __forceinline__ int wide_blocks(int c) { return (c + G_TOK - 1) / G_TOK; }
+// (c + G_TOK - 1 would pass INT32_MAX, which c may be)
+__device__ __forceinline__ int wide_blocks(int c) { return c / G_TOK + (c % G_TOK != 0 ? 1 : 0); }
 
 __device__ __forceinline__ bool next_wide(Walk& w, int E, int WB, const int* s_prefix, const int* s_off, WSeg& s) {
   if (!next_unit(w, s.unit, s.kb0, s.kb1)) return false;
