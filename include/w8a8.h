@@ -436,8 +436,13 @@ W8A8_API w8a8_status w8a8_fp8_grouped_matmul(const uint8_t* q, const float* x_sc
  * route -> each token quantised once and copied to its routed rows -> W13 ->
  * SwiGLU + quantisation -> W2 -> combine (as moe_unpermute_combine).
  * x [T,H] bf16, topk_ids int64 [T,k], topk_weights fp32 [T,k], w13 [E,2I,H]
- * (gate rows, then up rows; its scale blocks run over the 2I rows), w2 [E,H,I]
- * -> y [T,H] bf16.  H % 16 == 0, I % 16 == 0.  Device errors as in moe_layer. */
+ * (gate rows, then up rows), w2 [E,H,I] -> y [T,H] bf16.  H % 16 == 0, I % 16
+ * == 0.  Device errors as in moe_layer.
+ * w13's scale blocks run over the 2I joined rows: [E, ceil(2I/128),
+ * ceil(H/128)].  Gate and up matrices that were scaled on their own have other
+ * blocks where I % 128 != 0: pad each half's rows, and w2's columns, with zero
+ * codes to a multiple of 128, and pass that I and the halves' scales one after
+ * the other, [E, 2, ceil(I/128), ceil(H/128)]. */
 W8A8_API size_t moe_fp8_layer_workspace_bytes(int64_t T, int64_t k, int64_t H, int64_t I, int64_t E);
 W8A8_API w8a8_status moe_fp8_layer(const uint16_t* x, const int64_t* topk_ids, const float* topk_weights, int64_t T,
                                    int64_t k, int64_t E, int64_t H, int64_t I, const uint8_t* w13,

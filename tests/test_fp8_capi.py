@@ -97,3 +97,29 @@ def test_workspace_sizes(lib):
     assert lib.w8a8_fp8_grouped_matmul_workspace_bytes(8, 4096, 4096, 4096) <= 76 * 4 * 128 * 256 * 4 + (1 << 14)
     R, H, I = 77 * 3, 384, 208
     assert lib.moe_fp8_layer_workspace_bytes(77, 3, H, I, 12) >= R * (H + 4 * I + I + 2 * H)
+
+
+def test_pad_inner():
+    """Weights laid out for the layer: each half's channels and w2's columns end on whole blocks, in zero codes."""
+    import torch
+    import w8a8_dynamic_quant_gb300 as W
+    E, I, H = 2, 208, 48
+    w13 = torch.randint(0, 127, (E, 2 * I, H), dtype=torch.uint8).view(torch.float8_e4m3fn)
+    w2 = torch.randint(0, 127, (E, H, I), dtype=torch.uint8)
+    s = torch.rand(E, 2, 2, 1)
+    p13, ps, p2 = W.moe_fp8_pad_inner(w13, s, w2)
+    assert p13.dtype == w13.dtype and p2.dtype == w2.dtype and torch.equal(ps, s)
+    assert p13.shape == (E, 512, H) and p2.shape == (E, H, 256) and p13.is_contiguous() and p2.is_contiguous()
+    a, b = p13.view(torch.uint8), w13.view(torch.uint8)
+    assert torch.equal(a[:, :I], b[:, :I]) and torch.equal(a[:, 256:256 + I], b[:, I:])
+    assert not a[:, I:256].any() and not a[:, 256 + I:].any()
+    assert torch.equal(p2[:, :, :I], w2) and not p2[:, :, I:].any()
+    whole = torch.zeros(E, 512, H, dtype=torch.uint8)
+    p13, ps, p2 = W.moe_fp8_pad_inner(whole, s, torch.zeros(E, H, 256, dtype=torch.uint8))
+    assert p13 is whole
+    for bad in ((w13, s[:, 0], w2), (w13[:, :-1], s, w2), (w13, s, w2[:, :, 1:]), (w13, s[:, :, :1], w2)):
+        with pytest.raises(ValueError):
+            W.moe_fp8_pad_inner(*bad)
+    for bad in ((w13.float(), s, w2), (w13, s.double(), w2), (w13, s, w2.short())):
+        with pytest.raises(TypeError):
+            W.moe_fp8_pad_inner(*bad)

@@ -329,6 +329,60 @@ def test_layer_matches_its_parts():
     assert torch.equal(y.view(torch.int16), W.moe_unpermute_combine(yr, pos, wts).view(torch.int16))
 
 
+def quantise_blocks(v):
+    """[E,N,K] binary32 -> (E4M3 [E,N,K], scale per 128 x 128 block)."""
+    E, N, K = v.shape
+    p = torch.nn.functional.pad(v, (0, blocks(K) * 128 - K, 0, blocks(N) * 128 - N)).view(
+        E, blocks(N), 128, blocks(K), 128)
+    s = p.abs().amax((2, 4)) / 448.0
+    q = (p / s[:, :, None, :, None]).to(torch.float8_e4m3fn).view(E, blocks(N) * 128, -1)
+    return q[:, :N, :K].contiguous(), s
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(40, 6, 3, 272, 208), (9, 4, 2, 128, 144), (21, 5, 2, 256, 16),
+                                       (33, 4, 2, 256, 256)])
+def test_layer_from_separately_scaled_halves(T, E, k, H, I):
+    """Gate and up matrices quantised on their own, as checkpoints store them: each half has its own blocks."""
+    g = gen(T + I)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    ids, wts = W.moe_gate_topk(torch.randn(T, E, generator=g, device="cuda"), k, scoring="sigmoid")
+    # channels of very different size, so that a neighbouring block's scale is a wrong one
+    size = torch.exp2(torch.randint(-4, 5, (E, 2 * I, 1), generator=g, device="cuda").float())
+    w = torch.randn(E, 2 * I, H, generator=g, device="cuda") * size
+    (qg, sg), (qu, su) = quantise_blocks(w[:, :I]), quantise_blocks(w[:, I:])
+    q2, s2 = quantise_blocks(torch.randn(E, H, I, generator=g, device="cuda"))
+    q13, s13 = torch.cat([qg, qu], 1), torch.stack([sg, su], 1)
+    w13, w13_scale, w2 = W.moe_fp8_pad_inner(q13, s13, q2)
+    y = W.moe_fp8_layer(x, ids, wts, w13, w13_scale, w2, s2)
+    if I % 128 == 0:
+        assert w13 is q13 and w2 is q2
+    else:
+        with pytest.raises(ValueError, match="moe_fp8_pad_inner"):
+            W.moe_fp8_layer(x, ids, wts, q13, s13, q2, s2)
+    _, _, gl, pos = W.moe_permute_quant(x, None, ids, E)
+    q, s = W.w8a8_fp8_quant(x)
+    src = torch.empty(T * k, dtype=torch.int64, device="cuda")
+    src[pos.view(-1).long()] = torch.arange(T, device="cuda").repeat_interleave(k)
+    xq, xs = q.view(torch.uint8)[src].contiguous(), s[src].contiguous()
+    y13 = torch.cat([W.w8a8_fp8_grouped_matmul(xq, xs, gl, qg, sg), W.w8a8_fp8_grouped_matmul(xq, xs, gl, qu, su)], 1)
+    hq, hs = W.w8a8_fp8_swiglu_quant(y13)
+    yr = W.w8a8_fp8_grouped_matmul(hq, hs, gl, q2, s2)
+    want = W.moe_unpermute_combine(yr, pos, wts)
+    # K is short, so no unit's K is cut in either: the same sums in the same order
+    assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+    ref = torch.zeros(T, H, dtype=torch.float64, device="cuda")
+    xd = q.double() * spread(s, H)
+    for t in range(T):
+        for j in range(k):
+            e = int(ids[t, j])
+            gate = (xd[t] @ (qg[e].double() * spread_w(sg[e], I, H)).t()).to(torch.bfloat16).double()
+            up = (xd[t] @ (qu[e].double() * spread_w(su[e], I, H)).t()).to(torch.bfloat16).double()
+            d, ds = quant_reference((gate * torch.sigmoid(gate) * up).float().view(1, I))
+            o = (d.double() * spread(ds, I))[0] @ (q2[e].double() * spread_w(s2[e], H, I)).t()
+            ref[t] += float(wts[t, j]) * o.to(torch.bfloat16).double()
+    assert float((y.double() - ref).norm() / ref.norm()) < 0.02  # as in test_layer
+
+
 def test_layer_bad_ids_set_the_status():
     T, E, k, H, I = 5, 4, 2, 128, 128
     x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")

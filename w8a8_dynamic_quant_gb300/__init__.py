@@ -29,7 +29,7 @@ __all__ = [
     "w8a8_static_quant_matmul", "w8a8_mx_quant", "w8a8_mx_matmul", "moe_route_workspace_bytes", "moe_permute_quant", "moe_unpermute_combine", "moe_layer_workspace_bytes",
     "moe_layer_workspace_offset", "moe_layer", "moe_gate_topk", "w8a8_fp8_quant", "w8a8_fp8_swiglu_quant",
     "fp8_matmul_workspace_bytes", "w8a8_fp8_matmul", "fp8_grouped_matmul_workspace_bytes",
-    "w8a8_fp8_grouped_matmul", "moe_fp8_layer_workspace_bytes", "moe_fp8_layer",
+    "w8a8_fp8_grouped_matmul", "moe_fp8_layer_workspace_bytes", "moe_fp8_pad_inner", "moe_fp8_layer",
 ]
 
 
@@ -704,11 +704,47 @@ def moe_fp8_layer_workspace_bytes(T: int, k: int, H: int, I: int, E: int) -> int
     return _size("moe_fp8_layer_workspace_bytes", T, k, H, I, E)
 
 
+def moe_fp8_pad_inner(w13: torch.Tensor, w13_scale: torch.Tensor, w2: torch.Tensor):
+    """Weights whose gate and up halves have their own scale blocks, laid out once for moe_fp8_layer where I % 128 != 0.
+
+    E4M3 w13 [E,2I,H] (gate rows, then up rows), its float32 scales [E,2,ceil(I/128),ceil(H/128)] (torch.stack of
+    the two stored ones, dim 1) and E4M3 w2 [E,H,I] -> the same with I rounded up to a multiple of 128: the halves'
+    rows and w2's columns end in zero codes, which add nothing.  w2's scales serve both.  The tensors themselves
+    where I % 128 == 0.  Any device."""
+    E, two, H = _dims(w13, "w13", 3)
+    I, pad = two // 2, -(two // 2) % 128
+    for t, name in ((w13, "w13"), (w2, "w2")):
+        if isinstance(t, torch.Tensor) and t.dtype not in (_E4M3, torch.uint8):
+            raise TypeError(f"{name} must be {_E4M3}, got {t.dtype}")
+    if two % 2 or tuple(_dims(w2, "w2", 3)) != (E, H, I):
+        raise ValueError("w13 must be [E,2I,H] and w2 [E,H,I]")
+    if tuple(_dims(w13_scale, "w13_scale", 4)) != (E, 2, _blocks(I), _blocks(H)):
+        raise ValueError(f"w13_scale has shape {tuple(w13_scale.shape)}, expected {(E, 2, _blocks(I), _blocks(H))}")
+    if w13_scale.dtype is not _F32:
+        raise TypeError(f"w13_scale must be {_F32}, got {w13_scale.dtype}")
+    if pad == 0:
+        return w13, w13_scale, w2
+    # (as bytes: torch pads no float8)
+    p13 = torch.nn.functional.pad(w13.view(torch.uint8).view(E, 2, I, H), (0, 0, 0, pad)).view(E, two + 2 * pad, H)
+    p2 = torch.nn.functional.pad(w2.view(torch.uint8), (0, pad))
+    return p13.view(w13.dtype), w13_scale, p2.view(w2.dtype)
+
+
 def moe_fp8_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor, w13: torch.Tensor,
                   w13_scale: torch.Tensor, w2: torch.Tensor, w2_scale: torch.Tensor,
                   ws: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
     """MoE layer on block-scaled FP8 weights: bf16 x [T,H], topk_ids int64 [T,k] and topk_weights float32 [T,k]
-    (moe_gate_topk), E4M3 w13 [E,2I,H] and w2 [E,H,I] with their float32 block scales -> bf16 y [T,H]."""
+    (moe_gate_topk), E4M3 w13 [E,2I,H] (gate rows, then up rows) and w2 [E,H,I] with float32 block scales -> bf16
+    y [T,H].
+
+    w2_scale [E,ceil(H/128),ceil(I/128)].  w13_scale in one of two forms:
+      [E,2,ceil(I/128),ceil(H/128)]  gate and up scaled on their own, as checkpoints store the two matrices:
+                                     torch.stack([gate_scale, up_scale], 1).  I % 128 == 0; other I are laid out
+                                     for it once by moe_fp8_pad_inner.
+      [E,ceil(2I/128),ceil(H/128)]   blocks over the 2I joined rows (the two forms are the same for I % 128 == 0).
+                                     Where I % 128 != 0 a block spans both halves: two scale arrays made for the
+                                     halves are NOT this form, even where their rows add up to the same number.
+    Keep a workspace (`ws`) over calls: without one every call zero-fills its own."""
     T, H = _dims(x, "x", 2)
     T2, k = _dims(topk_ids, "topk_ids", 2)
     E, two, _ = _dims(w13, "w13", 3)
@@ -722,7 +758,12 @@ def moe_fp8_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.T
     _check(topk_weights, "topk_weights", torch.float32, (T, k), dev)
     _check_e4m3(w13, "w13", (E, two, H), dev)
     _check_e4m3(w2, "w2", (E, H, I), dev)
-    _check(w13_scale, "w13_scale", torch.float32, (E, _blocks(two), _blocks(H)), dev)
+    if isinstance(w13_scale, torch.Tensor) and w13_scale.dim() == 4:
+        if I % 128:
+            raise ValueError(f"w13_scale [E,2,ceil(I/128),...] needs I % 128 == 0 (I = {I}): see moe_fp8_pad_inner")
+        _check(w13_scale, "w13_scale", torch.float32, (E, 2, _blocks(I), _blocks(H)), dev)
+    else:
+        _check(w13_scale, "w13_scale", torch.float32, (E, _blocks(two), _blocks(H)), dev)
     _check(w2_scale, "w2_scale", torch.float32, (E, _blocks(H), _blocks(I)), dev)
     ws = _check_ws(ws, lambda: moe_fp8_layer_workspace_bytes(T, k, H, I, E), dev)
     if y is None:
