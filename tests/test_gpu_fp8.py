@@ -329,6 +329,28 @@ def test_layer_matches_its_parts():
     assert torch.equal(y.view(torch.int16), W.moe_unpermute_combine(yr, pos, wts).view(torch.int16))
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [(600, 4, 2, 16384, 384), (900, 3, 2, 1040, 528)])
+def test_layer_of_many_rows(T, E, k, H, I):
+    """Mean rows of an expert above 64: both contractions on tiles of 256 tokens, W13's units cut where K is long."""
+    g = gen(T + H)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    logits[:, 0] += 1.0  # uneven groups
+    ids, wts = W.moe_gate_topk(logits, k, scoring="sigmoid")
+    w13 = (torch.randn(E, 2 * I, H, generator=g, device="cuda") * 60).to(torch.float8_e4m3fn)
+    w2 = (torch.randn(E, H, I, generator=g, device="cuda") * 60).to(torch.float8_e4m3fn)
+    s13 = torch.rand(E, blocks(2 * I), blocks(H), generator=g, device="cuda") * 1e-4 + 1e-5
+    s2 = torch.rand(E, blocks(H), blocks(I), generator=g, device="cuda") * 1e-3 + 1e-4
+    work = W.workspace(W.moe_fp8_layer_workspace_bytes(T, k, H, I, E))
+    y = W.moe_fp8_layer(x, ids, wts, w13, s13, w2, s2, ws=work)
+    assert W.read_device_status(work) == 0
+    rows = torch.arange(0, T, 37, device="cuda")
+    ref = layer_reference(x[rows], ids[rows], wts[rows], w13, s13, w2, s2)
+    assert float((y[rows].double() - ref).norm() / ref.norm()) < 0.02  # as in test_layer
+    again = W.moe_fp8_layer(x, ids, wts, w13, s13, w2, s2, ws=work)
+    assert torch.equal(y.view(torch.int16), again.view(torch.int16))
+
+
 def quantise_blocks(v):
     """[E,N,K] binary32 -> (E4M3 [E,N,K], scale per 128 x 128 block)."""
     E, N, K = v.shape
