@@ -477,6 +477,49 @@ def test_dense_most_rows():
     assert not bool(y.any())
 
 
+def test_one_workspace_for_calls_of_every_kind():
+    """Calls with few and many tokens, whole and cut units, clusters, groups, and the layer, in turn on one workspace
+    that was zeroed once: each gives the bits that it gives on a workspace of its own."""
+    calls, need = [], 0
+
+    def dense(M, N, K):
+        q, xs, w, ws = problem(M + N + K, M, N, K)
+        return W.fp8_matmul_workspace_bytes(M, N, K), lambda work: W.w8a8_fp8_matmul(q, xs, w, ws, ws=work)
+
+    def grouped(counts, N, K):
+        E, R = len(counts), sum(counts)
+        q, xs, w, ws = problem(R + N + K, R, N, K, E)
+        gl = torch.tensor(counts, dtype=torch.int64, device="cuda")
+        return (W.fp8_grouped_matmul_workspace_bytes(E, R, N, K),
+                lambda work: W.w8a8_fp8_grouped_matmul(q, xs, gl, w, ws, ws=work))
+
+    def layer(T, E, k, H, I):
+        g = gen(T + H)
+        x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+        ids, wts = W.moe_gate_topk(torch.randn(T, E, generator=g, device="cuda"), k)
+        w13 = (torch.randn(E, 2 * I, H, generator=g, device="cuda") * 60).to(torch.float8_e4m3fn)
+        w2 = (torch.randn(E, H, I, generator=g, device="cuda") * 60).to(torch.float8_e4m3fn)
+        s13 = torch.rand(E, blocks(2 * I), blocks(H), generator=g, device="cuda") * 1e-4
+        s2 = torch.rand(E, blocks(H), blocks(I), generator=g, device="cuda") * 1e-4
+        return (W.moe_fp8_layer_workspace_bytes(T, k, H, I, E),
+                lambda work: W.moe_fp8_layer(x, ids, wts, w13, s13, w2, s2, ws=work))
+
+    for nbytes, call in (dense(64, 2048, 7168), dense(50, 9900, 8192), dense(16, 256, 512), dense(2100, 1111, 16384),
+                         dense(700, 2000, 1536), grouped([3, 0, 17, 1, 64], 577, 16384), grouped([1] * 33, 200, 400),
+                         grouped([130, 1, 0, 257, 40, 2], 577, 16384), layer(9, 8, 3, 272, 144),
+                         layer(600, 4, 2, 16384, 384)):
+        fresh = W.workspace(nbytes)
+        calls.append((call, call(fresh).view(torch.int16)))
+        assert W.read_device_status(fresh) == 0
+        need = max(need, nbytes)
+    shared = W.workspace(need)
+    for step in (1, 3, 7):  # three orders, in which every call follows different ones
+        for i in range(len(calls)):
+            call, want = calls[i * step % len(calls)]
+            assert torch.equal(call(shared).view(torch.int16), want)
+    assert W.read_device_status(shared) == 0
+
+
 @pytest.mark.parametrize("M,N,K", [(48, 1100, 4096), (300, 1100, 4096), (700, 2000, 1536)])
 def test_matmul_in_a_graph(M, N, K):
     """Captured and replayed on changed inputs: nothing of a call is left on the host, the workspace stays ready."""
