@@ -74,10 +74,10 @@ def weight_read_bound_ms(active_params: float, bytes_per_param: float, n_gpus: i
 KERNEL_SOURCES = {
     "dynamic_quant": ["quant.cu", "common.cuh", "kernels.cuh"],
     "quant_matmul": ["gemm_reg.cu", "gemm_dec.cu", "gemm_tc.cu", "gemm_tcp.cu", "tc_common.cuh", "capi.cu",
-                     "common.cuh", "kernels.cuh"],
+                     "capi_common.cuh", "common.cuh", "kernels.cuh"],
     "moe_layer": ["gemm_reg.cu", "gemm_tc.cu", "gemm_tcp.cu", "tc_common.cuh", "quant.cu", "route.cu", "capi.cu",
-                  "common.cuh", "kernels.cuh"],
-    "mx_matmul": ["mx.cu", "mx_tc.cu", "tc_common.cuh", "capi.cu", "common.cuh", "kernels.cuh"],
+                  "capi_common.cuh", "common.cuh", "kernels.cuh"],
+    "mx_matmul": ["mx.cu", "mx_tc.cu", "tc_common.cuh", "capi.cu", "capi_common.cuh", "common.cuh", "kernels.cuh"],
 }
 
 

@@ -4,7 +4,7 @@
 
 #include <atomic>
 
-#include "kernels.cuh"
+#include "fp8.cuh"
 #include "tc_common.cuh"
 
 namespace w8a8 {

@@ -19,7 +19,7 @@
 // the tail short (measured, back to back: 8192 x 4096 18.5 us, 5.5 TB/s, against
 // 20.3 us with 256 threads in eight waves; SwiGLU of 32768 x 2048 54.6 us, 6.2 TB/s,
 // against 58.7 us).  Two blocks a thread in flight gained nothing.
-#include "kernels.cuh"
+#include "fp8.cuh"
 
 namespace w8a8 {
 

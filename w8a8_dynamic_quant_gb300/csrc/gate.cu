@@ -29,7 +29,7 @@
 // small ones the chain of k choices (128 tokens, 256 experts in 8 groups of which
 // 4 stay, top-8: 3.3 us a launch; 16384 tokens, 64 experts, top-8: 5.8 us, where
 // the reads and writes alone would take 0.5).
-#include "kernels.cuh"
+#include "fp8.cuh"
 
 namespace w8a8 {
 
