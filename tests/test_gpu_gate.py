@@ -155,6 +155,14 @@ def test_many_tokens(T, E, k, n_group, topk_group, scoring):
         np.testing.assert_allclose(w.cpu().numpy()[rows], rw, rtol=64 * 2.0 ** -24, atol=0)
 
 
+@pytest.mark.parametrize("T,E,k,n_group,topk_group", [
+    (16385, 128, 16, 16, 9), (16390, 100, 8, 1, 1), (16384, 72, 9, 1, 1)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_more_tokens(T, E, k, n_group, topk_group, scoring):
+    """The batches from which on 65 to 128 experts go to 16 lanes a token."""
+    test_many_tokens(T, E, k, n_group, topk_group, scoring)
+
+
 def test_empty_and_other_stream():
     ids, w = W.moe_gate_topk(torch.empty(0, 16, device="cuda"), 4)
     assert ids.shape == (0, 4) and w.shape == (0, 4)

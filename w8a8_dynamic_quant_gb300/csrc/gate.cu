@@ -24,11 +24,12 @@
 // L lanes per token (32; 8 or 16 for many tokens of few experts); lane l holds
 // the experts [l * P, l * P + P), P = the experts per lane.  A choice is the
 // maximum of the lanes' best keys (as order-preserving integers) at the lowest
-// lane holding it.  Traffic is one read of the logits and 12 bytes per choice;
-// what bounds large batches is the issue of some hundred instructions a token,
-// small ones the chain of k choices (128 tokens, 256 experts in 8 groups of which
-// 4 stay, top-8: 3.3 us a launch; 16384 tokens, 64 experts, top-8: 5.8 us, where
-// the reads and writes alone would take 0.5).
+// lane holding it.  Traffic is one read of the logits and 12 bytes per choice.
+// What bounds large batches is the issue of about 190 warp instructions a token
+// (65536 tokens, 64 experts, top-8: 13.8 us, issuing in 72 % of the SMs' active
+// cycles); a wave of CTAs or less its latency (16384 such tokens 6.1 us at 53 %,
+// top-2 of them 5.2, the reads and writes alone 0.5); small batches the chain of
+// k choices (128 tokens, 256 experts in 8 groups of which 4 stay, top-8: 3.2 us).
 #include "fp8.cuh"
 
 namespace w8a8 {
@@ -367,17 +368,19 @@ cudaError_t launch_gate(const void* logits, bool bf16, int64_t T, int E, const f
                         cudaStream_t stream) {
   if (T == 0) return cudaSuccess;
   const GateArgs a{0, logits, bias, T, E, k, n_group, topk_group, top2, renorm, scale, ids, weights};
-  // Many tokens of few experts: 8 or 16 lanes a token, so that the steps of a choice serve four or two tokens.  Softmax,
-  // top-8, without groups, against a warp a token: E = 64 at 1024 tokens 2.6 us both, 2048 2.8 against 4.4, 16384 5.8
-  // against 8.3, 65536 14.1 against 28.6; E = 128 at 4096 tokens 5.7 against 5.3, 16384 8.7 against 10.0, 65536 28.5
-  // against 34.6.  (E = 256 in 16 lanes of 16: 57.8 us at 65536, against 47.)  Groups have to be whole lanes.
+  // Many tokens of few experts: 8 or 16 lanes a token, so that the steps of a choice serve four or two tokens.  Softmax
+  // without groups, top-8 (top-2), against a warp a token: E = 32 at 2048 tokens 2.4 (2.0) us against 3.7 (2.9), 16384
+  // 4.8 (3.8) against 6.1 (5.4); E = 64 at 2048 3.2 (2.8) against 4.9 (3.5), 16384 6.1 (5.2) against 8.3 (6.0), 65536
+  // 13.8 (11.7) against 28.6 (19.1); E = 128 at 8192 6.6 (5.3) against 5.8 (4.2), 16384 8.5 (6.8) against 9.8 (6.7),
+  // 65536 27.9 (22.2) against 33.9 (22.7).  (E = 256 in 16 lanes of 16: 57.8 us at 65536, against 47.)  Groups have to
+  // be whole lanes.
   const auto whole = [=](int P) {
     const int gs = E / n_group, lanes = gs / P;
     return topk_group == n_group || (lanes * P == gs && (lanes & (lanes - 1)) == 0);
   };
   if (T >= 2048 && E <= 32 && k <= 8 && whole(4)) return launch_p<8, 4>(a, bf16, sigmoid, stream);
   if (T >= 2048 && E > 32 && E <= 64 && k <= 8 && whole(8)) return launch_p<8, 8>(a, bf16, sigmoid, stream);
-  if (T >= 8192 && E > 64 && E <= 128 && k <= 16 && whole(8)) return launch_p<16, 8>(a, bf16, sigmoid, stream);
+  if (T >= 16384 && E > 64 && E <= 128 && k <= 16 && whole(8)) return launch_p<16, 8>(a, bf16, sigmoid, stream);
   // experts per lane: as few as hold E, so that common counts (96, 160, 192, 384 and the powers of two) fill every lane
   // and their groups are whole lanes
   const int P = (E + 31) / 32;
