@@ -350,8 +350,9 @@ W8A8_API int64_t moe_layer_workspace_offset(int64_t T, int64_t k, int64_t H, int
 /* Expert router: router logits -> topk_ids and topk_weights, as moe_layer   */
 /* and moe_fp8_layer take them.  Per token, over E experts:                  */
 /*   live    an expert whose logit is above -inf (-inf or NaN masks it)      */
-/*   s       sigmoid: 1 / (1 + exp(-l)); softmax: exp(l - m) / S over the    */
-/*           live experts (m their largest logit, S the sum)                 */
+/*   s       sigmoid: 1 / (1 + exp(-l)), in binary32 operations (so 0 for    */
+/*           l below about -88.7); softmax: exp(l - m) / S over the live     */
+/*           experts (m their largest logit, S the sum)                      */
 /*   key     s + bias[e] where a bias is given, else s; masked experts (and  */
 /*           keys of -inf or NaN) rank below all others                      */
 /*   groups  n_group runs of E / n_group experts; a group's score is its     */

@@ -641,7 +641,7 @@ def w8a8_fp8_matmul(q: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_s
                     bias: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                     y: Optional[torch.Tensor] = None):
     """E4M3 q [M,K] with x_scale [M, ceil(K/128)] x E4M3 w [N,K] with w_scale [ceil(N/128), ceil(K/128)]
-    (+ bf16 bias [N]) -> bf16 y [M,N]."""
+    (+ bf16 bias [N]) -> bf16 y [M,N].  Keep a workspace (`ws`) over calls: without one every call zero-fills its own."""
     M, K = _dims(q, "q", 2)
     N = _dims(w, "w", 2)[0]
     dev, kb = q.get_device(), (K + 127) // 128
@@ -674,7 +674,8 @@ def w8a8_fp8_grouped_matmul(q: torch.Tensor, x_scale: torch.Tensor, group_list: 
                             w_scale: torch.Tensor, ws: Optional[torch.Tensor] = None,
                             y: Optional[torch.Tensor] = None):
     """E4M3 q [R,K] (rows grouped by expert) with x_scale [R, ceil(K/128)] x E4M3 w [E,N,K] with w_scale
-    [E, ceil(N/128), ceil(K/128)] -> bf16 y [R,N]."""
+    [E, ceil(N/128), ceil(K/128)] -> bf16 y [R,N].  Keep a workspace (`ws`) over calls: without one every call
+    zero-fills its own."""
     R, K = _dims(q, "q", 2)
     E, N, K2 = _dims(w, "w", 3)
     dev, kb = q.get_device(), (K + 127) // 128

@@ -39,14 +39,18 @@
 // that arrives last at a unit adds the pieces in the order of K and writes the
 // result: no order of arrival changes a bit, and no warp waits for another.
 // The cluster's sum costs about 1.2 us, a cut unit's 5 and more (64 x 2048 x 7168:
-// 10.1 us in clusters of 6 pairs, 13.1 us in seven parts through the workspace), so
+// 10.2 us in clusters of 6 pairs, 13.1 us in seven parts through the workspace), so
 // units are cut only where they are few and long.
 //
-// What bounds it.  Many experts with few rows: the weight stream (256 experts of
-// 4096 x 7168, four rows each: 1041 us, 7.2 TB/s).  One small layer: latency.
+// What bounds it.  Many experts with few rows: the weight stream (1024 rows over
+// 256 experts of 4096 x 7168: 1040 us, 7.1 TB/s).  One small layer: latency.
 // 64 x 2048 x 7168 could stream its weights in 2.3 us; launch and the first
-// tiles' way take about 4 (16 x 256 x 512: 4.3 us in all), ten blocks a pair
+// tiles' way take about 4 (16 x 256 x 512: 4.5 us in all), ten blocks a pair
 // in turn and the sum over the cluster the rest.
+//
+// Registers: 159 to 168 of the 168 that 384 threads may have; with tiles of 128
+// tokens ptxas reports 24 bytes spilled (32 and 64: none).  That is a few values a
+// thread, and these tiles are bound by the weight stream or by latency.
 //
 // Every mbarrier wait is bounded (2 s): on expiry the CTA sets
 // W8A8_ERR_DEVICE_TIMEOUT, lets in-flight copies land, frees TMEM and returns.

@@ -13,9 +13,10 @@
 // What bounds it.  Per 128-deep block a pair's MMAs take 512 cycles; an epilogue
 // warp's round -- barrier, tensor-memory loads of 128 columns, 128 sums, release --
 // takes about 660, and the end of a tile about 2200 (sums to bf16, shared memory, TMA)
-// in which the MMAs are at most two blocks ahead.  On 8192 x 14336 x 4096, 338 us
-// (2.85 PFLOP/s, 0.75 of twice the measured BF16 burst; called without a pause, under
-// the power cap, 368):
+// in which the MMAs are at most two blocks ahead.  On 8192 x 14336 x 4096, 332 us in
+// a burst (2.90 PFLOP/s, 0.76 of twice the measured BF16 burst) and 371 without a
+// pause, under the power cap (0.68).  What was kept and what not, each beside the
+// step before it:
 //   - few, wide rounds: 2 x 128 channels a tile 392 us, 2 x 96 452 us, one part of
 //     160 with three accumulators 486 us (before the steps below); sixteen epilogue
 //     warps of 64 channels 365 us against 357; one barrier for two blocks 410 us: it
@@ -26,6 +27,8 @@
 //   - registers: the segment comes with its first scales from the warp that walks
 //     ahead, the walk is worked out again where it is seldom needed, and both halves
 //     of a tile are staged at once at the price of the fifth stage (355 -> 338 us).
+//     ptxas still reports 28 bytes a thread spilled and 128 loaded, in a kernel whose
+//     epilogue holds 128 sums and 48 buffer words of 216 registers.
 //
 // Warp roles (384 threads, one CTA per SM):
 //   warp 0       TMA producer
