@@ -16,9 +16,10 @@
 // Memory-bound: 2 (plain) or 4 (SwiGLU) bytes read and 1 written per value,
 // 1/32 byte of scale.  Eight lanes own a block, 16 values each; the block's
 // maximum meets through three shuffles.  CTAs of 128 threads in many waves keep
-// the tail short (measured, back to back: 8192 x 4096 18.5 us, 5.5 TB/s, against
-// 20.3 us with 256 threads in eight waves; SwiGLU of 32768 x 2048 54.6 us, 6.2 TB/s,
-// against 58.7 us).  Two blocks a thread in flight gained nothing.
+// the tail short (measured, back to back: 8192 x 4096 18.2 us, 5.6 TB/s, where 256
+// threads in eight waves took 20.3; SwiGLU of 32768 x 2048 54.6 us, 6.2 TB/s, and
+// with a shorter sigmoid 52.9 against 58.7 so).  Two blocks a thread in flight
+// gained nothing.
 #include "fp8.cuh"
 
 namespace w8a8 {
