@@ -480,6 +480,41 @@ W8A8_API w8a8_status w8a8_quant_matmul_noalloc(const int8_t* q, const float* x_s
 W8A8_API w8a8_status w8a8_quant_matmul_noalloc_status(w8a8_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Root-mean-square norm with an 8-bit output: what stands between two       */
+/* quantised products of a layer, in one pass over the rows.                 */
+/*   r = bf16(x + residual)  (binary32 sum; r = x where residual is NULL)    */
+/*   g = RN(1 / sqrt(S / K + eps)), S the sum of r^2 over the row rounded    */
+/*       once to binary32                                                    */
+/*   v = (r * g) * weight    (binary32)                                      */
+/* and v quantised as the quantiser of the same format quantises bf16 rows:  */
+/* codes and scales are exact functions of v, and v of S.  x, residual       */
+/* [M,K] bf16; weight [K] bf16, or fp32 with W8A8_NORM_WEIGHT_F32;           */
+/* residual_out [M,K] bf16 takes r (required with a residual, NULL without;  */
+/* it may be x or residual itself); y [M,K] bf16 takes bf16(v), or is NULL.  */
+/* eps > 0 and finite.  K % 16 == 0, tensors but the fp32 scales 16-byte     */
+/* aligned.  No other two of the tensors may overlap.                        */
+/* A row holding a NaN is NaN throughout, one whose S is infinite has g = 0; */
+/* NaNs then quantise as in the format's quantiser.                          */
+/* ------------------------------------------------------------------------ */
+
+#define W8A8_NORM_WEIGHT_F32 1u /* weight is fp32 */
+
+/* int8 q [M,K], one fp32 scale a row: s = max |v| / 127, q = clamp(rint(v / s), -127, 127), ties to even, NaN -> 0. */
+W8A8_API w8a8_status w8a8_rms_norm_quant(const uint16_t* x, const uint16_t* residual, const void* weight, int64_t M,
+                                         int64_t K, float eps, uint32_t flags, uint16_t* residual_out, uint16_t* y,
+                                         int8_t* q, float* scale, w8a8_stream_t stream);
+
+/* E4M3 q [M,K], scale [M, ceil(K/128)] fp32, as w8a8_fp8_quant. */
+W8A8_API w8a8_status w8a8_fp8_rms_norm_quant(const uint16_t* x, const uint16_t* residual, const void* weight,
+                                             int64_t M, int64_t K, float eps, uint32_t flags, uint16_t* residual_out,
+                                             uint16_t* y, uint8_t* q, float* scale, w8a8_stream_t stream);
+
+/* MXFP8: E4M3 q [M,K], scale [M, K/32] E8M0 bytes, as w8a8_mx_quant.  K % 32 == 0. */
+W8A8_API w8a8_status w8a8_mx_rms_norm_quant(const uint16_t* x, const uint16_t* residual, const void* weight,
+                                            int64_t M, int64_t K, float eps, uint32_t flags, uint16_t* residual_out,
+                                            uint16_t* y, uint8_t* q, uint8_t* scale, w8a8_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Device status                                                             */
 /* ------------------------------------------------------------------------ */
 

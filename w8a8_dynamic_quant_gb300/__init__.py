@@ -30,6 +30,7 @@ __all__ = [
     "moe_layer_workspace_offset", "moe_layer", "moe_gate_topk", "w8a8_fp8_quant", "w8a8_fp8_swiglu_quant",
     "fp8_matmul_workspace_bytes", "w8a8_fp8_matmul", "fp8_grouped_matmul_workspace_bytes",
     "w8a8_fp8_grouped_matmul", "moe_fp8_layer_workspace_bytes", "moe_fp8_pad_inner", "moe_fp8_layer",
+    "w8a8_rms_norm_quant", "w8a8_fp8_rms_norm_quant", "w8a8_mx_rms_norm_quant",
 ]
 
 
@@ -775,6 +776,75 @@ def moe_fp8_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.T
           w13.data_ptr(), w13_scale.data_ptr(), w2.data_ptr(), w2_scale.data_ptr(), ws.data_ptr(), ws.numel(),
           y.data_ptr())
     return y
+
+
+def _rms_norm(name, x, weight, eps, residual, want_y, q, scale, residual_out, y, q_dtype, s_dtype, s_cols):
+    M, K = _dims(x, "x", 2)
+    dev = x.get_device()
+    if not (dev >= 0 and x.dtype is _BF16 and x.is_contiguous()):
+        _check(x, "x", _BF16, (M, K), dev)
+    f32 = type(weight) is _Tensor and weight.dtype is _F32
+    _check(weight, "weight", _F32 if f32 else _BF16, (K,), dev)
+    if residual is not None:
+        _check(residual, "residual", _BF16, (M, K), dev)
+        if residual_out is None:
+            residual_out = _empty((M, K), dtype=_BF16, device=x.device)
+        else:
+            _check(residual_out, "residual_out", _BF16, (M, K), dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if y is not None:
+        _check(y, "y", _BF16, (M, K), dev)
+    elif want_y:
+        y = _empty((M, K), dtype=_BF16, device=x.device)
+    if q is None:
+        q = _empty((M, K), dtype=q_dtype, device=x.device)
+    elif q_dtype is _E4M3:
+        _check_e4m3(q, "q", (M, K), dev)
+    else:
+        _check(q, "q", q_dtype, (M, K), dev)
+    shape = (M,) if s_cols is None else (M, -(-K // s_cols))
+    if scale is None:
+        scale = _empty(shape, dtype=s_dtype, device=x.device)
+    else:
+        _check(scale, "scale", s_dtype, shape, dev)
+    _call(name, dev, x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), M, K, eps,
+          _capi.NORM_WEIGHT_F32 if f32 else 0, None if residual_out is None else residual_out.data_ptr(),
+          None if y is None else y.data_ptr(), q.data_ptr(), scale.data_ptr())
+    return q, scale, residual_out, y
+
+
+def w8a8_rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                        residual: Optional[torch.Tensor] = None, want_y: bool = False,
+                        q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                        residual_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
+    """Root-mean-square norm of bf16 x [M,K] (+ residual [M,K]) with weight [K] (bf16 or float32), quantised:
+    (int8 q [M,K], float32 scale [M], r, y).
+
+    r = bf16(x + residual), or None without a residual; the norm is of r.  y: the norm in bf16 where want_y (or a
+    tensor `y`) asks for it, else None.  residual_out may be x or residual itself: the residual stream in place."""
+    return _rms_norm("w8a8_rms_norm_quant", x, weight, eps, residual, want_y, q, scale, residual_out, y, torch.int8,
+                     _F32, None)
+
+
+def w8a8_fp8_rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                            residual: Optional[torch.Tensor] = None, want_y: bool = False,
+                            q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                            residual_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
+    """w8a8_rms_norm_quant with block-scaled FP8 codes: (float8_e4m3fn q [M,K], float32 scale [M, ceil(K/128)], r, y),
+    the operands of w8a8_fp8_matmul."""
+    return _rms_norm("w8a8_fp8_rms_norm_quant", x, weight, eps, residual, want_y, q, scale, residual_out, y, _E4M3,
+                     _F32, 128)
+
+
+def w8a8_mx_rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                           residual: Optional[torch.Tensor] = None, want_y: bool = False,
+                           q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                           residual_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
+    """w8a8_rms_norm_quant with MXFP8 codes (K % 32 == 0): (uint8 E4M3 codes q [M,K], uint8 E8M0 scales [M,K/32], r, y),
+    the operands of w8a8_mx_matmul."""
+    return _rms_norm("w8a8_mx_rms_norm_quant", x, weight, eps, residual, want_y, q, scale, residual_out, y,
+                     torch.uint8, torch.uint8, 32)
 
 
 def read_device_status(ws: torch.Tensor) -> int:

@@ -57,6 +57,8 @@ SIGNATURES = {
     "w8a8_fp8_grouped_matmul": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
     "moe_fp8_layer_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
     "moe_fp8_layer": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    **{n: (_int, [_vp, _vp, _vp, _i64, _i64, ctypes.c_float, _u32, _vp, _vp, _vp, _vp, _vp])
+       for n in ("w8a8_rms_norm_quant", "w8a8_fp8_rms_norm_quant", "w8a8_mx_rms_norm_quant")},
     "w8a8_quant_matmul_noalloc": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp]),
     "w8a8_quant_matmul_noalloc_status": (_int, [_vp]),
     "w8a8_read_device_status": (_int, [_vp, _vp]),
@@ -72,6 +74,7 @@ W8A8_OK, W8A8_ERR_WORKSPACE, W8A8_ERR_DEVICE_TIMEOUT, W8A8_ERR_PACKED = 0, 4, 6,
 PACK_GATE_UP = 1
 GATE_SIGMOID, GATE_GROUP_TOP2, GATE_RENORM, GATE_BF16 = 1, 2, 4, 8
 PACK_F16 = 2
+NORM_WEIGHT_F32 = 1
 
 _lib = None
 _lock = threading.Lock()

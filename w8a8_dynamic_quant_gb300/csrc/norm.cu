@@ -1,0 +1,433 @@
+// norm.cu -- root-mean-square norm of BF16 rows, with the residual's addition before it and the 8-bit quantisation
+// behind it in one pass: what stands between two quantised products of a layer.
+//
+//   r = bf16(x + residual)                (binary32 sum; r = x without a residual)
+//   g = RN(1 / sqrt(S / K + eps)),  S = sum_k r_k^2
+//   v = (r * g) * w                       (binary32, kept so into the quantisation: one rounding to 8 bits)
+//   INT8   s = max |v| / 127 a row,       q = rint(v / s)                 (as quant.cu)
+//   FP8    s = max |v| / 448 per 128,     q = E4M3(v / s)                 (as fp8_quant.cu)
+//   MXFP8  2^(floor(log2 max |v|) - 8) per 32, q = E4M3(v / 2^...)        (as mx.cu)
+//
+// r and bf16(v) are written where they are asked for.
+//
+// The sum decides every code of a row, so its bits must not hang on the order of the additions: squares of bf16 are
+// exact in binary32, and they are added with their rounding errors carried in a second word (Knuth's TwoSum), in the
+// threads and in the reductions.  S is the exact sum rounded once, up to a relative 2^-40 or so; every later step is one
+// rounding per element.  So the codes are those of the formula with a 64-bit sum, whatever the launch shape.
+//
+// Bound by memory: 2 bytes in (4 with a residual), 1 out (3 with it, 2 more for y).  A row lives in the registers of G
+// warps, CH chunks of 8 values a thread; two meetings of the group (the sum; INT8 the maximum), which other rows'
+// loads hide.
+#include "norm.cuh"
+
+namespace w8a8 {
+
+namespace {
+
+enum Form : int { F_INT8 = 0, F_FP8 = 1, F_MX = 2 };
+
+constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: y + kMagic holds rint(y), ties to even, in its low bits
+
+__device__ __forceinline__ uint64_t pk(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void upk(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+// Paired binary32 operations: each half is the correctly rounded operation of its own operands.
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// s + p in s, what its rounding lost added to c (Knuth, "The Art of Computer Programming" 2, 4.2.2).
+__device__ __forceinline__ void two_sum2(uint64_t& s, uint64_t& c, uint64_t p) {
+  const uint64_t t = add2(s, p), b = sub2(t, s);
+  c = add2(c, add2(sub2(s, sub2(t, b)), sub2(p, b)));
+  s = t;
+}
+__device__ __forceinline__ void two_sum(float& s, float& c, float p) {
+  const float t = __fadd_rn(s, p), b = __fsub_rn(t, s);
+  c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(p, b)));
+  s = t;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 16 bytes read once.  Not the read-only path: residual_out may be x or residual itself.
+__device__ __forceinline__ uint4 ld_once(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+  return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// RN(v / s) of two values from nv = -v, s and nrs = -RN(1 / s).  Markstein ("Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990): a quotient within one unit in the last place, corrected by its exact remainder times a
+// correctly rounded reciprocal, is the correctly rounded quotient.  The product v * rs may be a little more than a unit
+// off, hence two corrections.  s in [2^-100, 2^100]; values so small that their remainder underflows have code 0.
+// (From -v, so that -0 stays -0: its remainder 0 times -rs, added to -0, is -0.)
+__device__ __forceinline__ uint64_t quotient2(uint64_t nv, uint64_t nrs, uint64_t s) {
+  uint64_t y = mul2(nv, nrs);
+  y = fma2(fma2(y, s, nv), nrs, y);
+  return fma2(fma2(y, s, nv), nrs, y);
+}
+__device__ __forceinline__ bool plain_scale(float s) { return s >= 0x1p-100f && s <= 0x1p100f; }
+
+// The 8 int8 codes of a chunk of -v.  slow: the row holds a NaN (code 0) or its scale is out of quotient2's range.
+__device__ __forceinline__ uint2 codes_int8(const uint64_t (&nv)[4], float s, float rs, bool slow) {
+  uint32_t u[8];
+  if (!slow) {
+    const uint64_t rs2 = pk(-rs, -rs), s2 = pk(s, s), mg = pk(kMagic, kMagic);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      upk(add2(quotient2(nv[i], rs2, s2), mg), lo, hi);
+      u[2 * i] = __float_as_uint(lo);
+      u[2 * i + 1] = __float_as_uint(hi);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float f[2];
+      upk(nv[i], f[0], f[1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // s = 0: every value is zero or a NaN; s = inf: quotients 0 or NaN
+        const int r = s > 0.0f ? __float2int_rn(__fdiv_rn(-f[h], s)) : 0;  // a NaN converts to 0
+        u[2 * i + h] = static_cast<uint32_t>(max(-127, min(127, r)));
+      }
+    }
+  }
+  return make_uint2(__byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(u[4], u[5], 0x0040), __byte_perm(u[6], u[7], 0x0040), 0x5410));
+}
+
+// The 8 E4M3 codes of a chunk of -v under scale s.
+__device__ __forceinline__ uint2 codes_fp8(const uint64_t (&nv)[4], float s) {
+  uint32_t c[4];
+  if (plain_scale(s)) {
+    const float rs = __frcp_rn(s);
+    const uint64_t rs2 = pk(-rs, -rs), s2 = pk(s, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      upk(quotient2(nv[i], rs2, s2), lo, hi);
+      c[i] = e4m3x2_of(lo, hi);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      upk(nv[i], a, b);
+      a = -a;
+      b = -b;
+      // a block of zeros: +0, or NaN for a NaN value
+      const float lo = s == 0.0f ? __fadd_rn(__fmul_rn(a, 0.0f), 0.0f) : __fdiv_rn(a, s);
+      const float hi = s == 0.0f ? __fadd_rn(__fmul_rn(b, 0.0f), 0.0f) : __fdiv_rn(b, s);
+      c[i] = e4m3x2_of(lo, hi);
+    }
+  }
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+// Group grp's barrier of 32 G threads (ids as immediates: a register id would reserve all sixteen).
+template <int G>
+__device__ __forceinline__ void meet(int grp) {
+  switch (grp) {
+    case 0: asm volatile("bar.sync 1, %0;" ::"n"(32 * G) : "memory"); break;
+    case 1: asm volatile("bar.sync 2, %0;" ::"n"(32 * G) : "memory"); break;
+    case 2: asm volatile("bar.sync 3, %0;" ::"n"(32 * G) : "memory"); break;
+    default: asm volatile("bar.sync 4, %0;" ::"n"(32 * G) : "memory"); break;
+  }
+}
+
+// max of a group's values, the same in every thread; KeepNaN: a NaN among them is the result, else it is passed over.
+template <bool KeepNaN, int G>
+__device__ __forceinline__ float group_max(float m, float* red, int grp, int w, int lane) {
+  const auto op = [](float a, float b) { return KeepNaN ? max_nan(a, b) : fmaxf(a, b); };
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = op(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if constexpr (G > 1) {
+    if (lane == 0) red[w] = m;
+    meet<G>(grp);
+    m = red[lane % G];
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) m = op(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+  return m;
+}
+
+// FORM: the output.  A group of G warps holds one row, CH chunks of 8 values a thread.
+template <int FORM, int CH, int G>
+__global__ void __launch_bounds__(G > 8 ? 32 * G : 256) norm_quant_kernel(const NormArgs a) {
+  constexpr int kWarps = G > 8 ? G : 8;
+  constexpr int NG = kWarps / G;
+  __shared__ float red_s[kWarps], red_c[kWarps], red_m[kWarps], red_n[kWarps];
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int warp = static_cast<int>(threadIdx.x >> 5);
+  const int grp = warp / G, w = warp % G;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * NG + grp;
+  const int nchunk = a.K / 8;
+  const int t = w * 32 + lane;
+  const bool f32w = a.weight_f32;
+  pdl_wait();
+  if (row >= a.M) return;  // whole groups: their barriers are their own
+
+  const int64_t at = row * a.K;
+  uint4 v[CH];
+  {
+    const uint4* x = reinterpret_cast<const uint4*>(a.x + at);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) v[c] = t + 32 * G * c < nchunk ? ld_once(x + t + 32 * G * c) : zero;
+    if (a.residual != nullptr) {
+      const uint4* p = reinterpret_cast<const uint4*>(a.residual + at);
+      uint4 res[CH];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) res[c] = t + 32 * G * c < nchunk ? ld_once(p + t + 32 * G * c) : zero;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        uint32_t* p0 = &v[c].x;
+        const uint32_t q0[4] = {res[c].x, res[c].y, res[c].z, res[c].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          p0[i] = f32x2_to_bf16x2_bits(
+              __fadd_rn(__uint_as_float(p0[i] << 16), __uint_as_float(q0[i] << 16)),
+              __fadd_rn(__uint_as_float(p0[i] & 0xffff0000u), __uint_as_float(q0[i] & 0xffff0000u)));
+        if (t + 32 * G * c < nchunk) reinterpret_cast<uint4*>(a.residual_out + at)[t + 32 * G * c] = v[c];
+      }
+    }
+  }
+
+  // the sum of squares in two words, over the thread, the warp and the group
+  uint64_t s2 = 0ull, c2 = 0ull;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const uint32_t q0[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t r = pk(__uint_as_float(q0[i] << 16), __uint_as_float(q0[i] & 0xffff0000u));
+      two_sum2(s2, c2, mul2(r, r));
+    }
+  }
+  float s, e, s_hi, e_hi;
+  upk(s2, s, s_hi);
+  upk(c2, e, e_hi);
+  two_sum(s, e, s_hi);
+  e = __fadd_rn(e, e_hi);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float so = __shfl_xor_sync(0xffffffffu, s, o), eo = __shfl_xor_sync(0xffffffffu, e, o);
+    two_sum(s, e, so);
+    e = __fadd_rn(e, eo);
+  }
+  if constexpr (G > 1) {
+    if (lane == 0) {
+      red_s[warp] = s;
+      red_c[warp] = e;
+    }
+    meet<G>(grp);
+    s = red_s[grp * G + lane % G];
+    e = red_c[grp * G + lane % G];
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) {
+      const float so = __shfl_xor_sync(0xffffffffu, s, o), eo = __shfl_xor_sync(0xffffffffu, e, o);
+      two_sum(s, e, so);
+      e = __fadd_rn(e, eo);
+    }
+  }
+  // (a sum past the largest binary32 value is infinite, and what it lost is no number)
+  const float sum = fabsf(s) <= 3.4028234663852886e38f ? __fadd_rn(s, e) : s;
+  const float g = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(a.K)), a.eps));
+
+  // -v = (r * g) * -w
+  uint64_t f[CH][4];
+  const uint64_t g2 = pk(g, g);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int idx = t + 32 * G * c;
+    const uint32_t q0[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+    uint64_t wt[4] = {0ull, 0ull, 0ull, 0ull};
+    if (idx < nchunk) {
+      if (f32w) {
+        const float4 w0 = reinterpret_cast<const float4*>(a.weight)[2 * idx];
+        const float4 w1 = reinterpret_cast<const float4*>(a.weight)[2 * idx + 1];
+        wt[0] = pk(-w0.x, -w0.y);
+        wt[1] = pk(-w0.z, -w0.w);
+        wt[2] = pk(-w1.x, -w1.y);
+        wt[3] = pk(-w1.z, -w1.w);
+      } else {
+        const uint4 wb = reinterpret_cast<const uint4*>(a.weight)[idx];
+        const uint32_t w4[4] = {wb.x ^ 0x80008000u, wb.y ^ 0x80008000u, wb.z ^ 0x80008000u, wb.w ^ 0x80008000u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wt[i] = pk(__uint_as_float(w4[i] << 16), __uint_as_float(w4[i] & 0xffff0000u));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[c][i] = mul2(mul2(pk(__uint_as_float(q0[i] << 16), __uint_as_float(q0[i] & 0xffff0000u)), g2), wt[i]);
+    if (idx >= nchunk) {  // (0 * inf above)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[c][i] = 0ull;
+    }
+    if (a.y != nullptr && idx < nchunk) {
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        upk(f[c][i], lo, hi);
+        o[i] = f32x2_to_bf16x2_bits(lo, hi) ^ 0x80008000u;
+      }
+      reinterpret_cast<uint4*>(a.y + at)[idx] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+
+  if constexpr (FORM == F_INT8) {
+    float m = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        upk(f[c][i], lo, hi);
+        m = max_nan(m, max_nan(fabsf(lo), fabsf(hi)));
+      }
+    m = group_max<true, G>(m, red_m + grp * G, grp, w, lane);
+    const bool nan = m != m;
+    if (nan) {  // rare, the whole group together: the maximum over the other values
+      m = 0.0f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float lo, hi;
+          upk(f[c][i], lo, hi);
+          m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));
+        }
+      m = group_max<false, G>(m, red_n + grp * G, grp, w, lane);
+    }
+    const float sc = __fdiv_rn(m, 127.0f);
+    const bool slow = nan || !plain_scale(sc);
+    const float rs = slow ? 0.0f : __frcp_rn(sc);
+    if (t == 0) static_cast<float*>(a.scale)[row] = sc;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const uint2 q = codes_int8(f[c], sc, rs, slow);
+      if (t + 32 * G * c < nchunk) reinterpret_cast<uint2*>(a.q + at)[t + 32 * G * c] = q;
+    }
+  } else {
+    constexpr int kLanes = FORM == F_FP8 ? 16 : 4;  // lanes that share a scale
+    const int64_t sat = row * ((nchunk + kLanes - 1) / kLanes);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int idx = t + 32 * G * c;
+      float m = 0.0f;
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        upk(f[c][i], lo, hi);
+        m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));  // passes a NaN over
+        nan = nan || lo != lo || hi != hi;
+      }
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if constexpr (FORM == F_FP8) {
+        const float sc = __fdiv_rn(m, 448.0f);
+        const uint2 q = codes_fp8(f[c], sc);
+        if (idx < nchunk) {
+          reinterpret_cast<uint2*>(a.q + at)[idx] = q;
+          if ((lane & 15) == 0) static_cast<float*>(a.scale)[sat + idx / 16] = sc;
+        }
+      } else {
+        nan = (__ballot_sync(0xffffffffu, nan) >> (lane & ~3) & 15u) != 0u;
+        // floor(log2 m) - 8 of the largest magnitude, within E8M0's range (subnormal m: far below it)
+        const uint32_t bits = __float_as_uint(m);
+        const int field = static_cast<int>(bits >> 23);
+        const int shared = max(-127, field - 127 - 8);  // field <= 254, or 255 for an infinity
+        const int sh = min(127, shared);
+        const float inv = sh < 127 ? __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) : __uint_as_float(0x00400000u);
+        const uint64_t inv2 = pk(-inv, -inv);
+        uint32_t k[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float lo, hi;
+          upk(mul2(f[c][i], inv2), lo, hi);
+          k[i] = e4m3x2_of(lo, hi);
+        }
+        if (idx < nchunk) {
+          reinterpret_cast<uint2*>(a.q + at)[idx] = make_uint2(k[0] | k[1] << 16, k[2] | k[3] << 16);
+          if ((lane & 3) == 0)
+            static_cast<uint8_t*>(a.scale)[sat + idx / 4] =
+                nan ? 0xffu : m > 0.0f ? static_cast<uint8_t>(sh + 127) : static_cast<uint8_t>(0u);
+        }
+      }
+    }
+  }
+}
+
+template <int FORM, int CH, int G>
+cudaError_t go(const NormArgs& a, cudaStream_t stream) {
+  constexpr int kWarps = G > 8 ? G : 8;
+  const int64_t ctas = (a.M + kWarps / G - 1) / (kWarps / G);
+  return launch_pdl(norm_quant_kernel<FORM, CH, G>, dim3(static_cast<unsigned>(ctas)), dim3(32 * kWarps), 0, stream, a);
+}
+
+template <int FORM>
+cudaError_t pick(const NormArgs& a, int num_sms, cudaStream_t stream) {
+  const int nchunk = a.K / 8;
+  if (a.M <= 2 * num_sms && nchunk > 256) {  // few rows: one or two a SM, as many threads a row as it has chunks
+    if (nchunk <= 1024) return go<FORM, 1, 32>(a, stream);
+  }
+  if (nchunk <= 32) return go<FORM, 1, 1>(a, stream);
+  if (nchunk <= 64) return go<FORM, 1, 2>(a, stream);
+  if (nchunk <= 128) return go<FORM, 1, 4>(a, stream);
+  if (nchunk <= 256) return go<FORM, 1, 8>(a, stream);
+  if (nchunk <= 512) return go<FORM, 2, 8>(a, stream);
+  if (nchunk <= 1024) return go<FORM, 4, 8>(a, stream);
+  if (nchunk <= 2048) return go<FORM, 2, 32>(a, stream);
+  if (nchunk <= 4096) return go<FORM, 4, 32>(a, stream);
+  return go<FORM, 8, 32>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_quant(const NormArgs& a, int form, int num_sms, cudaStream_t stream) {
+  if (a.M == 0) return cudaSuccess;
+  switch (form) {
+    case 0: return pick<F_INT8>(a, num_sms, stream);
+    case 1: return pick<F_FP8>(a, num_sms, stream);
+    default: return pick<F_MX>(a, num_sms, stream);
+  }
+}
+
+}  // namespace w8a8
