@@ -515,6 +515,47 @@ W8A8_API w8a8_status w8a8_mx_rms_norm_quant(const uint16_t* x, const uint16_t* r
                                             uint16_t* y, uint8_t* q, uint8_t* scale, w8a8_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* bf16 products: the layers that a quantised model keeps in bf16 ([P1] §一: */
+/* the recipe excludes wo_a, wo_b and the gates), with what follows them in  */
+/* one pass:                                                                 */
+/*   y = act(x w^T + bias) (+ residual), rounded once to bf16, or to fp32    */
+/* with W8A8_MM_F32.  Sums, bias, activation and residual are binary32.      */
+/* W8A8_ACT_SWIGLU: w has 2N rows, the gate's N, then the up projection's    */
+/* (bias likewise); y = silu(gate) * up.  Weights are used as they lie.      */
+/* K % 16 == 0; x and w 16-byte aligned; any N (rows of y that start on      */
+/* 16-byte boundaries are stored faster).  residual may be y itself (bf16),  */
+/* no other tensors may overlap.  The workspace holds the status word alone. */
+/* w8a8_last_engine() is W8A8_ENGINE_TC.                                     */
+/* ------------------------------------------------------------------------ */
+
+enum {
+  W8A8_ACT_NONE = 0,
+  W8A8_ACT_RELU = 1,
+  W8A8_ACT_SILU = 2,      /* v / (1 + exp(-v)) */
+  W8A8_ACT_GELU = 3,      /* v * Phi(v) */
+  W8A8_ACT_GELU_TANH = 4, /* v / (1 + exp(-2u)), u = sqrt(2/pi) (v + 0.044715 v^3) */
+  W8A8_ACT_SWIGLU = 5     /* silu(gate) * up */
+};
+#define W8A8_MM_F32 1u /* y is fp32 */
+
+W8A8_API size_t w8a8_bf16_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* x [M,K] bf16, w [N,K] bf16 ([2N,K] for SWIGLU), bias [rows of w] bf16 or NULL, residual [M,N] bf16 or NULL
+ * -> y [M,N] bf16 or fp32. */
+W8A8_API w8a8_status w8a8_bf16_matmul(const uint16_t* x, int64_t M, int64_t K, const uint16_t* w, int64_t N,
+                                      const uint16_t* bias, int act, const uint16_t* residual, uint32_t flags,
+                                      void* y, void* ws, size_t ws_bytes, w8a8_stream_t stream);
+
+W8A8_API size_t w8a8_bf16_grouped_matmul_workspace_bytes(int64_t E, int64_t R, int64_t N, int64_t K);
+
+/* The same for rows grouped by expert: x [R,K], group_list [E] counts (device; a bad one is reported through the status
+ * word and y left as it was), w [E,N,K] ([E,2N,K]), bias [E, rows of an expert's w] or NULL -> y [R,N]. */
+W8A8_API w8a8_status w8a8_bf16_grouped_matmul(const uint16_t* x, const int64_t* group_list, int64_t E, int64_t R,
+                                              int64_t K, const uint16_t* w, int64_t N, const uint16_t* bias, int act,
+                                              uint32_t flags, void* y, void* ws, size_t ws_bytes,
+                                              w8a8_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Device status                                                             */
 /* ------------------------------------------------------------------------ */
 

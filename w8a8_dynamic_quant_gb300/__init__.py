@@ -30,7 +30,8 @@ __all__ = [
     "moe_layer_workspace_offset", "moe_layer", "moe_gate_topk", "w8a8_fp8_quant", "w8a8_fp8_swiglu_quant",
     "fp8_matmul_workspace_bytes", "w8a8_fp8_matmul", "fp8_grouped_matmul_workspace_bytes",
     "w8a8_fp8_grouped_matmul", "moe_fp8_layer_workspace_bytes", "moe_fp8_pad_inner", "moe_fp8_layer",
-    "w8a8_rms_norm_quant", "w8a8_fp8_rms_norm_quant", "w8a8_mx_rms_norm_quant",
+    "w8a8_rms_norm_quant", "w8a8_fp8_rms_norm_quant", "w8a8_mx_rms_norm_quant", "bf16_matmul_workspace_bytes",
+    "w8a8_bf16_matmul", "bf16_grouped_matmul_workspace_bytes", "w8a8_bf16_grouped_matmul",
 ]
 
 
@@ -845,6 +846,100 @@ def w8a8_mx_rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1
     the operands of w8a8_mx_matmul."""
     return _rms_norm("w8a8_mx_rms_norm_quant", x, weight, eps, residual, want_y, q, scale, residual_out, y,
                      torch.uint8, torch.uint8, 32)
+
+
+def _activation(name: str) -> int:
+    act = _capi.ACTIVATIONS.get(name)
+    if act is None:
+        raise ValueError(f"activation must be one of {', '.join(map(repr, _capi.ACTIVATIONS))}, got {name!r}")
+    return act
+
+
+def _out_dtype(dtype, y):
+    if y is not None:
+        dtype = y.dtype
+    if dtype is not _BF16 and dtype is not _F32:
+        raise TypeError(f"y must be {_BF16} or {_F32}, got {dtype}")
+    return dtype
+
+
+def bf16_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
+    return _size("w8a8_bf16_matmul_workspace_bytes", M, N, K)
+
+
+def w8a8_bf16_matmul(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, activation: str = "none",
+                     residual: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                     ws: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
+    """bf16 x [M,K] x bf16 w [N,K] -> y [M,N] = activation(x w^T + bias) (+ residual), bf16 or float32.
+
+    activation: "none", "relu", "silu", "gelu", "gelu_tanh", or "swiglu" with w [2N,K] (the gate's rows, then the up
+    projection's; bias [2N]): silu(gate) * up.  bias bf16 [rows of w], residual bf16 [M,N] (y itself is allowed).  The
+    layers that a quantised model keeps in bf16; with out_dtype float32 the router's logits.  Keep a workspace (`ws`)
+    over calls: without one every call zero-fills its own."""
+    M, K = _dims(x, "x", 2)
+    rows = _dims(w, "w", 2)[0]
+    dev, act = x.get_device(), _activation(activation)
+    if not (dev >= 0 and x.dtype is _BF16 and type(w) is _Tensor and w.dtype is _BF16 and w.get_device() == dev
+            and w.shape[1] == K and x.is_contiguous() and w.is_contiguous()):
+        _check(x, "x", _BF16, (M, K), dev)
+        _check(w, "w", _BF16, (rows, K), dev)
+    N = rows
+    if act == 5:
+        if rows % 2:
+            raise ValueError("w must be [2N,K] for 'swiglu'")
+        N = rows // 2
+    if bias is not None:
+        _check(bias, "bias", _BF16, (rows,), dev)
+    if residual is not None:
+        _check(residual, "residual", _BF16, (M, N), dev)
+    ws = _check_ws(ws, lambda: bf16_matmul_workspace_bytes(M, N, K), dev)
+    out_dtype = _out_dtype(out_dtype, y)
+    if y is None:
+        y = _empty((M, N), dtype=out_dtype, device=x.device)
+    else:
+        _check(y, "y", out_dtype, (M, N), dev)
+    _call("w8a8_bf16_matmul", dev, x.data_ptr(), M, K, w.data_ptr(), N, None if bias is None else bias.data_ptr(), act,
+          None if residual is None else residual.data_ptr(), 0 if out_dtype is _BF16 else _capi.MM_F32, y.data_ptr(),
+          ws.data_ptr(), ws.numel())
+    return y
+
+
+def bf16_grouped_matmul_workspace_bytes(E: int, R: int, N: int, K: int) -> int:
+    return _size("w8a8_bf16_grouped_matmul_workspace_bytes", E, R, N, K)
+
+
+def w8a8_bf16_grouped_matmul(x: torch.Tensor, group_list: torch.Tensor, w: torch.Tensor,
+                             bias: Optional[torch.Tensor] = None, activation: str = "none",
+                             out_dtype: torch.dtype = torch.bfloat16, ws: Optional[torch.Tensor] = None,
+                             y: Optional[torch.Tensor] = None):
+    """w8a8_bf16_matmul for rows grouped by expert: bf16 x [R,K], int64 group_list [E] (rows of every expert), bf16
+    w [E,N,K] ("swiglu": [E,2N,K]), bf16 bias [E, rows of w] -> y [R,N].  A group list that does not fit R leaves y as
+    it was (read_device_status)."""
+    R, K = _dims(x, "x", 2)
+    E, rows, K2 = _dims(w, "w", 3)
+    dev, act = x.get_device(), _activation(activation)
+    if not (dev >= 0 and x.dtype is _BF16 and type(w) is _Tensor and w.dtype is _BF16 and w.get_device() == dev
+            and K2 == K and x.is_contiguous() and w.is_contiguous()):
+        _check(x, "x", _BF16, (R, K), dev)
+        _check(w, "w", _BF16, (E, rows, K), dev)
+    _check(group_list, "group_list", _I64, (E,), dev)
+    N = rows
+    if act == 5:
+        if rows % 2:
+            raise ValueError("w must be [E,2N,K] for 'swiglu'")
+        N = rows // 2
+    if bias is not None:
+        _check(bias, "bias", _BF16, (E, rows), dev)
+    ws = _check_ws(ws, lambda: bf16_grouped_matmul_workspace_bytes(E, R, N, K), dev)
+    out_dtype = _out_dtype(out_dtype, y)
+    if y is None:
+        y = _empty((R, N), dtype=out_dtype, device=x.device)
+    else:
+        _check(y, "y", out_dtype, (R, N), dev)
+    _call("w8a8_bf16_grouped_matmul", dev, x.data_ptr(), group_list.data_ptr(), E, R, K, w.data_ptr(), N,
+          None if bias is None else bias.data_ptr(), act, 0 if out_dtype is _BF16 else _capi.MM_F32, y.data_ptr(),
+          ws.data_ptr(), ws.numel())
+    return y
 
 
 def read_device_status(ws: torch.Tensor) -> int:

@@ -1,6 +1,7 @@
-// capi_bf16.cu -- the extern "C" boundary of the norm with 8-bit outputs (declared in include/w8a8.h): argument
-// validation and stream-ordered launches, as capi.cu has them for the int8 and MXFP8 calls.
+// capi_bf16.cu -- the extern "C" boundary of the norm with 8-bit outputs and of the bf16 products (declared in
+// include/w8a8.h): argument validation and stream-ordered launches, as capi.cu has them for the int8 and MXFP8 calls.
 #include "capi_common.cuh"
+#include "gemm_bf16.cuh"
 #include "norm.cuh"
 
 using namespace w8a8;
@@ -37,6 +38,27 @@ w8a8_status norm_common(int form, const uint16_t* x, const uint16_t* residual, c
   return cuda_status(launch_norm_quant(a, form, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+w8a8_status matmul_common(Bf16GemmArgs& a, uint32_t flags, void* ws, size_t ws_bytes, w8a8_stream_t stream) {
+  // (a tile's last rows lie up to 255 past the tensor's: their coordinates are 32-bit integers)
+  constexpr int64_t kMaxRows = INT32_MAX - 256;
+  if (a.E <= 0 || a.E > kMaxE || a.R < 0 || a.R > kMaxRows || a.act < W8A8_ACT_NONE || a.act > W8A8_ACT_SWIGLU ||
+      (flags & ~W8A8_MM_F32) != 0u)
+    return W8A8_ERR_SHAPE;
+  if (a.N <= 0 || a.N > kMaxRows / a.E / (a.act == W8A8_ACT_SWIGLU ? 2 : 1)) return W8A8_ERR_SHAPE;
+  if (w8a8_status s = check_k(a.K)) return s;
+  if (a.R == 0) return W8A8_OK;
+  if (!a.x || !a.w || !a.y) return W8A8_ERR_NULL;
+  if (!ws) return W8A8_ERR_WORKSPACE;
+  if (!aligned16(a.x) || !aligned16(a.w)) return W8A8_ERR_ALIGN;
+  if (ws_bytes < kStatusBytes || !aligned16(ws)) return W8A8_ERR_WORKSPACE;
+  int sms = 0;
+  if (w8a8_status s = device_info(sms)) return s;  // refuses a device of another kind
+  a.f32 = (flags & W8A8_MM_F32) != 0u;
+  a.status = static_cast<DeviceStatus*>(ws);
+  t_last_engine = W8A8_ENGINE_TC;
+  return cuda_status(launch_bf16_gemm(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -57,6 +79,48 @@ w8a8_status w8a8_mx_rms_norm_quant(const uint16_t* x, const uint16_t* residual, 
                                    int64_t K, float eps, uint32_t flags, uint16_t* residual_out, uint16_t* y,
                                    uint8_t* q, uint8_t* scale, w8a8_stream_t stream) {
   return norm_common(2, x, residual, weight, M, K, eps, flags, residual_out, y, q, scale, stream);
+}
+
+size_t w8a8_bf16_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return M < 0 || N <= 0 || K <= 0 ? 0 : kStatusBytes;
+}
+
+size_t w8a8_bf16_grouped_matmul_workspace_bytes(int64_t E, int64_t R, int64_t N, int64_t K) {
+  return E <= 0 || E > kMaxE || R < 0 || N <= 0 || K <= 0 ? 0 : kStatusBytes;
+}
+
+w8a8_status w8a8_bf16_matmul(const uint16_t* x, int64_t M, int64_t K, const uint16_t* w, int64_t N,
+                             const uint16_t* bias, int act, const uint16_t* residual, uint32_t flags, void* y, void* ws,
+                             size_t ws_bytes, w8a8_stream_t stream) {
+  Bf16GemmArgs a;
+  a.x = x;
+  a.w = w;
+  a.bias = bias;
+  a.residual = residual;
+  a.y = y;
+  a.R = M;
+  a.K = K;
+  a.N = N;
+  a.act = act;
+  return matmul_common(a, flags, ws, ws_bytes, stream);
+}
+
+w8a8_status w8a8_bf16_grouped_matmul(const uint16_t* x, const int64_t* group_list, int64_t E, int64_t R, int64_t K,
+                                     const uint16_t* w, int64_t N, const uint16_t* bias, int act, uint32_t flags,
+                                     void* y, void* ws, size_t ws_bytes, w8a8_stream_t stream) {
+  if (R > 0 && !group_list) return W8A8_ERR_NULL;
+  Bf16GemmArgs a;
+  a.x = x;
+  a.group_list = group_list;
+  a.w = w;
+  a.bias = bias;
+  a.y = y;
+  a.E = E;
+  a.R = R;
+  a.K = K;
+  a.N = N;
+  a.act = act;
+  return matmul_common(a, flags, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -1,5 +1,6 @@
 // fp8_common.cuh -- what the two block-scaled FP8 contractions share: the work walk, tensor-memory loads, waits and
 // the MMA issue.  The kernels are in fp8_gemm.cu (weights as the MMA's M side) and fp8_wide.cu (tokens as M side).
+// The bf16 product (gemm_bf16.cu) takes the group scan, the waits, the elected loads and the launch from here.
 #pragma once
 
 #include <atomic>
@@ -211,8 +212,8 @@ __device__ __forceinline__ void unit_tile(int unit, int E, int WB, const int* s_
 // Rows and units of the groups, and whether the list is usable: scan_groups with its sum checked in 64 bits where 32
 // may not hold it.  Called by all NT threads; s_rows is 0 and s_bad set up before.  A __syncthreads (or a cluster
 // barrier) follows before bad_list() is asked.
-template <int NT, typename UnitsOf>
-__device__ __forceinline__ int scan_checked(const KArgs& a, UnitsOf units_of, int* s_off, int* s_prefix, int* s_warp,
+template <int NT, typename Args, typename UnitsOf>
+__device__ __forceinline__ int scan_checked(const Args& a, UnitsOf units_of, int* s_off, int* s_prefix, int* s_warp,
                                             int* s_bad, unsigned long long* s_rows, int* units) {
   if (a.group_list == nullptr) {  // one group of R rows (R <= INT32_MAX)
     const int u = units_of(static_cast<int>(a.R));
@@ -233,7 +234,8 @@ __device__ __forceinline__ int scan_checked(const KArgs& a, UnitsOf units_of, in
       atomicAdd(s_rows, static_cast<unsigned long long>(max(0ll, static_cast<long long>(a.group_list[e]))));
   return rows;
 }
-__device__ __forceinline__ bool bad_list(const KArgs& a, int rows, int s_bad, unsigned long long s_rows) {
+template <typename Args>
+__device__ __forceinline__ bool bad_list(const Args& a, int rows, int s_bad, unsigned long long s_rows) {
   return s_bad != 0 || rows != a.R ||
          (a.group_list != nullptr && a.R > INT32_MAX / a.E && s_rows != static_cast<unsigned long long>(a.R));
 }

@@ -1,0 +1,631 @@
+// gemm_bf16.cu -- bf16 x bf16 products on the 5th-generation tensor cores (tcgen05.mma.cta_group::2.kind::f16) with bias,
+// activation and residual in the epilogue, dense and grouped by expert: the layers that a quantised model keeps in bf16
+// (the router's projection, output projections, expert stacks that are not quantised).
+//
+//   y[m,n] = act(sum_k x[m,k] w[n,k] + bias[n]) (+ residual[m,n])          rounded once, to bf16 or binary32
+//   swiglu:  y[m,n] = silu(gate) * up,  gate = row n of the product, up = row N + n
+//
+// Products of bf16 are exact in binary32; the sum over K stays in the tensor core's binary32 accumulator, bias,
+// activation and residual in registers.
+//
+// Tile.  The weights are the MMA's M side, 256 rows per CTA pair (128 in each CTA); a block of up to NT tokens is N, in
+// steps of 16: the even CTA holds the first half of the block's token rows, the odd CTA the rest.  Ragged groups pad to
+// 16 rows, not to a tile.  A ring stage is 64 of K: 128 weight rows and the CTA's token rows, 128 bytes each, by TMA with
+// 128-byte swizzle.  Gated: each CTA's 128 rows are 64 gate rows and the 64 up rows that belong to them, so a channel's
+// two sums meet inside a CTA (through the epilogue's staging buffers) and the weights need no packing.
+//
+// Tensor memory (512 columns): accumulators of NT columns; the epilogue of one unit runs beside the MMAs of the next.
+//
+// Warp roles (320 threads, one CTA per SM):
+//   warp 0      TMA producer
+//   warp 1      TMEM owner; the even CTA's issues the MMAs (whole warp, one lane elected)
+//   warps 2-9   epilogue: warp w reads TMEM lanes 32 * (w % 4) .. (channels) and one half of the tokens, 16 at a time:
+//               activation with a channel a lane, then through shared memory to rows of 32 channels for the residual's
+//               loads and the stores
+//
+// Work.  A unit is one tile over the whole of K, and the pairs take every C-th one; a dense problem of few units gives
+// each to a cluster of 2 to 8 pairs that take parts of K and add their sums through distributed shared memory, in the
+// order of K.  No order of arrival changes a bit.
+//
+// Every mbarrier wait is bounded (2 s): on expiry the CTA sets W8A8_ERR_DEVICE_TIMEOUT, lets in-flight copies land,
+// frees TMEM and returns.
+#include "fp8_common.cuh"
+#include "gemm_bf16.cuh"
+
+namespace w8a8 {
+
+namespace {
+
+using namespace fp8;
+
+constexpr int B_BK = 64;       // K per stage: 128 bytes
+constexpr int B_HALF = 128;    // weight rows of a tile in each CTA
+constexpr int B_THREADS = 320;
+constexpr int B_EPI0 = 2;
+constexpr uint32_t B_W_BYTES = B_HALF * B_BK * 2;  // 16 KB
+constexpr int B_LD = 36;                           // floats a staged token row: 32 channels, and 4 against conflicts
+constexpr uint32_t B_STG_FLOATS = 16 * B_LD;       // per epilogue warp
+
+struct BArgs {
+  const int64_t* group_list;
+  const uint16_t* bias;
+  const uint16_t* residual;
+  void* y;
+  DeviceStatus* status;
+  int64_t R, N, K;
+  int E;
+  int act;
+  int split;   // pairs per cluster that share a unit's K
+  int blocks;  // dense: token blocks of `per` tokens each
+  int per;
+  int xbig, xsmall;  // token rows of the two TMA boxes
+  bool f32;
+  bool vec;    // rows of y (and the residual) start on 16-byte boundaries
+};
+
+template <int NT>
+struct BCfg {
+  static constexpr uint32_t kXBytes = NT / 2 * B_BK * 2;
+  static constexpr uint32_t kStageBytes = B_W_BYTES + kXBytes;
+  static constexpr int kStages = NT == 256 ? 6 : NT == 128 ? 8 : NT == 64 ? 9 : 10;
+  static constexpr int kAcc = NT == 256 ? 2 : 4;  // accumulators of NT columns
+  static constexpr int kCols = NT / 2;            // of them read by one epilogue warp, at most
+  static constexpr size_t kSmem =
+      static_cast<size_t>(kStages) * kStageBytes + F_EPI_WARPS * B_STG_FLOATS * 4 + 1024;
+  // the parts' sums of a shared unit lie in the ring
+  static_assert(static_cast<size_t>(F_EPI_WARPS) * kCols * 32 * 4 <= static_cast<size_t>(kStages) * kStageBytes, "");
+};
+
+// Instruction descriptor: binary32 accumulator, bf16 operands, both K-major, M = 256, N = n.
+__device__ __forceinline__ uint32_t idesc_bf16(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (256u >> 4 << 24);
+}
+
+// x * sigmoid(z): x / (1 + t) for z >= 0 and t x / (1 + t) below, t = exp(-|z|) <= 1, so nothing overflows and far
+// negative values keep what t has.
+__device__ __forceinline__ float times_sigmoid(float x, float z) {
+  const float t = __expf(-fabsf(z));
+  return __fdividef(z < 0.0f ? t * x : x, 1.0f + t);
+}
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
+  switch (act) {
+    case W8A8_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];  // a NaN stays
+      break;
+    case W8A8_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = times_sigmoid(v[i], v[i]);
+      break;
+    case W8A8_ACT_GELU:  // x Phi(x) = x erfc(-x / sqrt 2) / 2, which keeps its digits far below zero
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * erfcf(v[i] * -0.70710678118654752f);
+      break;
+    case W8A8_ACT_GELU_TANH:  // (1 + tanh u) / 2 = sigmoid(2u)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        v[i] = times_sigmoid(v[i], 1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
+      break;
+    default: break;
+  }
+}
+
+// One unit of work: the tile and its K range.
+struct Unit {
+  int e, wb;   // expert, block of weight rows
+  int row0;    // first token row (of all R)
+  int tvalid;  // tokens
+  int n;       // tokens rounded up to 16
+};
+
+// The barrier of an epilogue warp that holds gate rows and of the one that holds the up rows of the same channels and
+// tokens; the AND of what they bring.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pair_and(int id, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.and.pred q, %1, 64, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return r != 0u;
+}
+
+// An epilogue warp's place: what it stages, reads back and stores.
+struct Place {
+  float* stg;         // its staging buffer
+  const float* gate;  // gated: those of the two warps of its channels
+  const float* up;
+  int q, h, lane;
+  int bar;            // gated: the two warps' barrier
+};
+
+// 16 tokens x 32 channels: v[i] is this lane's channel of token i.  `rows` of the tokens exist and go to rows row..
+// of y, at channels n0 .. n0 + ncols.
+template <bool GATED>
+__device__ __forceinline__ void finish(const BArgs& a, const Place& p, float (&v)[16], float bias, int64_t row, int rows,
+                                       int64_t n0, int ncols) {
+  constexpr int kSlots = GATED ? 1 : 2;  // rows a lane stores
+  const int lane = p.lane;
+  const int c = (lane & 3) * 8;
+  const int r0 = (lane >> 2) + (GATED ? 8 * (p.q >> 1) : 0);
+  uint4 res[kSlots];
+  const bool add = a.residual != nullptr;
+  if (add && a.vec) {  // on their way while the activation is computed
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i)
+      if (r0 + 8 * i < rows && c < ncols)
+        res[i] = *reinterpret_cast<const uint4*>(a.residual + (row + r0 + 8 * i) * a.N + n0 + c);
+  }
+  if (a.bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += bias;
+  }
+  if constexpr (!GATED) activate(v, a.act);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) p.stg[i * B_LD + lane] = v[i];
+  if constexpr (GATED) pair_sync(p.bar);
+  else __syncwarp();
+  if (a.vec) {
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      const int r = r0 + 8 * i;
+      if (r < rows && c < ncols) {
+        float o[8];
+        const float* s = (GATED ? p.gate : p.stg) + r * B_LD + c;
+        const float4 s0 = *reinterpret_cast<const float4*>(s), s1 = *reinterpret_cast<const float4*>(s + 4);
+        o[0] = s0.x; o[1] = s0.y; o[2] = s0.z; o[3] = s0.w;
+        o[4] = s1.x; o[5] = s1.y; o[6] = s1.z; o[7] = s1.w;
+        if constexpr (GATED) {
+          const float* t = p.up + r * B_LD + c;
+          const float4 t0 = *reinterpret_cast<const float4*>(t), t1 = *reinterpret_cast<const float4*>(t + 4);
+          const float u[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] = times_sigmoid(o[k], o[k]) * u[k];
+        }
+        if (add) {
+          const uint32_t w[4] = {res[i].x, res[i].y, res[i].z, res[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            o[2 * k] += __uint_as_float(w[k] << 16);
+            o[2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
+          }
+        }
+        const int64_t at = (row + r) * a.N + n0 + c;
+        if (a.f32) {
+          float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.y) + at);
+          d[0] = make_float4(o[0], o[1], o[2], o[3]);
+          d[1] = make_float4(o[4], o[5], o[6], o[7]);
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + at) =
+              make_uint4(f32x2_to_bf16x2_bits(o[0], o[1]), f32x2_to_bf16x2_bits(o[2], o[3]),
+                         f32x2_to_bf16x2_bits(o[4], o[5]), f32x2_to_bf16x2_bits(o[6], o[7]));
+        }
+      }
+    }
+  } else {  // rows of y start anywhere: a channel a lane
+    const int first = GATED ? 8 * (p.q >> 1) : 0, last = min(rows, GATED ? first + 8 : 16);
+    for (int r = first; r < last; ++r) {
+      if (lane < ncols) {
+        float o = GATED ? p.gate[r * B_LD + lane] : p.stg[r * B_LD + lane];
+        if constexpr (GATED) o = times_sigmoid(o, o) * p.up[r * B_LD + lane];
+        const int64_t at = (row + r) * a.N + n0 + lane;
+        if (add) o += bf16_bits_to_f32(a.residual[at]);
+        if (a.f32) static_cast<float*>(a.y)[at] = o;
+        else static_cast<uint16_t*>(a.y)[at] = f32_to_bf16_bits(o);
+      }
+    }
+  }
+  if constexpr (GATED) pair_sync(p.bar);
+  else __syncwarp();
+}
+
+template <int NT, bool GATED>
+__global__ void __launch_bounds__(B_THREADS, 1)
+bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmXbig,
+                 const __grid_constant__ CUtensorMap tmXsmall, const BArgs a) {
+  using C = BCfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar_full[C::kStages];   // even CTA: both CTAs' tiles of the stage landed
+  __shared__ __align__(8) uint64_t bar_empty[C::kStages];  // the MMAs reading the stage are done
+  __shared__ __align__(8) uint64_t bar_accf[C::kAcc];      // the unit's accumulator is complete
+  __shared__ __align__(8) uint64_t bar_acce[C::kAcc];      // even CTA: both CTAs read it
+  __shared__ uint32_t s_tmem_base;
+  __shared__ volatile int s_abort;
+  __shared__ int s_bad;
+  __shared__ int s_prefix[F_MAX_E + 1];
+  __shared__ int s_off[F_MAX_E + 1];
+  __shared__ int s_warp[B_THREADS / 32];
+  __shared__ unsigned long long s_rows;  // the counts' sum where 32 bits may not hold it
+
+  const int tid = threadIdx.x;
+  const int warp = uni(tid >> 5);
+  const int lane = tid & 31;
+  const int E = a.E;
+  const int KB = static_cast<int>((a.K + B_BK - 1) / B_BK);
+  constexpr int kRows = GATED ? 128 : 256;  // channels of y per tile
+  const int WB = static_cast<int>((a.N + kRows - 1) / kRows);
+  const bool grouped = a.group_list != nullptr;
+
+  uint8_t* stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t stage_base = smem_u32(stages);
+  float* s_part = reinterpret_cast<float*>(stages);  // [epilogue warp][token][channel], after the last block
+  float* s_stg = reinterpret_cast<float*>(stages + C::kStages * C::kStageBytes);
+  // CTAs 2i and 2i + 1 of a cluster are a pair; rank: the CTA's place in it
+  uint32_t crank, cluster_id, nclusters;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
+  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(cluster_id));
+  asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(nclusters));
+  const uint32_t rank = crank & 1u, even = crank & ~1u;
+  const uint16_t pair_mask = static_cast<uint16_t>(3u << even);
+
+  if (tid == 0) {
+    s_abort = 0;
+    s_bad = 0;
+    s_rows = 0ull;
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&bar_full[s]), 1);
+      mbar_init(smem_u32(&bar_empty[s]), 1);
+    }
+    for (int b = 0; b < C::kAcc; ++b) {
+      mbar_init(smem_u32(&bar_accf[b]), 1);
+      mbar_init(smem_u32(&bar_acce[b]), 2 * F_EPI_WARPS);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmXbig);
+    tma_prefetch_desc(&tmXsmall);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem_base)),
+                 "r"(F_TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  __syncthreads();  // s_bad, before the scan may set it
+  pdl_trigger();
+  pdl_wait();
+  int units;
+  const int dense_blocks = a.blocks;
+  auto blocks_of = [grouped, dense_blocks](int cnt) { return grouped ? (cnt + NT - 1) / NT : dense_blocks; };
+  const int rows_total = scan_checked<B_THREADS>(
+      a, [WB, blocks_of](int c) { return blocks_of(c) * WB; }, s_off, s_prefix, s_warp, &s_bad, &s_rows, &units);
+  tc_fence_before();
+  cluster_sync_all();  // both CTAs' barriers and tensor memory exist before either touches the other's
+  tc_fence_after();
+  const uint32_t tmem_base = static_cast<uint32_t>(uni(static_cast<int>(s_tmem_base)));
+  if (bad_list(a, rows_total, s_bad, s_rows)) {
+    if (tid == 0 && blockIdx.x == 0) set_status(a.status, W8A8_ERR_GROUP_LIST, 0u);
+    units = 0;
+  }
+  // units first, first + step, ..; blocks [kb0, kb1) of each
+  const int part = static_cast<int>(crank >> 1);
+  const int first = static_cast<int>(cluster_id);
+  const int step = static_cast<int>(nclusters);
+  const int kb0 = KB * part / a.split, kb1 = KB * (part + 1) / a.split;
+  auto unit_of = [&](int unit) {
+    Unit u;
+    int tb, cnt, TB;
+    unit_tile(unit, E, WB, s_prefix, s_off, blocks_of, u.e, u.wb, tb, cnt, TB);
+    const int per = grouped ? ((cnt + TB - 1) / TB + 15) & ~15 : a.per;  // tokens split evenly over the blocks
+    u.row0 = s_off[u.e] + tb * per;
+    u.tvalid = min(per, cnt - tb * per);
+    u.n = (u.tvalid + 15) & ~15;
+    return u;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (both CTAs)
+    const uint32_t full_even0 = smem_cluster_addr(smem_u32(&bar_full[0]), even);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const int xbig = uni(a.xbig), xsmall = uni(a.xsmall);
+    for (int unit = first; ok && unit < units; unit += step) {
+      const Unit u = unit_of(unit);
+      const int64_t w0 = GATED ? static_cast<int64_t>(u.e) * 2 * a.N + static_cast<int64_t>(u.wb) * 128 + rank * 64
+                               : static_cast<int64_t>(u.e) * a.N + static_cast<int64_t>(u.wb) * 256 + rank * 128;
+      const int yw = uni(static_cast<int>(w0)), yu = uni(static_cast<int>(w0 + a.N));
+      const int rows = u.n >> 1;
+      const int small = (rows + xsmall - 1) / xsmall;  // loads of the small box that the rows would take
+      const bool few = uni(small <= 3 && rows < xbig);
+      const int loads = few ? uni(small) : 1;
+      const int box = few ? xsmall : xbig;
+      const CUtensorMap* tmX = few ? &tmXsmall : &tmXbig;
+      const int yx = uni(u.row0 + static_cast<int>(rank) * rows);
+      const uint32_t bytes = 2u * B_W_BYTES + static_cast<uint32_t>(2 * loads * box) * (B_BK * 2);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = wait_all(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 1u);
+        if (!ok) break;
+        if (rank == 0) expect_tx_elect(smem_u32(&bar_full[0]) + 8 * stage, bytes);
+        const uint32_t full = full_even0 + 8 * stage;
+        const uint32_t dst = stage_base + stage * C::kStageBytes;
+        tma_pair_elect(dst, &tmW, kb * B_BK, yw, full);
+        if constexpr (GATED) tma_pair_elect(dst + B_W_BYTES / 2, &tmW, kb * B_BK, yu, full);
+        for (int i = 0; i < loads; ++i)
+          tma_pair_elect(dst + B_W_BYTES + i * box * (B_BK * 2), tmX, kb * B_BK, yx + i * box, full);
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // Drain: the last fill of every stage has been consumed, so no copy into this CTA and no MMA arrival on its
+    // barriers is still in flight when the cluster leaves.
+    for (int i = 0; i < C::kStages && ok; ++i) {
+      ok = wait_all(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 5u);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- MMA issuer (even CTA, whole warp)
+    if (rank == 0) {
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, bphase = 0;
+      bool ok = true;
+      for (int unit = first; ok && unit < units; unit += step) {
+        const uint32_t idesc = idesc_bf16(uni(unit_of(unit).n));
+        ok = wait_all(smem_u32(&bar_acce[buf]), bphase ^ 1u, &s_abort, a.status, 2u);
+        if (!ok) break;
+        const uint32_t acc = tmem_base + buf * NT;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = wait_all(smem_u32(&bar_full[stage]), phase, &s_abort, a.status, 3u);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sa = stage_base + stage * C::kStageBytes;
+          const uint64_t adesc = smem_desc_sw128(sa);
+          const uint64_t bdesc = smem_desc_sw128(sa + B_W_BYTES);
+#pragma unroll
+          for (int k = 0; k < B_BK / 16; ++k)
+            tc_mma_pair(acc, adesc + 2u * k, bdesc + 2u * k, idesc, kb > kb0 || k > 0 ? 1u : 0u);
+          tc_commit_pair_mc(smem_u32(&bar_empty[stage]), pair_mask);  // frees the stage in both CTAs
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc_commit_pair_mc(smem_u32(&bar_accf[buf]), pair_mask);
+        if (++buf == C::kAcc) {
+          buf = 0;
+          bphase ^= 1u;
+        }
+      }
+    }
+  }
+
+  // ------------------------------------------------------------------ epilogue (both CTAs)
+  Place p;
+  const int ew = warp - B_EPI0;
+  p.q = warp & 3;
+  p.h = ew >> 2;
+  p.lane = lane;
+  p.bar = 1 + (p.q & 1) + 2 * p.h;
+  {
+    float* mine = s_stg + (p.h * 4 + p.q) * B_STG_FLOATS;
+    p.stg = mine;
+    p.gate = mine - (p.q >> 1) * 2 * B_STG_FLOATS;
+    p.up = p.gate + 2 * B_STG_FLOATS;
+  }
+  // channels of the warp in a tile (gated: the same ones for the two warps of a pair), and its bias row
+  const int c_tile = GATED ? static_cast<int>(rank) * 64 + 32 * (p.q & 1) : static_cast<int>(rank) * B_HALF + 32 * p.q;
+  auto bias_of = [&](const Unit& u, int64_t n0) {
+    if (a.bias == nullptr || n0 + lane >= a.N) return 0.0f;
+    const int64_t w_rows = GATED ? 2 * a.N : a.N;
+    return bf16_bits_to_f32(a.bias[u.e * w_rows + (GATED && p.q >= 2 ? a.N : 0) + n0 + lane]);
+  };
+  if (warp >= B_EPI0) {
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * p.q) << 16);
+    const uint32_t acce_even = smem_cluster_addr(smem_u32(&bar_acce[0]), even);
+    int buf = 0;
+    uint32_t bphase = 0;
+    for (int unit = first; unit < units; unit += step) {
+      const Unit u = unit_of(unit);
+      // the first half's warps read tokens [0, cut), the second's [cut, n)
+      const int n = uni(u.n);
+      const int cut = ((n >> 1) + 15) & ~15;
+      const int c0 = p.h == 0 ? 0 : cut;
+      const int cols = p.h == 0 ? cut : n - cut;
+      const int tv = uni(min(cols, u.tvalid - c0));  // tokens of this warp that exist (may be <= 0)
+      const int64_t n0 = static_cast<int64_t>(u.wb) * kRows + c_tile;
+      const int ncols = static_cast<int>(min(static_cast<int64_t>(32), a.N - n0));  // (may be <= 0)
+      const bool works = uni(tv > 0 && ncols > 0);
+      const float bias = bias_of(u, n0);
+      bool ok = wait_all(smem_u32(&bar_accf[buf]), bphase, &s_abort, a.status, 4u);
+      if constexpr (GATED) ok = pair_and(p.bar, ok);  // the two warps of a pair give up together
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t here = lane_addr + buf * NT + c0, release = acce_even + 8u * buf;
+      if (++buf == C::kAcc) {
+        buf = 0;
+        bphase ^= 1u;
+      }
+      if (!works) {
+        tc_fence_before();
+        arrive_lane0(release, lane);
+        continue;
+      }
+      float* part_at = s_part + ew * C::kCols * 32 + lane;
+      for (int t = 0; t < tv; t += 16) {
+        uint32_t r[16];
+        tmem_fetch(here + t, r);
+        tmem_ready(r);
+        if (t + 16 >= tv) {
+          tc_fence_before();
+          arrive_lane0(release, lane);
+        }
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+        if (a.split > 1) {  // a part of K of the cluster's unit: its sums to the ring, which is at rest
+#pragma unroll
+          for (int i = 0; i < 16; ++i) part_at[(t + i) * 32] = v[i];
+        } else {
+          finish<GATED>(a, p, v, bias, static_cast<int64_t>(u.row0) + c0 + t, min(16, tv - t), n0, ncols);
+        }
+      }
+    }
+  }
+
+  if (a.split > 1) {
+    // the parts' sums meet: every CTA adds its share of the tokens over its peers' shared memory, in the order of K
+    __syncwarp();
+    cluster_sync_all();
+    if (warp >= B_EPI0 && first < units) {
+      const Unit u = unit_of(first);
+      const int cut = ((u.n >> 1) + 15) & ~15;
+      const int c0 = p.h == 0 ? 0 : cut;
+      const int tv = uni(min(p.h == 0 ? cut : u.n - cut, u.tvalid - c0));
+      const int64_t n0 = static_cast<int64_t>(u.wb) * kRows + c_tile;
+      const int ncols = static_cast<int>(min(static_cast<int64_t>(32), a.N - n0));
+      if (uni(tv > 0 && ncols > 0)) {
+        const int t1 = tv * (part + 1) / a.split;
+        const float bias = bias_of(u, n0);
+        const uint32_t src = smem_u32(s_part + ew * C::kCols * 32 + lane);
+        for (int t = tv * part / a.split; t < t1; t += 16) {
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            float w[F_MAX_SPLIT][4];
+#pragma unroll
+            for (int j = 0; j < F_MAX_SPLIT; ++j) {  // every peer's words in flight, added in order
+              const uint32_t q = smem_cluster_addr(src, 2 * min(j, a.split - 1) + rank) + (t + i) * 128;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w[j][k] = j < a.split && t + i + k < t1 ? ld_cluster(q + k * 128) : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[i + k] = w[0][k];
+#pragma unroll
+            for (int j = 1; j < F_MAX_SPLIT; ++j)
+              if (j < a.split) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[i + k] += w[j][k];
+              }
+          }
+          finish<GATED>(a, p, v, bias, static_cast<int64_t>(u.row0) + c0 + t, min(16, t1 - t), n0, ncols);
+        }
+      }
+    }
+  }
+
+  // ---- teardown: on abort, give in-flight copies and MMAs time to land first, then the pair leaves together.
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (s_abort) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 20000000ull) {
+    }
+  }
+  cluster_sync_all();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(F_TMEM_COLS)
+                 : "memory");
+  }
+}
+
+struct BPlan {
+  int nt, blocks, per, split, pairs;
+};
+constexpr int round16(int64_t n) { return static_cast<int>((n + 15) & ~int64_t(15)); }
+
+// Cycles of one 64-deep block of a tile of n tokens: the tensor core's (four MMAs of n / 2, at least 40), or bringing
+// 128 weight rows and n / 2 token rows of 128 bytes to a SM at about 60 bytes a cycle.
+constexpr int64_t block_cost(int n) { return std::max(2 * n, std::max(160, (128 + n / 2) * 128 / 60)); }
+
+BPlan make_plan(int64_t E, int64_t R, int64_t channel_blocks, int64_t K, bool grouped) {
+  BPlan p{256, 0, 0, 1, F_MAX_CLUSTERS};
+  if (grouped) {
+    const int64_t want = 2 * ((R + E - 1) / E);  // twice the mean rows of a group
+    p.nt = want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
+    return p;
+  }
+  const int64_t KB = (K + B_BK - 1) / B_BK;
+  // clusters of 2 ks CTAs (one a SM) that are resident at once on 152 SMs, as the occupancy query gives them
+  constexpr int kFit[F_MAX_SPLIT + 1] = {0, 76, 36, 23, 15, 13, 8, 7, 7};
+  int64_t best = INT64_MAX;
+  const int64_t b0 = (R + 255) / 256;
+  for (int64_t b = b0; b <= b0 + 8 && b <= (R + 15) / 16; ++b) {
+    const int per = round16((R + b - 1) / b);
+    const int64_t blocks = (R + per - 1) / per;
+    const int64_t units = blocks * channel_blocks;
+    for (int ks = 1; ks <= F_MAX_SPLIT; ++ks) {
+      if (ks > 1 && (units > kFit[ks] || 2 * ks > KB)) continue;
+      const int64_t waves = ks > 1 ? 1 : (units + F_MAX_CLUSTERS - 1) / F_MAX_CLUSTERS;
+      const int64_t cost = waves * ((KB + ks - 1) / ks * block_cost(per) + 300) + (ks > 1 ? 1800 + 8 * per : 8 * per);
+      if (cost < best) {
+        best = cost;
+        p.per = per;
+        p.blocks = static_cast<int>(blocks);
+        p.split = ks;
+        p.pairs = static_cast<int>(ks > 1 ? units * ks : std::min<int64_t>(units, F_MAX_CLUSTERS));
+        p.nt = per <= 32 ? 32 : per <= 64 ? 64 : per <= 128 ? 128 : 256;
+      }
+    }
+  }
+  return p;
+}
+
+template <int NT, bool GATED>
+cudaError_t launch_nt(const Bf16GemmArgs& g, const BArgs& a, int pairs, cudaStream_t stream) {
+  using C = BCfg<NT>;
+  CUtensorMap mw, mb, ms;
+  const auto type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  if (!encode_map_2d(&mw, g.w, type, 2, g.E * g.N * (GATED ? 2 : 1), g.K, B_BK, GATED ? 64 : B_HALF, sw) ||
+      !encode_map_2d(&mb, g.x, type, 2, g.R, g.K, B_BK, a.xbig, sw) ||
+      !encode_map_2d(&ms, g.x, type, 2, g.R, g.K, B_BK, a.xsmall, sw))
+    return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(bf16_gemm_kernel<NT, GATED>), C::kSmem, ready);
+  if (e != cudaSuccess) return e;
+  return launch_pairs(bf16_gemm_kernel<NT, GATED>, pairs, a.split, B_THREADS, C::kSmem, stream, mw, mb, ms, a);
+}
+
+template <bool GATED>
+cudaError_t launch_gated(int nt, const Bf16GemmArgs& g, const BArgs& a, int pairs, cudaStream_t stream) {
+  switch (nt) {
+    case 32: return launch_nt<32, GATED>(g, a, pairs, stream);
+    case 64: return launch_nt<64, GATED>(g, a, pairs, stream);
+    case 128: return launch_nt<128, GATED>(g, a, pairs, stream);
+    default: return launch_nt<256, GATED>(g, a, pairs, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_bf16_gemm(const Bf16GemmArgs& g, cudaStream_t stream) {
+  if (g.R == 0) return cudaSuccess;
+  const bool grouped = g.group_list != nullptr, gated = g.act == W8A8_ACT_SWIGLU;
+  const int64_t channel_blocks = (g.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
+  const BPlan p = make_plan(g.E, g.R, channel_blocks, g.K, grouped);
+  if ((g.R / (grouped ? p.nt : p.per) + g.E) * channel_blocks > INT32_MAX) return cudaErrorInvalidValue;
+  BArgs a;
+  a.group_list = g.group_list;
+  a.bias = g.bias;
+  a.residual = g.residual;
+  a.y = g.y;
+  a.status = g.status;
+  a.R = g.R;
+  a.N = g.N;
+  a.K = g.K;
+  a.E = static_cast<int>(g.E);
+  a.act = g.act;
+  a.split = p.split;
+  a.blocks = p.blocks;
+  a.per = p.per;
+  a.xbig = (grouped ? p.nt : p.per) / 2;
+  a.xsmall = std::max(8, (a.xbig / 4 + 7) & ~7);
+  a.f32 = g.f32;
+  a.vec = g.N % 8 == 0 && (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0u &&
+          (reinterpret_cast<uintptr_t>(g.residual) & 15u) == 0u;
+  return gated ? launch_gated<true>(p.nt, g, a, p.pairs, stream) : launch_gated<false>(p.nt, g, a, p.pairs, stream);
+}
+
+}  // namespace w8a8

@@ -1,0 +1,23 @@
+// gemm_bf16.cuh -- launch of the bf16 products (gemm_bf16.cu).
+#pragma once
+
+#include "kernels.cuh"
+
+namespace w8a8 {
+
+// y = act(x w^T + bias) (+ residual), dense (group_list == nullptr: one group of R rows) or grouped by expert.
+struct Bf16GemmArgs {
+  const uint16_t* x = nullptr;          // [R,K] bf16
+  const int64_t* group_list = nullptr;  // [E] counts, or nullptr
+  const uint16_t* w = nullptr;          // [E,N,K] bf16, gated: [E,2N,K], the gate's N rows, then the up projection's
+  const uint16_t* bias = nullptr;       // [E, rows of w] bf16 or nullptr
+  const uint16_t* residual = nullptr;   // [R,N] bf16 or nullptr
+  void* y = nullptr;                    // [R,N] bf16 or fp32
+  DeviceStatus* status = nullptr;
+  int64_t E = 1, R = 0, K = 0, N = 0;   // N: channels of y
+  int act = 0;                          // W8A8_ACT_*
+  bool f32 = false;                     // y is fp32
+};
+cudaError_t launch_bf16_gemm(const Bf16GemmArgs& a, cudaStream_t stream);
+
+}  // namespace w8a8
