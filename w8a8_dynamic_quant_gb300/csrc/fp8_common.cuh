@@ -193,20 +193,20 @@ __device__ __forceinline__ bool next_unit(Walk& w, int& unit, int& kb0, int& kb1
   }
   return true;
 }
-// Unit -> expert, channel block, token block of TB.  Token blocks go in groups of F_SUPER with the channel block
+// Unit -> expert, channel block, token block of TB.  Token blocks go in groups of SUPER with the channel block
 // outside: the pairs in flight share weight blocks, and a group's token rows stay in L2 while the weights sweep past.
-template <typename BlocksOf>
+template <int SUPER = F_SUPER, typename BlocksOf>
 __device__ __forceinline__ void unit_tile(int unit, int E, int WB, const int* s_prefix, const int* s_off,
                                           BlocksOf blocks_of, int& e, int& wb, int& tb, int& cnt, int& TB) {
   e = expert_of(unit, E, s_prefix);
   const int local = unit - s_prefix[e];
   cnt = s_off[e + 1] - s_off[e];
   TB = blocks_of(cnt);
-  const int g = local / (WB * F_SUPER);
-  const int rem = local - g * WB * F_SUPER;
-  const int gt = min(F_SUPER, TB - g * F_SUPER);
+  const int g = local / (WB * SUPER);
+  const int rem = local - g * WB * SUPER;
+  const int gt = min(SUPER, TB - g * SUPER);
   wb = rem / gt;
-  tb = g * F_SUPER + rem - wb * gt;
+  tb = g * SUPER + rem - wb * gt;
 }
 
 // Rows and units of the groups, and whether the list is usable: scan_groups with its sum checked in 64 bits where 32

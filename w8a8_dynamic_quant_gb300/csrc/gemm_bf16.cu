@@ -40,6 +40,7 @@ using namespace fp8;
 
 constexpr int B_BK = 64;       // K per stage: 128 bytes
 constexpr int B_HALF = 128;    // weight rows of a tile in each CTA
+constexpr int B_SUPER = 16;    // token blocks per rasterisation group (32: 10 % slower at 8192 x 14336 x 4096, 8: 1 %)
 constexpr int B_THREADS = 320;
 constexpr int B_EPI0 = 2;
 constexpr uint32_t B_W_BYTES = B_HALF * B_BK * 2;  // 16 KB
@@ -58,7 +59,8 @@ struct BArgs {
   int split;   // pairs per cluster that share a unit's K
   int blocks;  // dense: token blocks of `per` tokens each
   int per;
-  int xbig, xsmall;  // token rows of the two TMA boxes
+  int chunk;         // blocks of K that an accumulator takes before its sum is added up in binary32
+  int xbig, xsmall;  // token rows of the two TMA boxes (dense: one)
   bool f32;
   bool vec;    // rows of y (and the residual) start on 16-byte boundaries
 };
@@ -68,12 +70,21 @@ struct BCfg {
   static constexpr uint32_t kXBytes = NT / 2 * B_BK * 2;
   static constexpr uint32_t kStageBytes = B_W_BYTES + kXBytes;
   static constexpr int kStages = NT == 256 ? 6 : NT == 128 ? 8 : NT == 64 ? 9 : 10;
-  static constexpr int kAcc = NT == 256 ? 2 : 4;  // accumulators of NT columns
-  static constexpr int kCols = NT / 2;            // of them read by one epilogue warp, at most
-  static constexpr size_t kSmem =
-      static_cast<size_t>(kStages) * kStageBytes + F_EPI_WARPS * B_STG_FLOATS * 4 + 1024;
-  // the parts' sums of a shared unit lie in the ring
-  static_assert(static_cast<size_t>(F_EPI_WARPS) * kCols * 32 * 4 <= static_cast<size_t>(kStages) * kStageBytes, "");
+  static constexpr int kAcc = NT == 128 ? 3 : 2;   // accumulators of NT columns
+  static constexpr uint32_t kSumCol = NT == 256 ? NT : kAcc * NT;  // NT columns of sums over chunks of K (NT = 256: in
+                                                                   // the place of the second accumulator)
+  static constexpr uint32_t kTmemCols = NT >= 128 ? 512 : NT == 64 ? 256 : 128;
+  static constexpr int kCols = NT / 2;             // columns read by one epilogue warp, at most
+  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes + F_EPI_WARPS * B_STG_FLOATS * 4 +
+                                  1024;  // and the groups' offsets
+  static_assert(kSmem + (F_MAX_E + 1) * 8 + 512 <= 227 * 1024, "shared memory of a CTA");
+  // Where the parts of a shared unit's K come in, [part][epilogue warp][its share of the tokens][32 channels]: the
+  // ring's last stages, which a launch whose units are shared does without.
+  static constexpr uint32_t kRecvBytes = (kCols + F_MAX_SPLIT) * F_EPI_WARPS * 32 * 4;
+  static constexpr int kRingShared = kStages - static_cast<int>((kRecvBytes + kStageBytes - 1) / kStageBytes);
+  // the parts go out from the stages that remain
+  static_assert(NT > 128 || static_cast<size_t>(F_EPI_WARPS) * kCols * 32 * 4 <= static_cast<size_t>(kRingShared) * kStageBytes,
+                "");
 };
 
 // Instruction descriptor: binary32 accumulator, bf16 operands, both K-major, M = 256, N = n.
@@ -81,11 +92,38 @@ __device__ __forceinline__ uint32_t idesc_bf16(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (256u >> 4 << 24);
 }
 
-// x * sigmoid(z): x / (1 + t) for z >= 0 and t x / (1 + t) below, t = exp(-|z|) <= 1, so nothing overflows and far
-// negative values keep what t has.
-__device__ __forceinline__ float times_sigmoid(float x, float z) {
-  const float t = __expf(-fabsf(z));
-  return __fdividef(z < 0.0f ? t * x : x, 1.0f + t);
+// x * sigmoid(z), z2 = z * log2 e: x / (1 + t) for z >= 0 and t x / (1 + t) below, t = exp(-|z|) <= 1, so nothing
+// overflows and far negative values keep what t has (down to 2^-126).
+__device__ __forceinline__ float times_sigmoid(float x, float z2) {
+  float t, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(-fabsf(z2)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+  return (z2 < 0.0f ? t * x : x) * r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float silu(float x) { return times_sigmoid(x, x * kLog2e); }
+// (1 + tanh u) / 2 = sigmoid(2u), u = sqrt(2 / pi) (x + 0.044715 x^3)
+__device__ __forceinline__ float gelu_tanh(float x) { return times_sigmoid(x, x * fmaf(x * x, 0.10294324f, 2.3022082f)); }
+// x Phi(x) = x erfc(-x / sqrt 2) / 2, which keeps its digits far below zero.  erfc(z) = t exp(-z^2 + P(t)),
+// t = 1 / (1 + z / 2), within a relative 1.2e-7 for z >= 0: the Chebyshev fit of Press, Teukolsky, Vetterling and
+// Flannery, "Numerical Recipes in C" (1992), 6.2 (erfcf: 687 us for 8192 x 14336 x 4096, this 552).
+__device__ __forceinline__ float gelu(float x) {
+  const float z = fabsf(x) * 0.70710678118654752f;
+  float t, e;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.5f, z, 1.0f)));
+  float p = fmaf(t, 0.17087277f, -0.82215223f);
+  p = fmaf(t, p, 1.48851587f);
+  p = fmaf(t, p, -1.13520398f);
+  p = fmaf(t, p, 0.27886807f);
+  p = fmaf(t, p, -0.18628806f);
+  p = fmaf(t, p, 0.09678418f);
+  p = fmaf(t, p, 0.37409196f);
+  p = fmaf(t, p, 1.00002368f);
+  p = fmaf(t, p, -1.26551223f);
+  p = fmaf(-z, z, p);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p * kLog2e));
+  const float h = 0.5f * t * e;  // erfc(|x| / sqrt 2) / 2
+  return x < 0.0f ? h * x : fmaf(-h, fminf(x, 3.4028234663852886e38f), x);  // (an infinity stays: h is 0)
 }
 template <int N>
 __device__ __forceinline__ void activate(float (&v)[N], int act) {
@@ -96,19 +134,70 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
       break;
     case W8A8_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = times_sigmoid(v[i], v[i]);
+      for (int i = 0; i < N; ++i) v[i] = silu(v[i]);
       break;
-    case W8A8_ACT_GELU:  // x Phi(x) = x erfc(-x / sqrt 2) / 2, which keeps its digits far below zero
+    case W8A8_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * erfcf(v[i] * -0.70710678118654752f);
+      for (int i = 0; i < N; ++i) v[i] = gelu(v[i]);
       break;
-    case W8A8_ACT_GELU_TANH:  // (1 + tanh u) / 2 = sigmoid(2u)
+    case W8A8_ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        v[i] = times_sigmoid(v[i], 1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
+      for (int i = 0; i < N; ++i) v[i] = gelu_tanh(v[i]);
       break;
     default: break;
   }
+}
+
+// Wait of a whole converged warp, bounded as wait_all; a probe sleeps in hardware for up to 20 us before it comes back:
+// a role that waits for a whole tile, polled without the hint, costs power that the tensor cores then lack (8192 x 14336
+// x 4096 without a pause: 3 %).
+__device__ __forceinline__ bool probe(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0u;
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, DeviceStatus* st,
+                                         uint32_t where) {
+  if (__all_sync(0xffffffffu, probe(bar, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!__all_sync(0xffffffffu, probe(bar, parity))) {
+    const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
+    if (__any_sync(0xffffffffu, late || *abort_flag)) {
+      if ((threadIdx.x & 31) == 0 && !*abort_flag) {
+        *abort_flag = 1;
+        set_status(st, W8A8_ERR_DEVICE_TIMEOUT, where);
+      }
+      return false;
+    }
+  }
+  return true;
+}
+
+// 16 columns of the warp's lanes to tensor memory.
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+
+// The cluster's CTAs meet.  Relaxed: no data rides on it (barriers' initialisation has its own fence, and what a CTA
+// stored for others to read in global memory is complete when the grid is), so nobody waits for stores on their way.
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Shared memory of this CTA to that of a CTA of the cluster, whose barrier counts the bytes (cluster-window addresses).
+__device__ __forceinline__ void copy_to_peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "r"(src),
+      "r"(bytes), "r"(bar)
+      : "memory");
 }
 
 // One unit of work: the tile and its K range.
@@ -142,23 +231,34 @@ struct Place {
   int bar;            // gated: the two warps' barrier
 };
 
+// The residual's values that finish() adds, asked for one step ahead.
+template <bool GATED>
+struct Residual {
+  static constexpr int kSlots = GATED ? 1 : 2;  // rows a lane stores
+  uint4 v[kSlots];
+};
+template <bool GATED>
+__device__ __forceinline__ void fetch_residual(const BArgs& a, const Place& p, Residual<GATED>& res, int64_t row,
+                                               int rows, int64_t n0, int ncols) {
+  if (a.residual == nullptr || !a.vec) return;
+  const int c = (p.lane & 3) * 8;
+  const int r0 = (p.lane >> 2) + (GATED ? 8 * (p.q >> 1) : 0);
+#pragma unroll
+  for (int i = 0; i < Residual<GATED>::kSlots; ++i)
+    if (r0 + 8 * i < rows && c < ncols)
+      res.v[i] = *reinterpret_cast<const uint4*>(a.residual + (row + r0 + 8 * i) * a.N + n0 + c);
+}
+
 // 16 tokens x 32 channels: v[i] is this lane's channel of token i.  `rows` of the tokens exist and go to rows row..
 // of y, at channels n0 .. n0 + ncols.
 template <bool GATED>
-__device__ __forceinline__ void finish(const BArgs& a, const Place& p, float (&v)[16], float bias, int64_t row, int rows,
-                                       int64_t n0, int ncols) {
-  constexpr int kSlots = GATED ? 1 : 2;  // rows a lane stores
+__device__ __forceinline__ void finish(const BArgs& a, const Place& p, float (&v)[16], float bias,
+                                       const Residual<GATED>& res, int64_t row, int rows, int64_t n0, int ncols) {
+  constexpr int kSlots = Residual<GATED>::kSlots;
   const int lane = p.lane;
   const int c = (lane & 3) * 8;
   const int r0 = (lane >> 2) + (GATED ? 8 * (p.q >> 1) : 0);
-  uint4 res[kSlots];
   const bool add = a.residual != nullptr;
-  if (add && a.vec) {  // on their way while the activation is computed
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      if (r0 + 8 * i < rows && c < ncols)
-        res[i] = *reinterpret_cast<const uint4*>(a.residual + (row + r0 + 8 * i) * a.N + n0 + c);
-  }
   if (a.bias != nullptr) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] += bias;
@@ -183,10 +283,10 @@ __device__ __forceinline__ void finish(const BArgs& a, const Place& p, float (&v
           const float4 t0 = *reinterpret_cast<const float4*>(t), t1 = *reinterpret_cast<const float4*>(t + 4);
           const float u[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
 #pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] = times_sigmoid(o[k], o[k]) * u[k];
+          for (int k = 0; k < 8; ++k) o[k] = silu(o[k]) * u[k];
         }
         if (add) {
-          const uint32_t w[4] = {res[i].x, res[i].y, res[i].z, res[i].w};
+          const uint32_t w[4] = {res.v[i].x, res.v[i].y, res.v[i].z, res.v[i].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             o[2 * k] += __uint_as_float(w[k] << 16);
@@ -210,7 +310,7 @@ __device__ __forceinline__ void finish(const BArgs& a, const Place& p, float (&v
     for (int r = first; r < last; ++r) {
       if (lane < ncols) {
         float o = GATED ? p.gate[r * B_LD + lane] : p.stg[r * B_LD + lane];
-        if constexpr (GATED) o = times_sigmoid(o, o) * p.up[r * B_LD + lane];
+        if constexpr (GATED) o = silu(o) * p.up[r * B_LD + lane];
         const int64_t at = (row + r) * a.N + n0 + lane;
         if (add) o += bf16_bits_to_f32(a.residual[at]);
         if (a.f32) static_cast<float*>(a.y)[at] = o;
@@ -235,8 +335,8 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   __shared__ uint32_t s_tmem_base;
   __shared__ volatile int s_abort;
   __shared__ int s_bad;
-  __shared__ int s_prefix[F_MAX_E + 1];
-  __shared__ int s_off[F_MAX_E + 1];
+  __shared__ __align__(8) uint64_t bar_alloc;              // even CTA: both CTAs hold their tensor memory
+  __shared__ __align__(8) uint64_t bar_recv[F_EPI_WARPS];  // the parts' sums for the warp are there
   __shared__ int s_warp[B_THREADS / 32];
   __shared__ unsigned long long s_rows;  // the counts' sum where 32 bits may not hold it
 
@@ -253,6 +353,10 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   const uint32_t stage_base = smem_u32(stages);
   float* s_part = reinterpret_cast<float*>(stages);  // [epilogue warp][token][channel], after the last block
   float* s_stg = reinterpret_cast<float*>(stages + C::kStages * C::kStageBytes);
+  const int nstages = a.split > 1 && NT <= 128 ? C::kRingShared : C::kStages;
+  float* s_recv = reinterpret_cast<float*>(stages + (NT <= 128 ? C::kRingShared : 0) * C::kStageBytes);
+  int* s_prefix = reinterpret_cast<int*>(s_stg + F_EPI_WARPS * B_STG_FLOATS);  // [E + 1]
+  int* s_off = s_prefix + E + 1;                                               // [E + 1]
   // CTAs 2i and 2i + 1 of a cluster are a pair; rank: the CTA's place in it
   uint32_t crank, cluster_id, nclusters;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(crank));
@@ -273,48 +377,78 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       mbar_init(smem_u32(&bar_accf[b]), 1);
       mbar_init(smem_u32(&bar_acce[b]), 2 * F_EPI_WARPS);
     }
+    mbar_init(smem_u32(&bar_alloc), 2);
+    for (int w = 0; w < F_EPI_WARPS; ++w) mbar_init(smem_u32(&bar_recv[w]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmXbig);
-    tma_prefetch_desc(&tmXsmall);
+    if (grouped) tma_prefetch_desc(&tmXsmall);
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem_base)),
-                 "r"(F_TMEM_COLS)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
-  __syncthreads();  // s_bad, before the scan may set it
-  pdl_trigger();
-  pdl_wait();
-  int units;
+  int units = 0, rows_total = 0;
   const int dense_blocks = a.blocks;
   auto blocks_of = [grouped, dense_blocks](int cnt) { return grouped ? (cnt + NT - 1) / NT : dense_blocks; };
-  const int rows_total = scan_checked<B_THREADS>(
-      a, [WB, blocks_of](int c) { return blocks_of(c) * WB; }, s_off, s_prefix, s_warp, &s_bad, &s_rows, &units);
-  tc_fence_before();
-  cluster_sync_all();  // both CTAs' barriers and tensor memory exist before either touches the other's
-  tc_fence_after();
-  const uint32_t tmem_base = static_cast<uint32_t>(uni(static_cast<int>(s_tmem_base)));
-  if (bad_list(a, rows_total, s_bad, s_rows)) {
-    if (tid == 0 && blockIdx.x == 0) set_status(a.status, W8A8_ERR_GROUP_LIST, 0u);
-    units = 0;
-  }
+  auto scan = [&] {
+    rows_total = scan_checked<B_THREADS>(
+        a, [WB, blocks_of](int c) { return blocks_of(c) * WB; }, s_off, s_prefix, s_warp, &s_bad, &s_rows, &units);
+  };
+  if (!grouped) scan();  // reads nothing from memory
+  __syncthreads();
+  pdl_trigger();
+  cluster_meet();  // the CTAs' barriers exist before any touches another's
   // units first, first + step, ..; blocks [kb0, kb1) of each
   const int part = static_cast<int>(crank >> 1);
   const int first = static_cast<int>(cluster_id);
   const int step = static_cast<int>(nclusters);
   const int kb0 = KB * part / a.split, kb1 = KB * (part + 1) / a.split;
+  const int chunk = a.chunk;
+  const int nacc = NT == 256 && chunk < KB ? 1 : C::kAcc;
   auto unit_of = [&](int unit) {
     Unit u;
     int tb, cnt, TB;
-    unit_tile(unit, E, WB, s_prefix, s_off, blocks_of, u.e, u.wb, tb, cnt, TB);
+    unit_tile<B_SUPER>(unit, E, WB, s_prefix, s_off, blocks_of, u.e, u.wb, tb, cnt, TB);
     const int per = grouped ? ((cnt + TB - 1) / TB + 15) & ~15 : a.per;  // tokens split evenly over the blocks
     u.row0 = s_off[u.e] + tb * per;
     u.tvalid = min(per, cnt - tb * per);
     u.n = (u.tvalid + 15) & ~15;
     return u;
   };
+
+  // rows of the weight that the CTA reads for a unit: from w_row (gated: the gate's, the up projection's N further on)
+  auto w_row = [&](const Unit& u) {
+    return static_cast<int>(GATED ? static_cast<int64_t>(u.e) * 2 * a.N + static_cast<int64_t>(u.wb) * 128 + rank * 64
+                                  : static_cast<int64_t>(u.e) * a.N + static_cast<int64_t>(u.wb) * 256 + rank * 128);
+  };
+  Unit u0 = {};  // the first unit, worked out while the kernel in front still runs
+  if (!grouped && first < units) u0 = unit_of(first);
+  pdl_wait();
+  if (grouped) {
+    scan();
+    __syncthreads();
+    if (bad_list(a, rows_total, s_bad, s_rows)) {
+      if (tid == 0 && blockIdx.x == 0) set_status(a.status, W8A8_ERR_GROUP_LIST, 0u);
+      units = 0;
+    }
+    if (first < units) u0 = unit_of(first);
+  }
+  // Tensor memory is asked for after the wait: a kernel in front that has not got its own yet is never waited for by
+  // a CTA that holds some.
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem_base)),
+                 "r"(C::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    tc_fence_before();
+    __syncwarp();
+    asm volatile("bar.arrive 15, 288;" ::: "memory");  // the epilogue warps of this CTA
+    if (lane == 0)
+      asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                       smem_cluster_addr(smem_u32(&bar_alloc), even))
+                   : "memory");
+  } else if (warp >= B_EPI0) {
+    asm volatile("bar.sync 15, 288;" ::: "memory");
+  }
+  tc_fence_after();
+  const uint32_t tmem_base = warp == 0 ? 0u : static_cast<uint32_t>(uni(static_cast<int>(s_tmem_base)));
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
@@ -324,20 +458,18 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     bool ok = true;
     const int xbig = uni(a.xbig), xsmall = uni(a.xsmall);
     for (int unit = first; ok && unit < units; unit += step) {
-      const Unit u = unit_of(unit);
-      const int64_t w0 = GATED ? static_cast<int64_t>(u.e) * 2 * a.N + static_cast<int64_t>(u.wb) * 128 + rank * 64
-                               : static_cast<int64_t>(u.e) * a.N + static_cast<int64_t>(u.wb) * 256 + rank * 128;
-      const int yw = uni(static_cast<int>(w0)), yu = uni(static_cast<int>(w0 + a.N));
+      const Unit u = unit == first ? u0 : unit_of(unit);
+      const int yw = uni(w_row(u)), yu = uni(yw + static_cast<int>(a.N));
       const int rows = u.n >> 1;
       const int small = (rows + xsmall - 1) / xsmall;  // loads of the small box that the rows would take
-      const bool few = uni(small <= 3 && rows < xbig);
+      const bool few = uni(grouped && small <= 3 && rows < xbig);
       const int loads = few ? uni(small) : 1;
       const int box = few ? xsmall : xbig;
       const CUtensorMap* tmX = few ? &tmXsmall : &tmXbig;
       const int yx = uni(u.row0 + static_cast<int>(rank) * rows);
       const uint32_t bytes = 2u * B_W_BYTES + static_cast<uint32_t>(2 * loads * box) * (B_BK * 2);
       for (int kb = kb0; kb < kb1; ++kb) {
-        ok = wait_all(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 1u);
+        ok = wait_for(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 1u);
         if (!ok) break;
         if (rank == 0) expect_tx_elect(smem_u32(&bar_full[0]) + 8 * stage, bytes);
         const uint32_t full = full_even0 + 8 * stage;
@@ -346,7 +478,7 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         if constexpr (GATED) tma_pair_elect(dst + B_W_BYTES / 2, &tmW, kb * B_BK, yu, full);
         for (int i = 0; i < loads; ++i)
           tma_pair_elect(dst + B_W_BYTES + i * box * (B_BK * 2), tmX, kb * B_BK, yx + i * box, full);
-        if (++stage == C::kStages) {
+        if (++stage == nstages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -354,9 +486,9 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     }
     // Drain: the last fill of every stage has been consumed, so no copy into this CTA and no MMA arrival on its
     // barriers is still in flight when the cluster leaves.
-    for (int i = 0; i < C::kStages && ok; ++i) {
-      ok = wait_all(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 5u);
-      if (++stage == C::kStages) {
+    for (int i = 0; i < nstages && ok; ++i) {
+      ok = wait_for(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 5u);
+      if (++stage == nstages) {
         stage = 0;
         phase ^= 1u;
       }
@@ -366,33 +498,36 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     if (rank == 0) {
       int stage = 0, buf = 0;
       uint32_t phase = 0, bphase = 0;
-      bool ok = true;
+      bool ok = wait_for(smem_u32(&bar_alloc), 0u, &s_abort, a.status, 7u);
       for (int unit = first; ok && unit < units; unit += step) {
-        const uint32_t idesc = idesc_bf16(uni(unit_of(unit).n));
-        ok = wait_all(smem_u32(&bar_acce[buf]), bphase ^ 1u, &s_abort, a.status, 2u);
-        if (!ok) break;
-        const uint32_t acc = tmem_base + buf * NT;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          ok = wait_all(smem_u32(&bar_full[stage]), phase, &s_abort, a.status, 3u);
+        const uint32_t idesc = idesc_bf16(uni((unit == first ? u0 : unit_of(unit)).n));
+        for (int c0 = kb0; ok && c0 < kb1; c0 += chunk) {
+          ok = wait_for(smem_u32(&bar_acce[buf]), bphase ^ 1u, &s_abort, a.status, 2u);
           if (!ok) break;
-          tc_fence_after();
-          const uint32_t sa = stage_base + stage * C::kStageBytes;
-          const uint64_t adesc = smem_desc_sw128(sa);
-          const uint64_t bdesc = smem_desc_sw128(sa + B_W_BYTES);
+          const uint32_t acc = tmem_base + buf * NT;
+          const int c1 = min(kb1, c0 + chunk);
+          for (int kb = c0; kb < c1; ++kb) {
+            ok = wait_for(smem_u32(&bar_full[stage]), phase, &s_abort, a.status, 3u);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sa = stage_base + stage * C::kStageBytes;
+            const uint64_t adesc = smem_desc_sw128(sa);
+            const uint64_t bdesc = smem_desc_sw128(sa + B_W_BYTES);
 #pragma unroll
-          for (int k = 0; k < B_BK / 16; ++k)
-            tc_mma_pair(acc, adesc + 2u * k, bdesc + 2u * k, idesc, kb > kb0 || k > 0 ? 1u : 0u);
-          tc_commit_pair_mc(smem_u32(&bar_empty[stage]), pair_mask);  // frees the stage in both CTAs
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
+            for (int k = 0; k < B_BK / 16; ++k)
+              tc_mma_pair(acc, adesc + 2u * k, bdesc + 2u * k, idesc, kb > c0 || k > 0 ? 1u : 0u);
+            tc_commit_pair_mc(smem_u32(&bar_empty[stage]), pair_mask);  // frees the stage in both CTAs
+            if (++stage == nstages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-        }
-        if (!ok) break;
-        tc_commit_pair_mc(smem_u32(&bar_accf[buf]), pair_mask);
-        if (++buf == C::kAcc) {
-          buf = 0;
-          bphase ^= 1u;
+          if (!ok) break;
+          tc_commit_pair_mc(smem_u32(&bar_accf[buf]), pair_mask);
+          if (++buf == nacc) {
+            buf = 0;
+            bphase ^= 1u;
+          }
         }
       }
     }
@@ -424,7 +559,7 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     int buf = 0;
     uint32_t bphase = 0;
     for (int unit = first; unit < units; unit += step) {
-      const Unit u = unit_of(unit);
+      const Unit u = unit == first ? u0 : unit_of(unit);
       // the first half's warps read tokens [0, cut), the second's [cut, n)
       const int n = uni(u.n);
       const int cut = ((n >> 1) + 15) & ~15;
@@ -434,79 +569,98 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       const int64_t n0 = static_cast<int64_t>(u.wb) * kRows + c_tile;
       const int ncols = static_cast<int>(min(static_cast<int64_t>(32), a.N - n0));  // (may be <= 0)
       const bool works = uni(tv > 0 && ncols > 0);
-      const float bias = bias_of(u, n0);
-      bool ok = wait_all(smem_u32(&bar_accf[buf]), bphase, &s_abort, a.status, 4u);
-      if constexpr (GATED) ok = pair_and(p.bar, ok);  // the two warps of a pair give up together
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t here = lane_addr + buf * NT + c0, release = acce_even + 8u * buf;
-      if (++buf == C::kAcc) {
-        buf = 0;
-        bphase ^= 1u;
-      }
-      if (!works) {
-        tc_fence_before();
-        arrive_lane0(release, lane);
-        continue;
-      }
+      const float bias = works ? bias_of(u, n0) : 0.0f;
+      const int64_t row0 = static_cast<int64_t>(u.row0) + c0;
+      Residual<GATED> res;
+      // the tokens that the warp finishes: all of its own, or its part's share of them
+      const int t0 = uni(a.split > 1 ? max(tv, 0) * part / a.split : 0);
+      const int t1 = uni(a.split > 1 ? max(tv, 0) * (part + 1) / a.split : tv);
+      if (works && t0 < t1) fetch_residual(a, p, res, row0 + t0, min(16, t1 - t0), n0, ncols);
       float* part_at = s_part + ew * C::kCols * 32 + lane;
-      for (int t = 0; t < tv; t += 16) {
-        uint32_t r[16];
-        tmem_fetch(here + t, r);
-        tmem_ready(r);
-        if (t + 16 >= tv) {
+      const uint32_t sum_at = lane_addr + C::kSumCol + c0;
+      bool ok = true;
+      for (int k0 = kb0; k0 < kb1; k0 += chunk) {
+        ok = wait_for(smem_u32(&bar_accf[buf]), bphase, &s_abort, a.status, 4u);
+        if constexpr (GATED) ok = pair_and(p.bar, ok);  // the two warps of a pair give up together
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t here = lane_addr + buf * NT + c0, release = acce_even + 8u * buf;
+        if (++buf == nacc) {
+          buf = 0;
+          bphase ^= 1u;
+        }
+        if (!works) {
           tc_fence_before();
           arrive_lane0(release, lane);
+          continue;
         }
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-        if (a.split > 1) {  // a part of K of the cluster's unit: its sums to the ring, which is at rest
-#pragma unroll
-          for (int i = 0; i < 16; ++i) part_at[(t + i) * 32] = v[i];
-        } else {
-          finish<GATED>(a, p, v, bias, static_cast<int64_t>(u.row0) + c0 + t, min(16, tv - t), n0, ncols);
-        }
-      }
-    }
-  }
-
-  if (a.split > 1) {
-    // the parts' sums meet: every CTA adds its share of the tokens over its peers' shared memory, in the order of K
-    __syncwarp();
-    cluster_sync_all();
-    if (warp >= B_EPI0 && first < units) {
-      const Unit u = unit_of(first);
-      const int cut = ((u.n >> 1) + 15) & ~15;
-      const int c0 = p.h == 0 ? 0 : cut;
-      const int tv = uni(min(p.h == 0 ? cut : u.n - cut, u.tvalid - c0));
-      const int64_t n0 = static_cast<int64_t>(u.wb) * kRows + c_tile;
-      const int ncols = static_cast<int>(min(static_cast<int64_t>(32), a.N - n0));
-      if (uni(tv > 0 && ncols > 0)) {
-        const int t1 = tv * (part + 1) / a.split;
-        const float bias = bias_of(u, n0);
-        const uint32_t src = smem_u32(s_part + ew * C::kCols * 32 + lane);
-        for (int t = tv * part / a.split; t < t1; t += 16) {
+        const bool more = k0 > kb0, last = k0 + chunk >= kb1;
+        for (int t = 0; t < tv; t += 16) {
+          uint32_t r[16], s[16];
+          tmem_fetch(here + t, r);
+          if (more) tmem_fetch(sum_at + t, s);
+          tmem_ready(r);
+          if (t + 16 >= tv) {
+            tc_fence_before();
+            arrive_lane0(release, lane);
+          }
           float v[16];
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            float w[F_MAX_SPLIT][4];
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+          if (more) {
+            tmem_ready(s);
 #pragma unroll
-            for (int j = 0; j < F_MAX_SPLIT; ++j) {  // every peer's words in flight, added in order
-              const uint32_t q = smem_cluster_addr(src, 2 * min(j, a.split - 1) + rank) + (t + i) * 128;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) w[j][k] = j < a.split && t + i + k < t1 ? ld_cluster(q + k * 128) : 0.0f;
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[i + k] = w[0][k];
-#pragma unroll
-            for (int j = 1; j < F_MAX_SPLIT; ++j)
-              if (j < a.split) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[i + k] += w[j][k];
-              }
+            for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(s[i]);
           }
-          finish<GATED>(a, p, v, bias, static_cast<int64_t>(u.row0) + c0 + t, min(16, t1 - t), n0, ncols);
+          if (!last) {
+            tmem_store(sum_at + t, v);
+          } else if (a.split > 1) {  // a part of K of the cluster's unit: its sums to the ring, which is at rest
+#pragma unroll
+            for (int i = 0; i < 16; ++i) part_at[(t + i) * 32] = v[i];
+          } else {
+            Residual<GATED> next;
+            if (t + 16 < tv) fetch_residual(a, p, next, row0 + t + 16, min(16, tv - t - 16), n0, ncols);
+            finish<GATED>(a, p, v, bias, res, row0 + t, min(16, tv - t), n0, ncols);
+            res = next;
+          }
+        }
+        if (!last) tmem_wait_st();
+      }
+      if (!ok) break;
+      if constexpr (NT <= 128) {
+        if (a.split > 1 && works) {
+          // the parts' sums meet: each goes out to the CTAs that add a share of the tokens each, in the order of K
+          const int cap = (C::kCols + a.split - 1) / a.split;  // tokens of a share, at most
+          const uint32_t bar = smem_u32(&bar_recv[ew]);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane < a.split) {
+            const int from = tv * lane / a.split, to = tv * (lane + 1) / a.split;
+            const uint32_t peer = 2 * lane + rank;
+            if (to > from)
+              copy_to_peer(smem_cluster_addr(smem_u32(s_recv + (part * F_EPI_WARPS + ew) * cap * 32), peer),
+                           smem_u32(s_part + (ew * C::kCols + from) * 32), static_cast<uint32_t>(to - from) * 128u,
+                           smem_cluster_addr(bar, peer));
+          }
+          __syncwarp();
+          if (t0 < t1) {
+            expect_tx_elect(bar, static_cast<uint32_t>(a.split * (t1 - t0)) * 128u);
+            ok = wait_for(bar, 0u, &s_abort, a.status, 6u);
+          }
+          if constexpr (GATED) ok = pair_and(p.bar, ok);
+          if (!ok) break;
+          const float* in = s_recv + ew * cap * 32 + lane;
+          for (int t = t0; t < t1; t += 16) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+            for (int j = 0; j < a.split; ++j)
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (t + i < t1) v[i] += in[(j * F_EPI_WARPS * cap + t - t0 + i) * 32];
+            if (t > t0) fetch_residual(a, p, res, row0 + t, min(16, t1 - t), n0, ncols);
+            finish<GATED>(a, p, v, bias, res, row0 + t, min(16, t1 - t), n0, ncols);
+          }
         }
       }
     }
@@ -521,11 +675,11 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     while (globaltimer_ns() - t0 < 20000000ull) {
     }
   }
-  cluster_sync_all();
+  cluster_meet();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(F_TMEM_COLS)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::kTmemCols)
                  : "memory");
   }
 }
@@ -536,8 +690,8 @@ struct BPlan {
 constexpr int round16(int64_t n) { return static_cast<int>((n + 15) & ~int64_t(15)); }
 
 // Cycles of one 64-deep block of a tile of n tokens: the tensor core's (four MMAs of n / 2, at least 40), or bringing
-// 128 weight rows and n / 2 token rows of 128 bytes to a SM at about 60 bytes a cycle.
-constexpr int64_t block_cost(int n) { return std::max(2 * n, std::max(160, (128 + n / 2) * 128 / 60)); }
+// 128 weight rows and n / 2 token rows of 128 bytes to a SM at about 58 bytes a cycle.
+constexpr int64_t block_cost(int n) { return std::max(2 * n, (128 + n / 2) * 128 / 58); }
 
 BPlan make_plan(int64_t E, int64_t R, int64_t channel_blocks, int64_t K, bool grouped) {
   BPlan p{256, 0, 0, 1, F_MAX_CLUSTERS};
@@ -556,7 +710,7 @@ BPlan make_plan(int64_t E, int64_t R, int64_t channel_blocks, int64_t K, bool gr
     const int64_t blocks = (R + per - 1) / per;
     const int64_t units = blocks * channel_blocks;
     for (int ks = 1; ks <= F_MAX_SPLIT; ++ks) {
-      if (ks > 1 && (units > kFit[ks] || 2 * ks > KB)) continue;
+      if (ks > 1 && (units > kFit[ks] || 2 * ks > KB || per > 128)) continue;
       const int64_t waves = ks > 1 ? 1 : (units + F_MAX_CLUSTERS - 1) / F_MAX_CLUSTERS;
       const int64_t cost = waves * ((KB + ks - 1) / ks * block_cost(per) + 300) + (ks > 1 ? 1800 + 8 * per : 8 * per);
       if (cost < best) {
@@ -579,13 +733,16 @@ cudaError_t launch_nt(const Bf16GemmArgs& g, const BArgs& a, int pairs, cudaStre
   const auto type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   if (!encode_map_2d(&mw, g.w, type, 2, g.E * g.N * (GATED ? 2 : 1), g.K, B_BK, GATED ? 64 : B_HALF, sw) ||
-      !encode_map_2d(&mb, g.x, type, 2, g.R, g.K, B_BK, a.xbig, sw) ||
-      !encode_map_2d(&ms, g.x, type, 2, g.R, g.K, B_BK, a.xsmall, sw))
+      !encode_map_2d(&mb, g.x, type, 2, g.R, g.K, B_BK, a.xbig, sw))
     return cudaErrorInvalidValue;
+  if (g.group_list == nullptr) ms = mb;  // not used
+  else if (!encode_map_2d(&ms, g.x, type, 2, g.R, g.K, B_BK, a.xsmall, sw)) return cudaErrorInvalidValue;
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(bf16_gemm_kernel<NT, GATED>), C::kSmem, ready);
+  constexpr size_t kMost = C::kSmem + (F_MAX_E + 1) * 8;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(bf16_gemm_kernel<NT, GATED>), kMost, ready);
   if (e != cudaSuccess) return e;
-  return launch_pairs(bf16_gemm_kernel<NT, GATED>, pairs, a.split, B_THREADS, C::kSmem, stream, mw, mb, ms, a);
+  return launch_pairs(bf16_gemm_kernel<NT, GATED>, pairs, a.split, B_THREADS, C::kSmem + (a.E + 1) * 8, stream, mw, mb,
+                      ms, a);
 }
 
 template <bool GATED>
@@ -620,6 +777,9 @@ cudaError_t launch_bf16_gemm(const Bf16GemmArgs& g, cudaStream_t stream) {
   a.split = p.split;
   a.blocks = p.blocks;
   a.per = p.per;
+  // An accumulator's additions truncate: over the whole of K a sum comes out low by about K * 2^-30 of itself (7168:
+  // 7.9e-6).  bf16 outputs round 2^-9 away; for fp32 ones an accumulator takes 512 of K.
+  a.chunk = g.f32 ? 8 : 1 << 20;
   a.xbig = (grouped ? p.nt : p.per) / 2;
   a.xsmall = std::max(8, (a.xbig / 4 + 7) & ~7);
   a.f32 = g.f32;
