@@ -477,7 +477,7 @@ def moe_layer(x: torch.Tensor, x_scale: Optional[torch.Tensor], topk_ids: torch.
 
 _bound = {}
 _raw_stream = _get_device = None  # torch's own, looked up with the first function: a torch without CUDA lacks them
-_empty, _Tensor = torch.empty, torch.Tensor
+_empty, _empty_like, _Tensor = torch.empty, torch.empty_like, torch.Tensor
 _BF16, _F32, _I64, _E4M3 = torch.bfloat16, torch.float32, torch.int64, torch.float8_e4m3fn
 
 
@@ -781,37 +781,41 @@ def moe_fp8_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.T
 
 def _rms_norm(name, x, weight, eps, residual, want_y, q, scale, residual_out, y, q_dtype, s_dtype, s_cols):
     M, K = _dims(x, "x", 2)
-    dev = x.get_device()
+    dev, device = x.get_device(), x.device
     if not (dev >= 0 and x.dtype is _BF16 and x.is_contiguous()):
         _check(x, "x", _BF16, (M, K), dev)
     f32 = type(weight) is _Tensor and weight.dtype is _F32
     _check(weight, "weight", _F32 if f32 else _BF16, (K,), dev)
+    r_ptr = out_ptr = y_ptr = None
     if residual is not None:
         _check(residual, "residual", _BF16, (M, K), dev)
+        r_ptr = residual.data_ptr()
         if residual_out is None:
-            residual_out = _empty((M, K), dtype=_BF16, device=x.device)
+            residual_out = _empty_like(residual)
         else:
             _check(residual_out, "residual_out", _BF16, (M, K), dev)
+        out_ptr = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if y is not None:
         _check(y, "y", _BF16, (M, K), dev)
+        y_ptr = y.data_ptr()
     elif want_y:
-        y = _empty((M, K), dtype=_BF16, device=x.device)
+        y = _empty_like(x)
+        y_ptr = y.data_ptr()
     if q is None:
-        q = _empty((M, K), dtype=q_dtype, device=x.device)
+        q = _empty((M, K), dtype=q_dtype, device=device)
     elif q_dtype is _E4M3:
         _check_e4m3(q, "q", (M, K), dev)
     else:
         _check(q, "q", q_dtype, (M, K), dev)
-    shape = (M,) if s_cols is None else (M, -(-K // s_cols))
+    shape = (M,) if s_cols == 0 else (M, (K + s_cols - 1) // s_cols)
     if scale is None:
-        scale = _empty(shape, dtype=s_dtype, device=x.device)
+        scale = _empty(shape, dtype=s_dtype, device=device)
     else:
         _check(scale, "scale", s_dtype, shape, dev)
-    _call(name, dev, x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), M, K, eps,
-          _capi.NORM_WEIGHT_F32 if f32 else 0, None if residual_out is None else residual_out.data_ptr(),
-          None if y is None else y.data_ptr(), q.data_ptr(), scale.data_ptr())
+    _call(name, dev, x.data_ptr(), r_ptr, weight.data_ptr(), M, K, eps, 1 if f32 else 0, out_ptr, y_ptr, q.data_ptr(),
+          scale.data_ptr())
     return q, scale, residual_out, y
 
 
@@ -825,7 +829,7 @@ def w8a8_rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6
     r = bf16(x + residual), or None without a residual; the norm is of r.  y: the norm in bf16 where want_y (or a
     tensor `y`) asks for it, else None.  residual_out may be x or residual itself: the residual stream in place."""
     return _rms_norm("w8a8_rms_norm_quant", x, weight, eps, residual, want_y, q, scale, residual_out, y, torch.int8,
-                     _F32, None)
+                     _F32, 0)
 
 
 def w8a8_fp8_rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,

@@ -76,6 +76,75 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// max of |a|, |b| and |c|; NaN if one is.
+__device__ __forceinline__ float max_abs3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// The same, a NaN passed over.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Two bf16 of a word, widened.
+__device__ __forceinline__ uint64_t wide2(uint32_t w) {
+  return pk(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// The sum of the squares of a thread's values as s + e.  The sum starts at B, a power of two above the largest square,
+// and B is taken off at the end (exact: s - B is a smaller multiple of what s's last place holds).  A sum that is never
+// smaller than what is added gives its rounding error in two operations (Dekker, "A floating-point technique for
+// extending the available precision", 1971), the second an fma since squares are exact; any order of magnitudes takes six.
+template <int CH>
+__device__ __forceinline__ void sum_squares(const uint4 (&v)[CH], float& s, float& e) {
+  uint32_t top = 0u;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const uint32_t q[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(q[i]));
+  }
+  const float m = max_nan(__uint_as_float((top << 16) & 0x7fff0000u), __uint_as_float(top & 0x7fff0000u));
+  const float above = __uint_as_float((__float_as_uint(m) & 0x7f800000u) + 0x00800000u);  // 2^k > m
+  const float B = __fmul_rn(above, above);
+  if (m < 0x1p59f) {
+    uint64_t s2 = pk(B, B), c2 = 0ull;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const uint32_t q[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t r = wide2(q[i]), t = fma2(r, r, s2);
+        c2 = add2(c2, fma2(r, r, sub2(s2, t)));
+        s2 = t;
+      }
+    }
+    float s1, e1;
+    upk(s2, s, s1);
+    upk(c2, e, e1);
+    s = __fsub_rn(s, B);
+    s1 = __fsub_rn(s1, B);
+    two_sum(s, e, s1);
+    e = __fadd_rn(e, e1);
+  } else {  // squares near the top of binary32 or above it, infinities and NaNs
+    uint64_t s2 = 0ull, c2 = 0ull;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const uint32_t q[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) two_sum2(s2, c2, mul2(wide2(q[i]), wide2(q[i])));
+    }
+    float s1, e1;
+    upk(s2, s, s1);
+    upk(c2, e, e1);
+    two_sum(s, e, s1);
+    e = __fadd_rn(e, e1);
+  }
+}
+
 // 16 bytes read once.  Not the read-only path: residual_out may be x or residual itself.
 __device__ __forceinline__ uint4 ld_once(const uint4* p) {
   uint4 r;
@@ -101,6 +170,17 @@ __device__ __forceinline__ uint64_t quotient2(uint64_t nv, uint64_t nrs, uint64_
   return fma2(fma2(y, s, nv), nrs, y);
 }
 __device__ __forceinline__ bool plain_scale(float s) { return s >= 0x1p-100f && s <= 0x1p100f; }
+
+// RN(m / 448) for m >= 0, by the same steps with a constant's reciprocal where the remainder cannot underflow.
+__device__ __forceinline__ float over_448(float m) {
+  if (m >= 0x1p-90f && m <= 0x1p120f) {
+    constexpr float kInv = 1.0f / 448.0f;
+    float y = __fmul_rn(m, kInv);
+    y = __fmaf_rn(__fmaf_rn(-y, 448.0f, m), kInv, y);
+    return __fmaf_rn(__fmaf_rn(-y, 448.0f, m), kInv, y);
+  }
+  return __fdiv_rn(m, 448.0f);
+}
 
 // The 8 int8 codes of a chunk of -v.  slow: the row holds a NaN (code 0) or its scale is out of quotient2's range.
 __device__ __forceinline__ uint2 codes_int8(const uint64_t (&nv)[4], float s, float rs, bool slow) {
@@ -186,9 +266,12 @@ __device__ __forceinline__ float group_max(float m, float* red, int grp, int w, 
 }
 
 // FORM: the output.  A group of G warps holds one row, CH chunks of 8 values a thread.
+template <int G>
+constexpr int kCtaWarps = G > 4 ? G : 4;
+
 template <int FORM, int CH, int G>
-__global__ void __launch_bounds__(G > 8 ? 32 * G : 256) norm_quant_kernel(const NormArgs a) {
-  constexpr int kWarps = G > 8 ? G : 8;
+__global__ void __launch_bounds__(32 * kCtaWarps<G>) norm_quant_kernel(const NormArgs a) {
+  constexpr int kWarps = kCtaWarps<G>;
   constexpr int NG = kWarps / G;
   __shared__ float red_s[kWarps], red_c[kWarps], red_m[kWarps], red_n[kWarps];
   pdl_trigger();
@@ -219,31 +302,16 @@ __global__ void __launch_bounds__(G > 8 ? 32 * G : 256) norm_quant_kernel(const 
         uint32_t* p0 = &v[c].x;
         const uint32_t q0[4] = {res[c].x, res[c].y, res[c].z, res[c].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          p0[i] = f32x2_to_bf16x2_bits(
-              __fadd_rn(__uint_as_float(p0[i] << 16), __uint_as_float(q0[i] << 16)),
-              __fadd_rn(__uint_as_float(p0[i] & 0xffff0000u), __uint_as_float(q0[i] & 0xffff0000u)));
+        for (int i = 0; i < 4; ++i)  // one rounding: the same as that of the binary32 sum, which is exact or far from a tie
+          asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(p0[i]) : "r"(q0[i]));
         if (t + 32 * G * c < nchunk) reinterpret_cast<uint4*>(a.residual_out + at)[t + 32 * G * c] = v[c];
       }
     }
   }
 
   // the sum of squares in two words, over the thread, the warp and the group
-  uint64_t s2 = 0ull, c2 = 0ull;
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const uint32_t q0[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint64_t r = pk(__uint_as_float(q0[i] << 16), __uint_as_float(q0[i] & 0xffff0000u));
-      two_sum2(s2, c2, mul2(r, r));
-    }
-  }
-  float s, e, s_hi, e_hi;
-  upk(s2, s, s_hi);
-  upk(c2, e, e_hi);
-  two_sum(s, e, s_hi);
-  e = __fadd_rn(e, e_hi);
+  float s = 0.0f, e = 0.0f;
+  sum_squares<CH>(v, s, e);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float so = __shfl_xor_sync(0xffffffffu, s, o), eo = __shfl_xor_sync(0xffffffffu, e, o);
@@ -269,9 +337,9 @@ __global__ void __launch_bounds__(G > 8 ? 32 * G : 256) norm_quant_kernel(const 
   const float sum = fabsf(s) <= 3.4028234663852886e38f ? __fadd_rn(s, e) : s;
   const float g = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(a.K)), a.eps));
 
-  // -v = (r * g) * -w
+  // -v = (r * -g) * w
   uint64_t f[CH][4];
-  const uint64_t g2 = pk(g, g);
+  const uint64_t ng2 = pk(-g, -g);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int idx = t + 32 * G * c;
@@ -281,20 +349,20 @@ __global__ void __launch_bounds__(G > 8 ? 32 * G : 256) norm_quant_kernel(const 
       if (f32w) {
         const float4 w0 = reinterpret_cast<const float4*>(a.weight)[2 * idx];
         const float4 w1 = reinterpret_cast<const float4*>(a.weight)[2 * idx + 1];
-        wt[0] = pk(-w0.x, -w0.y);
-        wt[1] = pk(-w0.z, -w0.w);
-        wt[2] = pk(-w1.x, -w1.y);
-        wt[3] = pk(-w1.z, -w1.w);
+        wt[0] = pk(w0.x, w0.y);
+        wt[1] = pk(w0.z, w0.w);
+        wt[2] = pk(w1.x, w1.y);
+        wt[3] = pk(w1.z, w1.w);
       } else {
         const uint4 wb = reinterpret_cast<const uint4*>(a.weight)[idx];
-        const uint32_t w4[4] = {wb.x ^ 0x80008000u, wb.y ^ 0x80008000u, wb.z ^ 0x80008000u, wb.w ^ 0x80008000u};
+        const uint32_t w4[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) wt[i] = pk(__uint_as_float(w4[i] << 16), __uint_as_float(w4[i] & 0xffff0000u));
+        for (int i = 0; i < 4; ++i) wt[i] = wide2(w4[i]);
       }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      f[c][i] = mul2(mul2(pk(__uint_as_float(q0[i] << 16), __uint_as_float(q0[i] & 0xffff0000u)), g2), wt[i]);
+      f[c][i] = mul2(mul2(wide2(q0[i]), ng2), wt[i]);
     if (idx >= nchunk) {  // (0 * inf above)
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[c][i] = 0ull;
@@ -319,7 +387,7 @@ __global__ void __launch_bounds__(G > 8 ? 32 * G : 256) norm_quant_kernel(const 
       for (int i = 0; i < 4; ++i) {
         float lo, hi;
         upk(f[c][i], lo, hi);
-        m = max_nan(m, max_nan(fabsf(lo), fabsf(hi)));
+        m = max_abs3_nan(m, lo, hi);
       }
     m = group_max<true, G>(m, red_m + grp * G, grp, w, lane);
     const bool nan = m != m;
@@ -331,7 +399,7 @@ __global__ void __launch_bounds__(G > 8 ? 32 * G : 256) norm_quant_kernel(const 
         for (int i = 0; i < 4; ++i) {
           float lo, hi;
           upk(f[c][i], lo, hi);
-          m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));
+          m = max_abs3(m, lo, hi);
         }
       m = group_max<false, G>(m, red_n + grp * G, grp, w, lane);
     }
@@ -356,13 +424,13 @@ __global__ void __launch_bounds__(G > 8 ? 32 * G : 256) norm_quant_kernel(const 
       for (int i = 0; i < 4; ++i) {
         float lo, hi;
         upk(f[c][i], lo, hi);
-        m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));  // passes a NaN over
+        m = max_abs3(m, lo, hi);  // passes a NaN over
         nan = nan || lo != lo || hi != hi;
       }
 #pragma unroll
       for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       if constexpr (FORM == F_FP8) {
-        const float sc = __fdiv_rn(m, 448.0f);
+        const float sc = over_448(m);
         const uint2 q = codes_fp8(f[c], sc);
         if (idx < nchunk) {
           reinterpret_cast<uint2*>(a.q + at)[idx] = q;
@@ -397,7 +465,7 @@ __global__ void __launch_bounds__(G > 8 ? 32 * G : 256) norm_quant_kernel(const 
 
 template <int FORM, int CH, int G>
 cudaError_t go(const NormArgs& a, cudaStream_t stream) {
-  constexpr int kWarps = G > 8 ? G : 8;
+  constexpr int kWarps = kCtaWarps<G>;
   const int64_t ctas = (a.M + kWarps / G - 1) / (kWarps / G);
   return launch_pdl(norm_quant_kernel<FORM, CH, G>, dim3(static_cast<unsigned>(ctas)), dim3(32 * kWarps), 0, stream, a);
 }
@@ -405,16 +473,21 @@ cudaError_t go(const NormArgs& a, cudaStream_t stream) {
 template <int FORM>
 cudaError_t pick(const NormArgs& a, int num_sms, cudaStream_t stream) {
   const int nchunk = a.K / 8;
-  if (a.M <= 2 * num_sms && nchunk > 256) {  // few rows: one or two a SM, as many threads a row as it has chunks
-    if (nchunk <= 1024) return go<FORM, 1, 32>(a, stream);
-  }
+  // Four chunks a thread where the rows then still fill the GPU (16 warps a SM): a row's reductions are a warp's work,
+  // so fewer warps a row leave fewer instructions.  Else a chunk a thread: the shortest way through a row.
   if (nchunk <= 32) return go<FORM, 1, 1>(a, stream);
-  if (nchunk <= 64) return go<FORM, 1, 2>(a, stream);
-  if (nchunk <= 128) return go<FORM, 1, 4>(a, stream);
-  if (nchunk <= 256) return go<FORM, 1, 8>(a, stream);
-  if (nchunk <= 512) return go<FORM, 2, 8>(a, stream);
+  if (nchunk <= 1024 && a.M * ((nchunk + 127) / 128) < 16 * num_sms) {
+    if (nchunk <= 64) return go<FORM, 1, 2>(a, stream);
+    if (nchunk <= 128) return go<FORM, 1, 4>(a, stream);
+    if (nchunk <= 256) return go<FORM, 1, 8>(a, stream);
+    if (nchunk <= 512) return go<FORM, 1, 16>(a, stream);
+    return go<FORM, 1, 32>(a, stream);
+  }
+  if (nchunk <= 128) return go<FORM, 4, 1>(a, stream);
+  if (nchunk <= 256) return go<FORM, 4, 2>(a, stream);
+  if (nchunk <= 512) return go<FORM, 4, 4>(a, stream);
   if (nchunk <= 1024) return go<FORM, 4, 8>(a, stream);
-  if (nchunk <= 2048) return go<FORM, 2, 32>(a, stream);
+  if (nchunk <= 2048) return go<FORM, 4, 16>(a, stream);
   if (nchunk <= 4096) return go<FORM, 4, 32>(a, stream);
   return go<FORM, 8, 32>(a, stream);
 }
