@@ -92,38 +92,81 @@ __device__ __forceinline__ uint32_t idesc_bf16(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (256u >> 4 << 24);
 }
 
+// Two binary32 values side by side, and paired operations on them.
+__device__ __forceinline__ uint64_t pk(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pk(float both) { return pk(both, both); }
+__device__ __forceinline__ void upk(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // x * sigmoid(z), z2 = z * log2 e: x / (1 + t) for z >= 0 and t x / (1 + t) below, t = exp(-|z|) <= 1, so nothing
 // overflows and far negative values keep what t has (down to 2^-126).
 __device__ __forceinline__ float times_sigmoid(float x, float z2) {
-  float t, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(-fabsf(z2)));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
-  return (z2 < 0.0f ? t * x : x) * r;
+  const float t = exp2_fast(-fabsf(z2));
+  return (z2 < 0.0f ? t * x : x) * rcp_fast(1.0f + t);
 }
-constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float silu(float x) { return times_sigmoid(x, x * kLog2e); }
+__device__ __forceinline__ float silu(float x) { return times_sigmoid(x, x * 1.4426950408889634f); }
 // (1 + tanh u) / 2 = sigmoid(2u), u = sqrt(2 / pi) (x + 0.044715 x^3)
-__device__ __forceinline__ float gelu_tanh(float x) { return times_sigmoid(x, x * fmaf(x * x, 0.10294324f, 2.3022082f)); }
-// x Phi(x) = x erfc(-x / sqrt 2) / 2, which keeps its digits far below zero.  erfc(z) = t exp(-z^2 + P(t)),
-// t = 1 / (1 + z / 2), within a relative 1.2e-7 for z >= 0: the Chebyshev fit of Press, Teukolsky, Vetterling and
-// Flannery, "Numerical Recipes in C" (1992), 6.2 (erfcf: 687 us for 8192 x 14336 x 4096, this 552).
-__device__ __forceinline__ float gelu(float x) {
-  const float z = fabsf(x) * 0.70710678118654752f;
-  float t, e;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.5f, z, 1.0f)));
-  float p = fmaf(t, 0.17087277f, -0.82215223f);
-  p = fmaf(t, p, 1.48851587f);
-  p = fmaf(t, p, -1.13520398f);
-  p = fmaf(t, p, 0.27886807f);
-  p = fmaf(t, p, -0.18628806f);
-  p = fmaf(t, p, 0.09678418f);
-  p = fmaf(t, p, 0.37409196f);
-  p = fmaf(t, p, 1.00002368f);
-  p = fmaf(t, p, -1.26551223f);
-  p = fmaf(-z, z, p);
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p * kLog2e));
-  const float h = 0.5f * t * e;  // erfc(|x| / sqrt 2) / 2
-  return x < 0.0f ? h * x : fmaf(-h, fminf(x, 3.4028234663852886e38f), x);  // (an infinity stays: h is 0)
+__device__ __forceinline__ void gelu_tanh2(float& x0, float& x1) {
+  const uint64_t x = pk(x0, x1), z = mul2(x, fma2(mul2(x, x), pk(0.10294324f), pk(2.3022082f)));
+  float z0, z1;
+  upk(z, z0, z1);
+  x0 = times_sigmoid(x0, z0);
+  x1 = times_sigmoid(x1, z1);
+}
+// x Phi(x) = max(x, 0) - |x| erfc(z) / 2, z = |x| / sqrt 2, which keeps its digits far below zero.  erfc(z) =
+// t exp(-z^2 + P(t)), t = 1 / (1 + z / 2), within a relative 1.2e-7: the Chebyshev fit of Press, Teukolsky, Vetterling
+// and Flannery, "Numerical Recipes in C" (1992), 6.2, here with its coefficients times log2 e and the half in the
+// exponent.  |x| is cut at 2^60, where erfc is 0, so that an infinity is not multiplied by it.
+__device__ __forceinline__ void gelu2(float& x0, float& x1) {
+  constexpr float kL = 1.4426950408889634f;
+  const float a0 = fminf(fabsf(x0), 0x1p60f), a1 = fminf(fabsf(x1), 0x1p60f);
+  const uint64_t a = pk(a0, a1);
+  float d0, d1;
+  upk(fma2(a, pk(0.35355339059327376f), pk(1.0f)), d0, d1);
+  const uint64_t t = pk(rcp_fast(d0), rcp_fast(d1));
+  uint64_t p = fma2(t, pk(0.17087277f * kL), pk(-0.82215223f * kL));
+  p = fma2(t, p, pk(1.48851587f * kL));
+  p = fma2(t, p, pk(-1.13520398f * kL));
+  p = fma2(t, p, pk(0.27886807f * kL));
+  p = fma2(t, p, pk(-0.18628806f * kL));
+  p = fma2(t, p, pk(0.09678418f * kL));
+  p = fma2(t, p, pk(0.37409196f * kL));
+  p = fma2(t, p, pk(1.00002368f * kL));
+  p = fma2(t, p, pk(-1.26551223f * kL - 1.0f));
+  p = fma2(mul2(a, a), pk(-0.5f * kL), p);
+  float p0, p1, h0, h1;
+  upk(p, p0, p1);
+  upk(mul2(mul2(t, pk(exp2_fast(p0), exp2_fast(p1))), a), h0, h1);
+  float m0, m1;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m0) : "f"(x0), "f"(0.0f));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m1) : "f"(x1), "f"(0.0f));
+  x0 = m0 - h0;
+  x1 = m1 - h1;
 }
 template <int N>
 __device__ __forceinline__ void activate(float (&v)[N], int act) {
@@ -138,11 +181,11 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
       break;
     case W8A8_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = gelu(v[i]);
+      for (int i = 0; i < N; i += 2) gelu2(v[i], v[i + 1]);
       break;
     case W8A8_ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = gelu_tanh(v[i]);
+      for (int i = 0; i < N; i += 2) gelu_tanh2(v[i], v[i + 1]);
       break;
     default: break;
   }
@@ -420,8 +463,10 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   };
   Unit u0 = {};  // the first unit, worked out while the kernel in front still runs
   if (!grouped && first < units) u0 = unit_of(first);
-  pdl_wait();
+  // Each role waits for the kernel in front at its first access to memory: what is before it in the code, and the
+  // code's own way into the instruction cache, is behind it then.
   if (grouped) {
+    pdl_wait();
     scan();
     __syncthreads();
     if (bad_list(a, rows_total, s_bad, s_rows)) {
@@ -430,26 +475,6 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     }
     if (first < units) u0 = unit_of(first);
   }
-  // Tensor memory is asked for after the wait: a kernel in front that has not got its own yet is never waited for by
-  // a CTA that holds some.
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem_base)),
-                 "r"(C::kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    tc_fence_before();
-    __syncwarp();
-    asm volatile("bar.arrive 15, 288;" ::: "memory");  // the epilogue warps of this CTA
-    if (lane == 0)
-      asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                       smem_cluster_addr(smem_u32(&bar_alloc), even))
-                   : "memory");
-  } else if (warp >= B_EPI0) {
-    asm volatile("bar.sync 15, 288;" ::: "memory");
-  }
-  tc_fence_after();
-  const uint32_t tmem_base = warp == 0 ? 0u : static_cast<uint32_t>(uni(static_cast<int>(s_tmem_base)));
-
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
     const uint32_t full_even0 = smem_cluster_addr(smem_u32(&bar_full[0]), even);
@@ -468,6 +493,7 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       const CUtensorMap* tmX = few ? &tmXsmall : &tmXbig;
       const int yx = uni(u.row0 + static_cast<int>(rank) * rows);
       const uint32_t bytes = 2u * B_W_BYTES + static_cast<uint32_t>(2 * loads * box) * (B_BK * 2);
+      if (unit == first) pdl_wait();
       for (int kb = kb0; kb < kb1; ++kb) {
         ok = wait_for(smem_u32(&bar_empty[stage]), phase ^ 1u, &s_abort, a.status, 1u);
         if (!ok) break;
@@ -494,8 +520,25 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------- MMA issuer (even CTA, whole warp)
+    // ------------------------------------------------------------- TMEM owner; MMA issuer (even CTA, whole warp)
+    // Tensor memory is asked for after the wait: a kernel in front that has not got its own yet is never waited for by
+    // a CTA that holds some.
+    pdl_wait();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem_base)),
+                 "r"(C::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    tc_fence_before();
+    __syncwarp();
+    asm volatile("bar.arrive 15, 288;" ::: "memory");  // the epilogue warps of this CTA
+    if (lane == 0)
+      asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                       smem_cluster_addr(smem_u32(&bar_alloc), even))
+                   : "memory");
+    __syncwarp();
+    tc_fence_after();
     if (rank == 0) {
+      const uint32_t tmem_base = static_cast<uint32_t>(uni(static_cast<int>(s_tmem_base)));
       int stage = 0, buf = 0;
       uint32_t phase = 0, bphase = 0;
       bool ok = wait_for(smem_u32(&bar_alloc), 0u, &s_abort, a.status, 7u);
@@ -554,6 +597,10 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     return bf16_bits_to_f32(a.bias[u.e * w_rows + (GATED && p.q >= 2 ? a.N : 0) + n0 + lane]);
   };
   if (warp >= B_EPI0) {
+    pdl_wait();
+    asm volatile("bar.sync 15, 288;" ::: "memory");
+    tc_fence_after();
+    const uint32_t tmem_base = static_cast<uint32_t>(uni(static_cast<int>(s_tmem_base)));
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * p.q) << 16);
     const uint32_t acce_even = smem_cluster_addr(smem_u32(&bar_acce[0]), even);
     int buf = 0;
@@ -576,6 +623,16 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       const int t0 = uni(a.split > 1 ? max(tv, 0) * part / a.split : 0);
       const int t1 = uni(a.split > 1 ? max(tv, 0) * (part + 1) / a.split : tv);
       if (works && t0 < t1) fetch_residual(a, p, res, row0 + t0, min(16, t1 - t0), n0, ncols);
+      // where this lane's share of the warp's sums goes: CTA 2 lane + rank of the cluster
+      const int cap = (C::kCols + a.split - 1) / a.split;  // tokens of a share, at most
+      uint32_t send = 0, send_to = 0, send_from = 0, send_bar = 0;
+      if (NT <= 128 && a.split > 1 && works && lane < a.split) {
+        const int from = tv * lane / a.split;
+        send = static_cast<uint32_t>(tv * (lane + 1) / a.split - from) * 128u;
+        send_from = smem_u32(s_part + (ew * C::kCols + from) * 32);
+        send_to = smem_cluster_addr(smem_u32(s_recv + (part * F_EPI_WARPS + ew) * cap * 32), 2 * lane + rank);
+        send_bar = smem_cluster_addr(smem_u32(&bar_recv[ew]), 2 * lane + rank);
+      }
       float* part_at = s_part + ew * C::kCols * 32 + lane;
       const uint32_t sum_at = lane_addr + C::kSumCol + c0;
       bool ok = true;
@@ -630,18 +687,10 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       if constexpr (NT <= 128) {
         if (a.split > 1 && works) {
           // the parts' sums meet: each goes out to the CTAs that add a share of the tokens each, in the order of K
-          const int cap = (C::kCols + a.split - 1) / a.split;  // tokens of a share, at most
           const uint32_t bar = smem_u32(&bar_recv[ew]);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane < a.split) {
-            const int from = tv * lane / a.split, to = tv * (lane + 1) / a.split;
-            const uint32_t peer = 2 * lane + rank;
-            if (to > from)
-              copy_to_peer(smem_cluster_addr(smem_u32(s_recv + (part * F_EPI_WARPS + ew) * cap * 32), peer),
-                           smem_u32(s_part + (ew * C::kCols + from) * 32), static_cast<uint32_t>(to - from) * 128u,
-                           smem_cluster_addr(bar, peer));
-          }
+          if (send != 0u) copy_to_peer(send_to, send_from, send, send_bar);
           __syncwarp();
           if (t0 < t1) {
             expect_tx_elect(bar, static_cast<uint32_t>(a.split * (t1 - t0)) * 128u);
@@ -654,10 +703,17 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
             float v[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-            for (int j = 0; j < a.split; ++j)
+            const float* at = in + (t - t0) * 32;
+            for (int j = 0; j < a.split; ++j, at += F_EPI_WARPS * cap * 32) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (t + i < t1) v[i] += in[(j * F_EPI_WARPS * cap + t - t0 + i) * 32];
+              for (int i = 0; i < 8; ++i)
+                if (t + i < t1) v[i] += at[i * 32];
+              if (t + 8 < t1) {
+#pragma unroll
+                for (int i = 8; i < 16; ++i)
+                  if (t + i < t1) v[i] += at[i * 32];
+              }
+            }
             if (t > t0) fetch_residual(a, p, res, row0 + t, min(16, t1 - t), n0, ncols);
             finish<GATED>(a, p, v, bias, res, row0 + t, min(16, t1 - t), n0, ncols);
           }
@@ -679,7 +735,7 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::kTmemCols)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(s_tmem_base), "r"(C::kTmemCols)
                  : "memory");
   }
 }
@@ -704,15 +760,14 @@ BPlan make_plan(int64_t E, int64_t R, int64_t channel_blocks, int64_t K, bool gr
   // clusters of 2 ks CTAs (one a SM) that are resident at once on 152 SMs, as the occupancy query gives them
   constexpr int kFit[F_MAX_SPLIT + 1] = {0, 76, 36, 23, 15, 13, 8, 7, 7};
   int64_t best = INT64_MAX;
-  const int64_t b0 = (R + 255) / 256;
-  for (int64_t b = b0; b <= b0 + 8 && b <= (R + 15) / 16; ++b) {
-    const int per = round16((R + b - 1) / b);
+  const int widest = static_cast<int>(std::min<int64_t>(256, round16(R)));
+  for (int per = widest; per >= 16; per -= 16) {
     const int64_t blocks = (R + per - 1) / per;
     const int64_t units = blocks * channel_blocks;
     for (int ks = 1; ks <= F_MAX_SPLIT; ++ks) {
       if (ks > 1 && (units > kFit[ks] || 2 * ks > KB || per > 128)) continue;
       const int64_t waves = ks > 1 ? 1 : (units + F_MAX_CLUSTERS - 1) / F_MAX_CLUSTERS;
-      const int64_t cost = waves * ((KB + ks - 1) / ks * block_cost(per) + 300) + (ks > 1 ? 1800 + 8 * per : 8 * per);
+      const int64_t cost = waves * ((KB + ks - 1) / ks * block_cost(per) + 300) + (ks > 1 ? 900 + 6 * per : 8 * per);
       if (cost < best) {
         best = cost;
         p.per = per;
@@ -778,8 +833,9 @@ cudaError_t launch_bf16_gemm(const Bf16GemmArgs& g, cudaStream_t stream) {
   a.blocks = p.blocks;
   a.per = p.per;
   // An accumulator's additions truncate: over the whole of K a sum comes out low by about K * 2^-30 of itself (7168:
-  // 7.9e-6).  bf16 outputs round 2^-9 away; for fp32 ones an accumulator takes 512 of K.
-  a.chunk = g.f32 ? 8 : 1 << 20;
+  // 7.9e-6).  bf16 outputs round 2^-9 away; for fp32 ones an accumulator takes 512 of K (4.8e-7
+  // whatever K is), or 768 where its sums are not added up beside the next MMAs.
+  a.chunk = !g.f32 ? 1 << 20 : p.nt == 256 ? 12 : 8;
   a.xbig = (grouped ? p.nt : p.per) / 2;
   a.xsmall = std::max(8, (a.xbig / 4 + 7) & ~7);
   a.f32 = g.f32;
