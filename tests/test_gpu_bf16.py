@@ -168,3 +168,198 @@ def test_bad_group_list(counts):
     assert W.read_device_status(ws) == 5 and bool((y == 5.0).all())
     W.w8a8_bf16_grouped_matmul(x, torch.tensor([3, 5], dtype=torch.int64, device="cuda"), w, ws=ws, y=y)
     assert W.read_device_status(ws) == 0 and not bool((y == 5.0).all())
+
+
+def test_fp32_long_sums():
+    """A sum of 32768 positive products as fp32: an accumulator takes 768 of K at most, 48 additions of at most 2^-23 of
+    the partial sum, 16 more for the alignment inside each; the chunks' sums add one rounding each.  (In one accumulator
+    2048 additions lose 2^-24 of the partial sum on average: 1e-4.)"""
+    K = 32768
+    for M in (5, 300):
+        x = (torch.rand(M, K, generator=gen(1), device="cuda") + 0.5).to(torch.bfloat16)
+        w = (torch.rand(40, K, generator=gen(2), device="cuda") + 0.5).to(torch.bfloat16)
+        v = x.double() @ w.double().t()
+        y = W.w8a8_bf16_matmul(x, w, out_dtype=torch.float32)
+        assert bool(((y.double() - v).abs() <= (64 * 2.0 ** -23 + K / 512 * 2.0 ** -24) * v).all())
+
+
+@pytest.mark.parametrize("M,N,K,act", [(5, 512, 2048, "none"), (300, 512, 256, "silu"), (64, 130, 1024, "none"),
+                                       (40, 77, 512, "swiglu"), (200, 264, 64, "swiglu")])
+def test_residual_in_place(M, N, K, act):
+    x, w, b, r = inputs(M, N, K, act, True, True, M + N)
+    want = W.w8a8_bf16_matmul(x, w, b, act, r)
+    stream = r.clone()
+    got = W.w8a8_bf16_matmul(x, w, b, act, stream, y=stream)
+    assert got is stream and torch.equal(got, want)
+
+
+def test_empty_and_given_outputs():
+    x, w, b, _ = inputs(6, 40, 64, "none", True, False, 3)
+    assert W.w8a8_bf16_matmul(x[:0], w, b).shape == (0, 40)
+    pad = torch.full((9, 40), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = W.w8a8_bf16_matmul(x, w, b, y=pad[:6])
+    assert torch.equal(y, W.w8a8_bf16_matmul(x, w, b)) and bool((pad[6:] == 7.0).all())
+    gl = torch.tensor([0, 4, 0, 2], dtype=torch.int64, device="cuda")
+    w4 = w.expand(4, 40, 64).contiguous()
+    pad = torch.full((9, 40), 7.0, device="cuda")
+    y = W.w8a8_bf16_grouped_matmul(x, gl, w4, y=pad[:6])  # y's own type decides
+    assert y.dtype is torch.float32 and bool((pad[6:] == 7.0).all())
+    close(y, *reference(x, w, None, "none", None))
+    zero = torch.zeros(4, dtype=torch.int64, device="cuda")
+    assert W.w8a8_bf16_grouped_matmul(x[:0], zero, w4).shape == (0, 40)
+
+
+def test_unaligned_outputs():
+    """y and the residual on 2-byte boundaries, and a bias that starts on one."""
+    x, w, b, r = inputs(70, 64, 128, "none", True, True, 9)
+    buf = torch.empty(3 * 70 * 64 + 8, dtype=torch.bfloat16, device="cuda")
+    y, res = buf[1:1 + 70 * 64].view(70, 64), buf[70 * 64 + 3:70 * 64 * 2 + 3].view(70, 64)
+    bias = buf[-63 - 2:-1]
+    res.copy_(r)
+    bias.copy_(b)
+    assert torch.equal(W.w8a8_bf16_matmul(x, w, bias, "gelu", res, y=y), W.w8a8_bf16_matmul(x, w, b, "gelu", r))
+
+
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_nan_stays_where_it_is(act):
+    M, N, K = 40, 96, 256
+    x, w, _, _ = inputs(M, N, K, act, False, False, 4)
+    want = W.w8a8_bf16_matmul(x, w, activation=act)
+    x2, w2 = x.clone(), w.clone()
+    x2[7, 3], x2[21, 200], w2[50, 9] = float("nan"), float("inf"), float("nan")
+    y = W.w8a8_bf16_matmul(x2, w2, activation=act)
+    keep = torch.ones(M, N, dtype=torch.bool, device="cuda")
+    keep[[7, 21]], keep[:, 50] = False, False
+    assert torch.equal(y[keep], want[keep])
+    assert bool(y[7].isnan().all()) and bool(y[:, 50].isnan().all()) and not bool(y[21].isfinite().any())
+    # rows of another group, read with a tile and not part of it
+    counts = [3, 20, 17]
+    gl = torch.tensor(counts, dtype=torch.int64, device="cuda")
+    w3 = torch.stack([w, w * float("nan"), w])
+    x3 = x.clone()
+    x3[3:23] = float("inf")
+    y = W.w8a8_bf16_grouped_matmul(x3, gl, w3, activation=act)
+    assert torch.equal(y[:3], want[:3]) and torch.equal(y[23:], want[23:]) and bool(y[3:23].isnan().all())
+
+
+def test_calls_that_follow_one_another():
+    """A call's output as the next one's weight, rows, residual and bias, with nothing between the launches."""
+    M, K = 64, 512
+    x, w, _, _ = inputs(M, K, K, "none", False, False, 12)
+
+    def chain(wait):
+        h, out = x, []
+        for i in range(6):
+            h = W.w8a8_bf16_matmul(h, w, activation="silu" if i % 2 else "none", residual=h, ws=ws)
+            wait()
+            s = W.w8a8_bf16_matmul(h, h, ws=ws, out_dtype=torch.float32)  # [M,M]: the rows are the weight as well
+            wait()
+            q, sc, r, y = W.w8a8_fp8_rms_norm_quant(h, w[0], residual=x, want_y=True)
+            wait()
+            h = W.w8a8_bf16_matmul(y, w, bias=r[0], ws=ws)
+            wait()
+            out += [h, s, q, sc, r, y]
+        return out
+
+    ws = W.workspace(W.bf16_matmul_workspace_bytes(M, K, K))
+    want = chain(torch.cuda.synchronize)
+    for _ in range(20):
+        for a, b in zip(chain(lambda: None), want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert W.read_device_status(ws) == 0
+
+
+def test_graphs_streams_and_repeats():
+    """Two captured graphs on one workspace, replayed in turn; another stream; the same bits every time."""
+    x, w, b, r = inputs(64, 2048, 2048, "none", True, True, 5)
+    x2, w2, _, _ = inputs(300, 256, 512, "swiglu", False, False, 6)
+    ws = W.workspace(256)
+    y, y2 = torch.empty_like(r), torch.empty(300, 256, dtype=torch.bfloat16, device="cuda")
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    with torch.cuda.graph(graphs[0]):
+        W.w8a8_bf16_matmul(x, w, b, "gelu", r, ws=ws, y=y)
+    with torch.cuda.graph(graphs[1]):
+        W.w8a8_bf16_matmul(x2, w2, activation="swiglu", ws=ws, y=y2)
+    for k in range(3):
+        x.mul_(1.5)
+        x2.mul_(0.5)
+        for g in graphs:
+            g.replay()
+        assert torch.equal(y, W.w8a8_bf16_matmul(x, w, b, "gelu", r))
+        assert torch.equal(y2, W.w8a8_bf16_matmul(x2, w2, activation="swiglu"))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = W.w8a8_bf16_matmul(x, w, b, "gelu", r)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(other, y)
+    # two streams at once, each with its own workspace
+    ws2 = W.workspace(256)
+    with torch.cuda.stream(side):
+        a = [W.w8a8_bf16_matmul(x, w, b, "gelu", r, ws=ws2) for _ in range(30)]
+    c = [W.w8a8_bf16_matmul(x2, w2, activation="swiglu", ws=ws) for _ in range(30)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, y) for t in a) and all(torch.equal(t, y2) for t in c)
+
+
+@pytest.mark.parametrize("rows,weight,out", [(270000, 16, torch.bfloat16), (3, 280000, torch.float32)])
+def test_offsets_past_32_bits(rows, weight, out):
+    """x, or w, of more than 2^31 values."""
+    K = 8192
+    x = torch.randn(min(rows, 1000), K, generator=gen(1), device="cuda").to(torch.bfloat16)
+    w = (torch.randn(min(weight, 1000), K, generator=gen(2), device="cuda") * 0.02).to(torch.bfloat16)
+    x, w = x.repeat(-(-rows // 1000), 1)[:rows], w.repeat(-(-weight // 1000), 1)[:weight]
+    y = W.w8a8_bf16_matmul(x, w, out_dtype=out)
+    r, c = min(rows, 700), min(weight, 700)
+    close(y[-r:, -c:], *reference(x[-r:], w[-c:], None, "none", None))
+    close(y[:r, :c], *reference(x[:r], w[:c], None, "none", None))
+
+
+def test_output_past_32_bits():
+    M, N, K = 70000, 32768, 16
+    x, w, b, _ = inputs(M, N, K, "none", True, False, 1)
+    y = W.w8a8_bf16_matmul(x, w, b, "relu")
+    close(y[-300:], *reference(x[-300:], w, b, "relu", None))
+    close(y[:300], *reference(x[:300], w, b, "relu", None))
+
+
+@pytest.mark.parametrize("R", [9, 700, 40000])
+def test_a_thousand_experts(R):
+    E, N, K = 1024, 40, 64
+    pick = torch.randint(0, E, (R,), generator=gen(R), device="cuda").sort().values
+    gl = torch.bincount(pick, minlength=E)
+    x = torch.randn(R, K, generator=gen(1), device="cuda").to(torch.bfloat16)
+    w = torch.randn(E, 2 * N, K, generator=gen(2), device="cuda").to(torch.bfloat16)
+    y = W.w8a8_bf16_grouped_matmul(x, gl, w, activation="swiglu", out_dtype=torch.float32)
+    v = torch.bmm(w.double()[pick[:2000]], x.double()[:2000, :, None])[:, :, 0]
+    a = torch.bmm(w.double().abs()[pick[:2000]], x.double().abs()[:2000, :, None])[:, :, 0]
+    g, u, eg, eu = v[:, :N], v[:, N:], a[:, :N] * 22 * 2.0 ** -23, a[:, N:] * 22 * 2.0 ** -23
+    s = g * torch.sigmoid(g)
+    err = 1.13 * eg * (u.abs() + eu) + (s.abs() + 1.13 * eg) * eu + 300 * 2.0 ** -23 * (s * u).abs()
+    close(y[:2000], s * u, err)
+
+
+def test_refusals():
+    x, w, b, r = inputs(8, 32, 64, "none", True, True, 2)
+    for bad in (dict(x=x.float()), dict(w=w.half()), dict(bias=b.float()), dict(residual=r.float()),
+                dict(out_dtype=torch.float16), dict(y=r.half()), dict(ws=torch.zeros(256, device="cuda"))):
+        with pytest.raises(TypeError):
+            W.w8a8_bf16_matmul(**{"x": x, "w": w, **bad})
+    for bad in (dict(x=x[:, :48]), dict(w=w[:, ::2]), dict(bias=b[:-1]), dict(residual=r[:7]), dict(y=r[:7]),
+                dict(x=x.cpu()), dict(w=w.cpu()), dict(bias=b.cpu()), dict(activation="tanh"), dict(activation=None),
+                dict(w=w[:-1], activation="swiglu"), dict(w=w, activation="swiglu", bias=b[:16]), dict(x=x.t())):
+        with pytest.raises(ValueError):
+            W.w8a8_bf16_matmul(**{"x": x, "w": w, **bad})
+    with pytest.raises(W.W8A8Error):
+        W.w8a8_bf16_matmul(x, w, ws=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(W.W8A8Error):
+        W.w8a8_bf16_matmul(x[:, :40].contiguous(), w[:, :40].contiguous())
+    gl = torch.tensor([3, 5], dtype=torch.int64, device="cuda")
+    w2 = torch.stack([w, w])
+    for bad in (dict(group_list=gl[:1]), dict(w=w), dict(bias=b), dict(group_list=gl.cpu()), dict(x=x.t())):
+        with pytest.raises(ValueError):
+            W.w8a8_bf16_grouped_matmul(**{"x": x, "group_list": gl, "w": w2, **bad})
+    with pytest.raises(TypeError):
+        W.w8a8_bf16_grouped_matmul(x, gl.int(), w2)
+    assert W.last_engine() == W.ENGINE_TC
+    assert _capi.ACTIVATIONS["swiglu"] == 5
