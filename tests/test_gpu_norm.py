@@ -237,3 +237,29 @@ def test_other_stream_and_graph():
     want = W.w8a8_fp8_rms_norm_quant(x, w, residual=res, want_y=True)
     for a, b in zip(out, want):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+def test_offsets_past_32_bits(form):
+    """More than 2^31 values; the last rows and those around the border against the formula."""
+    M, K = 270000, 8192
+    x = torch.randn(1000, K, generator=gen(31), device="cuda").to(torch.bfloat16).repeat(M // 1000, 1)
+    w = torch.rand(K, generator=gen(32), device="cuda") + 0.5
+    q, s, r, y = FORMS[form](x, w, residual=x, want_y=True)
+    for rows in (slice(0, 300), slice(262100, 262200), slice(M - 300, M)):
+        rr, v = norm_reference(x[rows], w, 1e-6, x[rows])
+        rq, rs = codes_reference(v, form)
+        assert torch.equal(s[rows], rs) and same_codes(q[rows].contiguous(), rq, form)
+        assert torch.equal(r[rows], rr) and torch.equal(y[rows], v.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+def test_same_bits_at_every_batch(form):
+    """A row's codes do not hang on how many rows there are: one chunk a thread for few, four for many."""
+    K = 4096
+    x = torch.randn(3000, K, generator=gen(41), device="cuda").to(torch.bfloat16)
+    w = torch.rand(K, generator=gen(42), device="cuda") + 0.5
+    q, s, _, _ = FORMS[form](x, w)
+    for n in (1, 7, 200, 700):
+        qn, sn, _, _ = FORMS[form](x[:n], w)
+        assert torch.equal(qn.view(torch.uint8), q[:n].view(torch.uint8)) and torch.equal(sn, s[:n])

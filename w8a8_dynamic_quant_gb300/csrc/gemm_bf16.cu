@@ -243,6 +243,8 @@ __device__ __forceinline__ void copy_to_peer(uint32_t dst, uint32_t src, uint32_
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // One unit of work: the tile and its K range.
 struct Unit {
   int e, wb;   // expert, block of weight rows
@@ -271,6 +273,7 @@ struct Place {
   const float* gate;  // gated: those of the two warps of its channels
   const float* up;
   int q, h, lane;
+  int r0, c;          // the first token and channel of 16 x 32 that the lane stores
   int bar;            // gated: the two warps' barrier
 };
 
@@ -280,27 +283,23 @@ struct Residual {
   static constexpr int kSlots = GATED ? 1 : 2;  // rows a lane stores
   uint4 v[kSlots];
 };
+// (at: as in finish())
 template <bool GATED>
-__device__ __forceinline__ void fetch_residual(const BArgs& a, const Place& p, Residual<GATED>& res, int64_t row,
-                                               int rows, int64_t n0, int ncols) {
+__device__ __forceinline__ void fetch_residual(const BArgs& a, const Place& p, Residual<GATED>& res, int64_t at, int rows,
+                                               int ncols) {
   if (a.residual == nullptr || !a.vec) return;
-  const int c = (p.lane & 3) * 8;
-  const int r0 = (p.lane >> 2) + (GATED ? 8 * (p.q >> 1) : 0);
 #pragma unroll
   for (int i = 0; i < Residual<GATED>::kSlots; ++i)
-    if (r0 + 8 * i < rows && c < ncols)
-      res.v[i] = *reinterpret_cast<const uint4*>(a.residual + (row + r0 + 8 * i) * a.N + n0 + c);
+    if (p.r0 + 8 * i < rows && p.c < ncols) res.v[i] = *reinterpret_cast<const uint4*>(a.residual + at + 8 * i * a.N);
 }
 
-// 16 tokens x 32 channels: v[i] is this lane's channel of token i.  `rows` of the tokens exist and go to rows row..
-// of y, at channels n0 .. n0 + ncols.
+// 16 tokens x 32 channels: v[i] is this lane's channel of token i.  `rows` of the tokens and ncols of the channels exist;
+// at: where the value of token r0 at channel c, the lane's first one to store, stands in y and in the residual.
 template <bool GATED>
 __device__ __forceinline__ void finish(const BArgs& a, const Place& p, float (&v)[16], float bias,
-                                       const Residual<GATED>& res, int64_t row, int rows, int64_t n0, int ncols) {
+                                       const Residual<GATED>& res, int64_t at, int rows, int ncols) {
   constexpr int kSlots = Residual<GATED>::kSlots;
-  const int lane = p.lane;
-  const int c = (lane & 3) * 8;
-  const int r0 = (lane >> 2) + (GATED ? 8 * (p.q >> 1) : 0);
+  const int lane = p.lane, c = p.c, r0 = p.r0;
   const bool add = a.residual != nullptr;
   if (a.bias != nullptr) {
 #pragma unroll
@@ -336,28 +335,38 @@ __device__ __forceinline__ void finish(const BArgs& a, const Place& p, float (&v
             o[2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
           }
         }
-        const int64_t at = (row + r) * a.N + n0 + c;
+        const int64_t to = at + 8 * i * a.N;
         if (a.f32) {
-          float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.y) + at);
+          float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.y) + to);
           d[0] = make_float4(o[0], o[1], o[2], o[3]);
           d[1] = make_float4(o[4], o[5], o[6], o[7]);
         } else {
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + at) =
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + to) =
               make_uint4(f32x2_to_bf16x2_bits(o[0], o[1]), f32x2_to_bf16x2_bits(o[2], o[3]),
                          f32x2_to_bf16x2_bits(o[4], o[5]), f32x2_to_bf16x2_bits(o[6], o[7]));
         }
       }
     }
-  } else {  // rows of y start anywhere: a channel a lane
-    const int first = GATED ? 8 * (p.q >> 1) : 0, last = min(rows, GATED ? first + 8 : 16);
-    for (int r = first; r < last; ++r) {
-      if (lane < ncols) {
-        float o = GATED ? p.gate[r * B_LD + lane] : p.stg[r * B_LD + lane];
-        if constexpr (GATED) o = silu(o) * p.up[r * B_LD + lane];
-        const int64_t at = (row + r) * a.N + n0 + lane;
-        if (add) o += bf16_bits_to_f32(a.residual[at]);
-        if (a.f32) static_cast<float*>(a.y)[at] = o;
-        else static_cast<uint16_t*>(a.y)[at] = f32_to_bf16_bits(o);
+  } else {  // rows of y start anywhere: a channel a lane, eight rows' residuals on their way at once
+    const int64_t first = at - r0 * a.N - c + lane;  // token 0, the lane's channel
+#pragma unroll 1
+    for (int r = GATED ? 8 * (p.q >> 1) : 0, i = 0; i < kSlots; r += 8, ++i) {
+      const int64_t to = first + r * a.N;
+      float o[8];
+      if (add) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          o[k] = r + k < rows && lane < ncols ? bf16_bits_to_f32(a.residual[to + k * a.N]) : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float u = (GATED ? p.gate : p.stg)[(r + k) * B_LD + lane];
+        if constexpr (GATED) u = silu(u) * p.up[(r + k) * B_LD + lane];
+        if (add) u += o[k];
+        if (r + k < rows && lane < ncols) {
+          if (a.f32) static_cast<float*>(a.y)[to + k * a.N] = u;
+          else static_cast<uint16_t*>(a.y)[to + k * a.N] = f32_to_bf16_bits(u);
+        }
       }
     }
   }
@@ -583,6 +592,8 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   p.h = ew >> 2;
   p.lane = lane;
   p.bar = 1 + (p.q & 1) + 2 * p.h;
+  p.r0 = (lane >> 2) + (GATED ? 8 * (p.q >> 1) : 0);
+  p.c = (lane & 3) * 8;
   {
     float* mine = s_stg + (p.h * 4 + p.q) * B_STG_FLOATS;
     p.stg = mine;
@@ -620,12 +631,21 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       const int64_t row0 = static_cast<int64_t>(u.row0) + c0;
       Residual<GATED> res;
       // the tokens that the warp finishes: all of its own, or its part's share of them
-      const int t0 = uni(a.split > 1 ? max(tv, 0) * part / a.split : 0);
-      const int t1 = uni(a.split > 1 ? max(tv, 0) * (part + 1) / a.split : tv);
-      if (works && t0 < t1) fetch_residual(a, p, res, row0 + t0, min(16, t1 - t0), n0, ncols);
+      int t0 = 0, t1 = tv;
+      if (a.split > 1) {
+        t0 = uni(max(tv, 0) * part / a.split);
+        t1 = uni(max(tv, 0) * (part + 1) / a.split);
+      }
+      const int64_t at0 = (row0 + p.r0) * a.N + n0 + p.c;
+      if (works && t0 < t1) {
+        if (a.residual != nullptr && a.vec)  // the rest of the tile's rows come as far as L2
+          for (int t = t0 + 16 + lane; t < t1; t += 32) prefetch_l2(a.residual + (row0 + t) * a.N + n0);
+        fetch_residual(a, p, res, at0 + t0 * a.N, min(16, t1 - t0), ncols);
+      }
       // where this lane's share of the warp's sums goes: CTA 2 lane + rank of the cluster
-      const int cap = (C::kCols + a.split - 1) / a.split;  // tokens of a share, at most
+      int cap = 0;  // tokens of a share, at most
       uint32_t send = 0, send_to = 0, send_from = 0, send_bar = 0;
+      if (NT <= 128 && a.split > 1) cap = (C::kCols + a.split - 1) / a.split;
       if (NT <= 128 && a.split > 1 && works && lane < a.split) {
         const int from = tv * lane / a.split;
         send = static_cast<uint32_t>(tv * (lane + 1) / a.split - from) * 128u;
@@ -676,8 +696,8 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
             for (int i = 0; i < 16; ++i) part_at[(t + i) * 32] = v[i];
           } else {
             Residual<GATED> next;
-            if (t + 16 < tv) fetch_residual(a, p, next, row0 + t + 16, min(16, tv - t - 16), n0, ncols);
-            finish<GATED>(a, p, v, bias, res, row0 + t, min(16, tv - t), n0, ncols);
+            if (t + 16 < tv) fetch_residual(a, p, next, at0 + (t + 16) * a.N, min(16, tv - t - 16), ncols);
+            finish<GATED>(a, p, v, bias, res, at0 + t * a.N, min(16, tv - t), ncols);
             res = next;
           }
         }
@@ -714,8 +734,8 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                   if (t + i < t1) v[i] += at[i * 32];
               }
             }
-            if (t > t0) fetch_residual(a, p, res, row0 + t, min(16, t1 - t), n0, ncols);
-            finish<GATED>(a, p, v, bias, res, row0 + t, min(16, t1 - t), n0, ncols);
+            if (t > t0) fetch_residual(a, p, res, at0 + t * a.N, min(16, t1 - t), ncols);
+            finish<GATED>(a, p, v, bias, res, at0 + t * a.N, min(16, t1 - t), ncols);
           }
         }
       }
