@@ -804,7 +804,7 @@ def _rms_norm(name, x, weight, eps, residual, want_y, q, scale, residual_out, y,
         y = _empty_like(x)
         y_ptr = y.data_ptr()
     if q is None:
-        q = _empty((M, K), dtype=q_dtype, device=device)
+        q = _empty_like(x, dtype=q_dtype)
     elif q_dtype is _E4M3:
         _check_e4m3(q, "q", (M, K), dev)
     else:
