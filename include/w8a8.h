@@ -524,7 +524,8 @@ W8A8_API w8a8_status w8a8_mx_rms_norm_quant(const uint16_t* x, const uint16_t* r
 /* (bias likewise); y = silu(gate) * up.  Weights are used as they lie.      */
 /* K % 16 == 0; x and w 16-byte aligned; any N (rows of y that start on      */
 /* 16-byte boundaries are stored faster).  residual may be y itself (bf16),  */
-/* no other tensors may overlap.  The workspace holds the status word alone. */
+/* no other tensors may overlap.  One workspace may serve bf16 products of   */
+/* different sizes in turn; after a device timeout zero-fill it again.       */
 /* w8a8_last_engine() is W8A8_ENGINE_TC.                                     */
 /* ------------------------------------------------------------------------ */
 

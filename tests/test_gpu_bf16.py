@@ -363,3 +363,38 @@ def test_refusals():
         W.w8a8_bf16_grouped_matmul(x, gl.int(), w2)
     assert W.last_engine() == W.ENGINE_TC
     assert _capi.ACTIVATIONS["swiglu"] == 5
+
+
+# more tiles than CTA pairs by a little: the last ones' K is cut over all pairs and joined through the workspace
+CUT = [(16, 20000, 1024, "none"), (40, 20800, 4096, "none"), (64, 20480, 2048, "gelu"), (33, 10200, 4096, "swiglu"),
+       (2483, 2048, 7168, "none"), (1241, 2000, 8192, "swiglu"), (64, 40000, 2048, "silu")]
+
+
+@pytest.mark.parametrize("M,N,K,act", CUT)
+def test_cut_tiles(M, N, K, act):
+    x, w, b, r = inputs(M, N, K, act, True, True, M + N)
+    need = W.bf16_matmul_workspace_bytes(M, N, K)
+    assert need > 256, "not a case of this test"
+    ws = W.workspace(need)
+    bf16 = W.w8a8_bf16_matmul(x, w, b, act, r, ws=ws)
+    fp32 = W.w8a8_bf16_matmul(x, w, b, act, None, torch.float32, ws=ws)
+    close(bf16, *reference(x, w, b, act, r))
+    close(fp32, *reference(x, w, b, act, None))
+    assert W.read_device_status(ws) == 0
+    # the same bits every time, whichever part comes last, and from a graph; the workspace is as it was
+    y = torch.empty_like(bf16)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        W.w8a8_bf16_matmul(x, w, b, act, r, ws=ws, y=y)
+    for _ in range(20):
+        graph.replay()
+        assert torch.equal(y, bf16)
+        assert torch.equal(W.w8a8_bf16_matmul(x, w, b, act, None, torch.float32, ws=ws), fp32)
+    assert not bool(ws[:256 + 4864].any())
+    with pytest.raises(W.W8A8Error):  # (need is the larger of the gated and the plain product's)
+        W.w8a8_bf16_matmul(x, w, b, act, r, ws=W.workspace(256))
+    # one workspace for products of other sizes in turn
+    x2, w2, _, _ = inputs(50, 300, 1024, "none", False, False, 1)
+    a = W.w8a8_bf16_matmul(x2, w2, ws=ws)
+    assert torch.equal(W.w8a8_bf16_matmul(x, w, b, act, r, ws=ws), bf16)
+    assert torch.equal(W.w8a8_bf16_matmul(x2, w2, ws=ws), a)

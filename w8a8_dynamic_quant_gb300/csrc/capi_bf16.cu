@@ -50,13 +50,13 @@ w8a8_status matmul_common(Bf16GemmArgs& a, uint32_t flags, void* ws, size_t ws_b
   if (!a.x || !a.w || !a.y) return W8A8_ERR_NULL;
   if (!ws) return W8A8_ERR_WORKSPACE;
   if (!aligned16(a.x) || !aligned16(a.w)) return W8A8_ERR_ALIGN;
-  if (ws_bytes < kStatusBytes || !aligned16(ws)) return W8A8_ERR_WORKSPACE;
+  if (ws_bytes < kStatusBytes + plan_bf16_gemm(a) || !aligned16(ws)) return W8A8_ERR_WORKSPACE;
   int sms = 0;
   if (w8a8_status s = device_info(sms)) return s;  // refuses a device of another kind
   a.f32 = (flags & W8A8_MM_F32) != 0u;
   a.status = static_cast<DeviceStatus*>(ws);
   t_last_engine = W8A8_ENGINE_TC;
-  return cuda_status(launch_bf16_gemm(a, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_bf16_gemm(a, static_cast<uint8_t*>(ws) + kStatusBytes, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -82,7 +82,7 @@ w8a8_status w8a8_mx_rms_norm_quant(const uint16_t* x, const uint16_t* residual, 
 }
 
 size_t w8a8_bf16_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return M < 0 || N <= 0 || K <= 0 ? 0 : kStatusBytes;
+  return M < 0 || N <= 0 || K <= 0 ? 0 : kStatusBytes + bf16_gemm_ws_bytes(M, N, K);
 }
 
 size_t w8a8_bf16_grouped_matmul_workspace_bytes(int64_t E, int64_t R, int64_t N, int64_t K) {

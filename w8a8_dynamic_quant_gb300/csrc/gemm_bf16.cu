@@ -57,6 +57,9 @@ struct BArgs {
   int E;
   int act;
   int split;   // pairs per cluster that share a unit's K
+  int cut;     // the last units' blocks in sequence are cut into equal runs, one a pair
+  uint32_t* counters;  // cut: [pairs][2 CTAs][epilogue warps], zero between calls
+  float* pieces;       // cut: [pairs][head, tail][2 CTAs][epilogue warp][token][32 channels]
   int blocks;  // dense: token blocks of `per` tokens each
   int per;
   int chunk;         // blocks of K that an accumulator takes before its sum is added up in binary32
@@ -253,6 +256,33 @@ struct Unit {
   int n;       // tokens rounded up to 16
 };
 
+// The segments of one pair, blocks [kb0, kb1) of a unit each.  Every role walks them on its own.
+template <bool CUT>
+struct Segments;
+// Every step-th unit, whole or the pair's part of it: the same blocks of each (kb0 and kb1 stay as they are).
+template <>
+struct Segments<false> {
+  int unit, units, step;
+};
+// Whole units, then a run of blocks.
+template <>
+struct Segments<true> {
+  Walk units, run;
+};
+__device__ __forceinline__ bool next_segment(Segments<false>& w, int& unit, int&, int&) {
+  unit = w.unit;
+  w.unit += w.step;
+  return unit < w.units;
+}
+__device__ __forceinline__ bool next_segment(Segments<true>& w, int& unit, int& kb0, int& kb1) {
+  int u = 0, k0 = 0, k1 = 0;
+  const bool more = next_unit(w.units, u, k0, k1) || next_unit(w.run, u, k0, k1);
+  unit = uni(u);
+  kb0 = uni(k0);
+  kb1 = uni(k1);
+  return uni(more);
+}
+
 // The barrier of an epilogue warp that holds gate rows and of the one that holds the up rows of the same channels and
 // tokens; the AND of what they bring.
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
@@ -374,7 +404,42 @@ __device__ __forceinline__ void finish(const BArgs& a, const Place& p, float (&v
   else __syncwarp();
 }
 
-template <int NT, bool GATED>
+// A cut unit's counter (one per epilogue warp, gated: per pair of warps): 1 the tail's sums are in the workspace, 2 the
+// head's.  seen(): whether it reads `what`.  arrive(): the warp's sums are written; adds `what` and says whether the
+// other's were there already, in which case it is back at zero.  The two warps of a gated pair decide together.
+template <bool GATED>
+__device__ __forceinline__ bool agreed(const Place& p, uint32_t answer) {
+  answer = __shfl_sync(0xffffffffu, answer, 0);
+  if constexpr (GATED) return pair_and(p.bar, p.q >= 2 || answer != 0u);
+  return answer != 0u;
+}
+template <bool GATED>
+__device__ __forceinline__ bool seen(const BArgs& a, const Place& p, int key, int lane, uint32_t what) {
+  uint32_t v = 0;
+  if (lane == 0 && (!GATED || p.q < 2))
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.counters + key) : "memory");
+  const bool yes = agreed<GATED>(p, v == what);
+  if (yes) __threadfence();
+  return yes;
+}
+template <bool GATED>
+__device__ __forceinline__ bool arrive(const BArgs& a, const Place& p, int key, int lane, uint32_t what) {
+  __threadfence();
+  if constexpr (GATED) pair_sync(p.bar);
+  else __syncwarp();
+  uint32_t before = 0;
+  if (lane == 0 && (!GATED || p.q < 2)) {
+    before = atomicAdd(a.counters + key, what);
+    if (before != 0u) a.counters[key] = 0u;
+  }
+  const bool last = agreed<GATED>(p, before != 0u);
+  if (last) __threadfence();
+  return last;
+}
+
+// CUT: the last units' K is cut over all pairs.  (A kernel of its own: the code that joins the pieces costs every other
+// launch about 1 us and the large ones up to 8 %.)
+template <int NT, bool GATED, bool CUT>
 __global__ void __launch_bounds__(B_THREADS, 1)
 bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmXbig,
                  const __grid_constant__ CUtensorMap tmXsmall, const BArgs a) {
@@ -447,13 +512,24 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   __syncthreads();
   pdl_trigger();
   cluster_meet();  // the CTAs' barriers exist before any touches another's
-  // units first, first + step, ..; blocks [kb0, kb1) of each
-  const int part = static_cast<int>(crank >> 1);
-  const int first = static_cast<int>(cluster_id);
-  const int step = static_cast<int>(nclusters);
-  const int kb0 = KB * part / a.split, kb1 = KB * (part + 1) / a.split;
+  const int part = static_cast<int>(crank >> 1), me = static_cast<int>(cluster_id);
   const int chunk = a.chunk;
   const int nacc = NT == 256 && chunk < KB ? 1 : C::kAcc;
+  const int part0 = KB * part / a.split, part1 = KB * (part + 1) / a.split;  // the pair's part of K (split 1: all of it)
+  // Whole units, every C-th one; or the pair's part of its cluster's unit; CUT: whole units, then the pair's run of the
+  // blocks of the last C to 2 C units, which ends and begins inside units.
+  auto start = [&] {
+    Segments<CUT> w;
+    const int C = static_cast<int>(nclusters);
+    if constexpr (CUT) {
+      const int64_t whole = static_cast<int64_t>(units / C - 1) * C, rest = (units - whole) * KB;
+      w.units = Walk{me, whole, C, KB};
+      w.run = Walk{whole * KB + run_begin(rest, C, me), whole * KB + run_begin(rest, C, me + 1), 0, KB};
+    } else {
+      w = Segments<CUT>{me, units, C};
+    }
+    return w;
+  };
   auto unit_of = [&](int unit) {
     Unit u;
     int tb, cnt, TB;
@@ -471,7 +547,13 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
                                   : static_cast<int64_t>(u.e) * a.N + static_cast<int64_t>(u.wb) * 256 + rank * 128);
   };
   Unit u0 = {};  // the first unit, worked out while the kernel in front still runs
-  if (!grouped && first < units) u0 = unit_of(first);
+  int first = -1;
+  auto begin = [&] {
+    Segments<CUT> w = start();
+    int k0, k1;
+    if (next_segment(w, first, k0, k1)) u0 = unit_of(first);
+  };
+  if (!grouped) begin();
   // Each role waits for the kernel in front at its first access to memory: what is before it in the code, and the
   // code's own way into the instruction cache, is behind it then.
   if (grouped) {
@@ -482,7 +564,7 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       if (tid == 0 && blockIdx.x == 0) set_status(a.status, W8A8_ERR_GROUP_LIST, 0u);
       units = 0;
     }
-    if (first < units) u0 = unit_of(first);
+    begin();
   }
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
@@ -491,7 +573,9 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     uint32_t phase = 0;
     bool ok = true;
     const int xbig = uni(a.xbig), xsmall = uni(a.xsmall);
-    for (int unit = first; ok && unit < units; unit += step) {
+    Segments<CUT> w = start();
+    int unit = 0, kb0 = part0, kb1 = part1;
+    while (ok && next_segment(w, unit, kb0, kb1)) {
       const Unit u = unit == first ? u0 : unit_of(unit);
       const int yw = uni(w_row(u)), yu = uni(yw + static_cast<int>(a.N));
       const int rows = u.n >> 1;
@@ -551,7 +635,9 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       int stage = 0, buf = 0;
       uint32_t phase = 0, bphase = 0;
       bool ok = wait_for(smem_u32(&bar_alloc), 0u, &s_abort, a.status, 7u);
-      for (int unit = first; ok && unit < units; unit += step) {
+      Segments<CUT> w = start();
+      int unit = 0, kb0 = part0, kb1 = part1;
+      while (ok && next_segment(w, unit, kb0, kb1)) {
         const uint32_t idesc = idesc_bf16(uni((unit == first ? u0 : unit_of(unit)).n));
         for (int c0 = kb0; ok && c0 < kb1; c0 += chunk) {
           ok = wait_for(smem_u32(&bar_acce[buf]), bphase ^ 1u, &s_abort, a.status, 2u);
@@ -616,7 +702,9 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     const uint32_t acce_even = smem_cluster_addr(smem_u32(&bar_acce[0]), even);
     int buf = 0;
     uint32_t bphase = 0;
-    for (int unit = first; unit < units; unit += step) {
+    Segments<CUT> w = start();
+    int unit = 0, kb0 = part0, kb1 = part1;
+    while (next_segment(w, unit, kb0, kb1)) {
       const Unit u = unit == first ? u0 : unit_of(unit);
       // the first half's warps read tokens [0, cut), the second's [cut, n)
       const int n = uni(u.n);
@@ -654,6 +742,22 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         send_bar = smem_cluster_addr(smem_u32(&bar_recv[ew]), 2 * lane + rank);
       }
       float* part_at = s_part + ew * C::kCols * 32 + lane;
+      // A cut unit's head (its first blocks, the end of this run) and tail (the beginning of the next pair's) are joined
+      // by whichever comes last, as a rule the head: it finds the tail's sums in the workspace and adds them to its own.
+      const bool head = CUT && kb1 < KB, tail = CUT && kb0 > 0;
+      const int key = ((tail ? me - 1 : me) * 2 + static_cast<int>(rank)) * F_EPI_WARPS + (GATED ? (p.h * 4 + (p.q & 1)) : ew);
+      auto piece = [&](bool of_tail) {
+        return a.pieces + ((((static_cast<int64_t>(tail ? me - 1 : me) * 2 + (of_tail ? 1 : 0)) * 2 + rank) * F_EPI_WARPS + ew) *
+                           C::kCols) * 32 + lane;
+      };
+      bool joined = CUT && head && works && seen<GATED>(a, p, key, lane, 1u);  // the tail was there
+      float other[16];  // its sums, a step ahead of their use
+      auto fetch_other = [&](int t) {
+        const float* from = piece(true) + t * 32;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) other[i] = __ldcg(from + i * 32);
+      };
+      if (joined) fetch_other(0);
       const uint32_t sum_at = lane_addr + C::kSumCol + c0;
       bool ok = true;
       for (int k0 = kb0; k0 < kb1; k0 += chunk) {
@@ -672,6 +776,10 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
           continue;
         }
         const bool more = k0 > kb0, last = k0 + chunk >= kb1;
+        if (CUT && last && head && !joined) {
+          joined = seen<GATED>(a, p, key, lane, 1u);
+          if (joined) fetch_other(0);
+        }
         for (int t = 0; t < tv; t += 16) {
           uint32_t r[16], s[16];
           tmem_fetch(here + t, r);
@@ -694,7 +802,16 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
           } else if (a.split > 1) {  // a part of K of the cluster's unit: its sums to the ring, which is at rest
 #pragma unroll
             for (int i = 0; i < 16; ++i) part_at[(t + i) * 32] = v[i];
+          } else if (CUT && ((head && !joined) || tail)) {
+            float* to = piece(tail) + t * 32;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) __stcg(to + i * 32, v[i]);
           } else {
+            if (CUT && joined) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] += other[i];
+              if (t + 16 < tv) fetch_other(t + 16);
+            }
             Residual<GATED> next;
             if (t + 16 < tv) fetch_residual(a, p, next, at0 + (t + 16) * a.N, min(16, tv - t - 16), ncols);
             finish<GATED>(a, p, v, bias, res, at0 + t * a.N, min(16, tv - t), ncols);
@@ -704,6 +821,23 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         if (!last) tmem_wait_st();
       }
       if (!ok) break;
+      if (CUT && works && (head || tail)) {
+        if (joined) {
+          if (lane == 0 && (!GATED || p.q < 2)) a.counters[key] = 0u;
+        } else if (arrive<GATED>(a, p, key, lane, tail ? 1u : 2u)) {
+          // the other one came while this one's sums were written: both are in the workspace
+          fetch_residual(a, p, res, at0, min(16, tv), ncols);
+          for (int t = 0; t < tv; t += 16) {
+            const float* h = piece(false) + t * 32;
+            const float* l = piece(true) + t * 32;
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __ldcg(h + i * 32) + __ldcg(l + i * 32);
+            if (t > 0) fetch_residual(a, p, res, at0 + t * a.N, min(16, tv - t), ncols);
+            finish<GATED>(a, p, v, bias, res, at0 + t * a.N, min(16, tv - t), ncols);
+          }
+        }
+      }
       if constexpr (NT <= 128) {
         if (a.split > 1 && works) {
           // the parts' sums meet: each goes out to the CTAs that add a share of the tokens each, in the order of K
@@ -760,9 +894,7 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   }
 }
 
-struct BPlan {
-  int nt, blocks, per, split, pairs;
-};
+using BPlan = decltype(Bf16GemmArgs::plan);
 constexpr int round16(int64_t n) { return static_cast<int>((n + 15) & ~int64_t(15)); }
 
 // Cycles of one 64-deep block of a tile of n tokens: the tensor core's (four MMAs of n / 2, at least 40), or bringing
@@ -770,7 +902,7 @@ constexpr int round16(int64_t n) { return static_cast<int>((n + 15) & ~int64_t(1
 constexpr int64_t block_cost(int n) { return std::max(2 * n, (128 + n / 2) * 128 / 58); }
 
 BPlan make_plan(int64_t E, int64_t R, int64_t channel_blocks, int64_t K, bool grouped) {
-  BPlan p{256, 0, 0, 1, F_MAX_CLUSTERS};
+  BPlan p{256, 0, 0, 1, F_MAX_CLUSTERS, 0};
   if (grouped) {
     const int64_t want = 2 * ((R + E - 1) / E);  // twice the mean rows of a group
     p.nt = want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
@@ -784,24 +916,32 @@ BPlan make_plan(int64_t E, int64_t R, int64_t channel_blocks, int64_t K, bool gr
   for (int per = widest; per >= 16; per -= 16) {
     const int64_t blocks = (R + per - 1) / per;
     const int64_t units = blocks * channel_blocks;
-    for (int ks = 1; ks <= F_MAX_SPLIT; ++ks) {
-      if (ks > 1 && (units > kFit[ks] || 2 * ks > KB || per > 128)) continue;
-      const int64_t waves = ks > 1 ? 1 : (units + F_MAX_CLUSTERS - 1) / F_MAX_CLUSTERS;
-      const int64_t cost = waves * ((KB + ks - 1) / ks * block_cost(per) + 300) + (ks > 1 ? 900 + 6 * per : 8 * per);
-      if (cost < best) {
-        best = cost;
-        p.per = per;
-        p.blocks = static_cast<int>(blocks);
-        p.split = ks;
-        p.pairs = static_cast<int>(ks > 1 ? units * ks : std::min<int64_t>(units, F_MAX_CLUSTERS));
-        p.nt = per <= 32 ? 32 : per <= 64 ? 64 : per <= 128 ? 128 : 256;
-      }
-    }
+    auto take = [&](int64_t cost, int ks, int cut) {
+      if (cost >= best) return;
+      best = cost;
+      p.per = per;
+      p.blocks = static_cast<int>(blocks);
+      p.split = ks;
+      p.cut = cut;
+      p.pairs = static_cast<int>(ks > 1 ? units * ks : std::min<int64_t>(units, F_MAX_CLUSTERS));
+      p.nt = per <= 32 ? 32 : per <= 64 ? 64 : per <= 128 ? 128 : 256;
+    };
+    const int64_t waves = (units + F_MAX_CLUSTERS - 1) / F_MAX_CLUSTERS;
+    take(waves * (KB * block_cost(per) + 300) + 8 * per, 1, 0);
+    // Whole units in `waves` rounds, or as many blocks a pair.  The cut units' sums go through the workspace, and pairs
+    // that are not at the same block of K at the same time share fewer of their reads in L2: about 3 us at 16 tokens a
+    // tile, 10 at 128, 19 at 256 (64 x 20480 x 7168, 80 units: 69.0 us whole, 50.0 cut; 2483 x 2048 x 7168: 59.4 and
+    // 50.4; 4096 x 4096 x 4096: 80.1 and 87.1).
+    if (units > F_MAX_CLUSTERS && units < 4 * F_MAX_CLUSTERS && units % F_MAX_CLUSTERS != 0)
+      take((units * KB + F_MAX_CLUSTERS - 1) / F_MAX_CLUSTERS * block_cost(per) + (waves + 1) * 300 + 2000 + 100 * per, 1, 1);
+    for (int ks = 2; ks <= F_MAX_SPLIT; ++ks)
+      if (units <= kFit[ks] && 2 * ks <= KB && per <= 128)
+        take((KB + ks - 1) / ks * block_cost(per) + 1200 + 6 * per, ks, 0);
   }
   return p;
 }
 
-template <int NT, bool GATED>
+template <int NT, bool GATED, bool CUT>
 cudaError_t launch_nt(const Bf16GemmArgs& g, const BArgs& a, int pairs, cudaStream_t stream) {
   using C = BCfg<NT>;
   CUtensorMap mw, mb, ms;
@@ -814,29 +954,46 @@ cudaError_t launch_nt(const Bf16GemmArgs& g, const BArgs& a, int pairs, cudaStre
   else if (!encode_map_2d(&ms, g.x, type, 2, g.R, g.K, B_BK, a.xsmall, sw)) return cudaErrorInvalidValue;
   static std::atomic<uint64_t> ready{0};
   constexpr size_t kMost = C::kSmem + (F_MAX_E + 1) * 8;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(bf16_gemm_kernel<NT, GATED>), kMost, ready);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(bf16_gemm_kernel<NT, GATED, CUT>), kMost, ready);
   if (e != cudaSuccess) return e;
-  return launch_pairs(bf16_gemm_kernel<NT, GATED>, pairs, a.split, B_THREADS, C::kSmem + (a.E + 1) * 8, stream, mw, mb,
+  return launch_pairs(bf16_gemm_kernel<NT, GATED, CUT>, pairs, a.split, B_THREADS, C::kSmem + (a.E + 1) * 8, stream, mw, mb,
                       ms, a);
 }
 
 template <bool GATED>
 cudaError_t launch_gated(int nt, const Bf16GemmArgs& g, const BArgs& a, int pairs, cudaStream_t stream) {
   switch (nt) {
-    case 32: return launch_nt<32, GATED>(g, a, pairs, stream);
-    case 64: return launch_nt<64, GATED>(g, a, pairs, stream);
-    case 128: return launch_nt<128, GATED>(g, a, pairs, stream);
-    default: return launch_nt<256, GATED>(g, a, pairs, stream);
+    case 32: return a.cut ? launch_nt<32, GATED, true>(g, a, pairs, stream) : launch_nt<32, GATED, false>(g, a, pairs, stream);
+    case 64: return a.cut ? launch_nt<64, GATED, true>(g, a, pairs, stream) : launch_nt<64, GATED, false>(g, a, pairs, stream);
+    case 128: return a.cut ? launch_nt<128, GATED, true>(g, a, pairs, stream) : launch_nt<128, GATED, false>(g, a, pairs, stream);
+    default: return a.cut ? launch_nt<256, GATED, true>(g, a, pairs, stream) : launch_nt<256, GATED, false>(g, a, pairs, stream);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_bf16_gemm(const Bf16GemmArgs& g, cudaStream_t stream) {
+size_t plan_bf16_gemm(Bf16GemmArgs& a) {
+  const int64_t width = a.act == W8A8_ACT_SWIGLU ? 128 : 256;  // channels of a tile
+  a.plan = make_plan(a.E, a.R, (a.N + width - 1) / width, a.K, a.group_list != nullptr);
+  // two pieces a pair, [2 CTAs][128 channels][tile tokens] binary32 each
+  return a.plan.cut ? kCounterBytes + static_cast<size_t>(a.plan.pairs) * 4 * B_HALF * a.plan.nt * 4 : 0;
+}
+
+size_t bf16_gemm_ws_bytes(int64_t R, int64_t N, int64_t K) {
+  Bf16GemmArgs a;
+  a.R = R;
+  a.N = N;
+  a.K = K;
+  const size_t plain = plan_bf16_gemm(a);
+  a.act = W8A8_ACT_SWIGLU;
+  return std::max(plain, plan_bf16_gemm(a));
+}
+
+cudaError_t launch_bf16_gemm(const Bf16GemmArgs& g, void* ws, cudaStream_t stream) {
   if (g.R == 0) return cudaSuccess;
   const bool grouped = g.group_list != nullptr, gated = g.act == W8A8_ACT_SWIGLU;
   const int64_t channel_blocks = (g.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
-  const BPlan p = make_plan(g.E, g.R, channel_blocks, g.K, grouped);
+  const BPlan& p = g.plan;
   if ((g.R / (grouped ? p.nt : p.per) + g.E) * channel_blocks > INT32_MAX) return cudaErrorInvalidValue;
   BArgs a;
   a.group_list = g.group_list;
@@ -850,6 +1007,9 @@ cudaError_t launch_bf16_gemm(const Bf16GemmArgs& g, cudaStream_t stream) {
   a.E = static_cast<int>(g.E);
   a.act = g.act;
   a.split = p.split;
+  a.cut = p.cut;
+  a.counters = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws));
+  a.pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
   a.blocks = p.blocks;
   a.per = p.per;
   // An accumulator's additions truncate: over the whole of K a sum comes out low by about K * 2^-30 of itself (7168:

@@ -17,7 +17,14 @@ struct Bf16GemmArgs {
   int64_t E = 1, R = 0, K = 0, N = 0;   // N: channels of y
   int act = 0;                          // W8A8_ACT_*
   bool f32 = false;                     // y is fp32
+  struct {
+    int nt, blocks, per, split, pairs, cut;
+  } plan = {};                          // plan_bf16_gemm's
 };
-cudaError_t launch_bf16_gemm(const Bf16GemmArgs& a, cudaStream_t stream);
+// Chooses the tiles and returns the scratch that they need (zero-filled once; grouped products need none).
+size_t plan_bf16_gemm(Bf16GemmArgs& a);
+// The most that a dense product of R rows to N channels asks for, gated or not.
+size_t bf16_gemm_ws_bytes(int64_t R, int64_t N, int64_t K);
+cudaError_t launch_bf16_gemm(const Bf16GemmArgs& a, void* ws, cudaStream_t stream);
 
 }  // namespace w8a8
