@@ -248,6 +248,7 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, const float (&v)[16])
 
 // The cluster's CTAs meet.  Relaxed: no data rides on it (barriers' initialisation has its own fence, and what a CTA
 // stored for others to read in global memory is complete when the grid is), so nobody waits for stores on their way.
+// What a CTA sends to a barrier or the shared memory of another one has been waited for there before they leave.
 __device__ __forceinline__ void cluster_meet() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -680,6 +681,14 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
             buf = 0;
             bphase ^= 1u;
           }
+        }
+      }
+      // Drain: the odd CTA's last arrivals on this CTA's barriers have come, so none is in flight when the pair leaves.
+      for (int i = 0; i < nacc && ok; ++i) {
+        ok = wait_for(smem_u32(&bar_acce[buf]), bphase ^ 1u, &s_abort, a.status, 9u);
+        if (++buf == nacc) {
+          buf = 0;
+          bphase ^= 1u;
         }
       }
     }
