@@ -398,3 +398,23 @@ def test_cut_tiles(M, N, K, act):
     a = W.w8a8_bf16_matmul(x2, w2, ws=ws)
     assert torch.equal(W.w8a8_bf16_matmul(x, w, b, act, r, ws=ws), bf16)
     assert torch.equal(W.w8a8_bf16_matmul(x2, w2, ws=ws), a)
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_activation_of_every_value(act):
+    """Every bf16 value through an activation, in binary32; the bound of the head, and what exp loses below 2^-126."""
+    every = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16)
+    every = torch.where(every.float().abs() >= 2.0 ** -100, every, torch.zeros_like(every))  # (normal products)
+    every = every[every.isfinite()]
+    w = torch.zeros(every.numel(), 16, dtype=torch.bfloat16, device="cuda")
+    w[:, 0] = every
+    x = torch.zeros(3, 16, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1.0
+    y = W.w8a8_bf16_matmul(x, w, activation=act, out_dtype=torch.float32)
+    v = act64(every.double(), act)
+    err = (300 * 2.0 ** -23 if act != "relu" else 0.0) * v.abs() + 2.0 ** -119
+    assert bool(((y.double() - v).abs() <= err).all()), act
+    # infinities and NaN
+    w[:3, 0] = torch.tensor([float("inf"), float("nan"), -float("inf")], device="cuda")
+    y = W.w8a8_bf16_matmul(x, w[:3].contiguous(), activation=act)
+    assert not bool(y[:, :2].isfinite().any()) and bool(y[:, 1].isnan().all())

@@ -263,3 +263,16 @@ def test_same_bits_at_every_batch(form):
     for n in (1, 7, 200, 700):
         qn, sn, _, _ = FORMS[form](x[:n], w)
         assert torch.equal(qn.view(torch.uint8), q[:n].view(torch.uint8)) and torch.equal(sn, s[:n])
+
+
+def test_residual_sum_of_every_value():
+    """All 65536 bf16 values plus 96 of them, zeros, subnormals, the largest and non-numbers among those: the binary32
+    sum rounded to bf16."""
+    every = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16)
+    some = [0, 1, 0x7f, 0x80, 0x3f80, 0x3f81, 0x4000, 0x7f7f, 0x7f80, 0x7fc0, 0x4b00, 0x2f55]
+    some += [v | 0x8000 for v in some] + torch.randint(0, 65536, (72,), generator=torch.Generator().manual_seed(3)).tolist()
+    other = torch.tensor(some, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16)
+    x, res = every.expand(96, 65536).contiguous(), other[:, None].expand(96, 65536).contiguous()
+    r = W.w8a8_rms_norm_quant(x, torch.ones(65536, device="cuda"), residual=res)[2]
+    want = (x.float() + res.float()).to(torch.bfloat16)
+    assert bool(((r.view(torch.int16) == want.view(torch.int16)) | (r.isnan() & want.isnan())).all())

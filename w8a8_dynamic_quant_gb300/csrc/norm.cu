@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<G>) norm_quant_kernel(const Nor
         uint32_t* p0 = &v[c].x;
         const uint32_t q0[4] = {res[c].x, res[c].y, res[c].z, res[c].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // one rounding: the same as that of the binary32 sum, which is exact or far from a tie
+        for (int i = 0; i < 4; ++i)  // one rounding, as of the binary32 sum, which is exact or far from a tie (all 2^32 pairs: the same)
           asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(p0[i]) : "r"(q0[i]));
         if (t + 32 * G * c < nchunk) reinterpret_cast<uint4*>(a.residual_out + at)[t + 32 * G * c] = v[c];
       }
