@@ -184,7 +184,8 @@ def test_fp32_long_sums():
 
 
 @pytest.mark.parametrize("M,N,K,act", [(5, 512, 2048, "none"), (300, 512, 256, "silu"), (64, 130, 1024, "none"),
-                                       (40, 77, 512, "swiglu"), (200, 264, 64, "swiglu")])
+                                       (40, 77, 512, "swiglu"), (200, 264, 64, "swiglu"),
+                                       (64, 20480, 2048, "none"), (33, 10200, 4096, "swiglu")])
 def test_residual_in_place(M, N, K, act):
     x, w, b, r = inputs(M, N, K, act, True, True, M + N)
     want = W.w8a8_bf16_matmul(x, w, b, act, r)
