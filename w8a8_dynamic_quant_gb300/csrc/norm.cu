@@ -12,15 +12,18 @@
 //
 // The sum decides every code of a row, so its bits must not hang on the order of the additions: squares of bf16 are
 // exact in binary32, and they are added with their rounding errors carried in a second word (Knuth's TwoSum), in the
-// threads and in the reductions.  S is the exact sum rounded once, up to a relative 2^-40 or so; every later step is one
-// rounding per element.  So the codes are those of the formula with a 64-bit sum, whatever the launch shape.
+// threads and in the reductions.  What the second word itself loses is bounded (slack()): where the two together lie so
+// close to the middle between two binary32 values that it could decide, about one row in 6000, the group adds the row's
+// squares up anew as integers.  So S is the exact sum rounded once, every later step is one rounding per element, and
+// codes and scales are functions of the row alone, whatever the launch shape.
 //
 // Bound by memory: 2 bytes in (4 with a residual), 1 out (3 with it, 2 more for y).  A row lives in the registers of G
 // warps, CH chunks of 8 values a thread; two meetings of the group (the sum; INT8 the maximum), which other rows'
-// loads hide.  8192 x 4096 with residual: INT8 40.2 us, FP8 40.8, MXFP8 39.4, 5.8 to 6.0 TB/s, 0.86 to 0.88 of the copy
+// loads hide.  8192 x 4096 with residual: INT8 39.2 us, FP8 39.8, MXFP8 38.7, 5.9 to 6.1 TB/s, 0.87 to 0.90 of the copy
 // rate; 16384 x 2048 the same.  The first form, one chunk or two a thread, six operations a square and the residual's
-// sum in binary32, issued 302 instructions a chunk and was bound by them (43.9 and 57.7 us).  One row: 2.3 us.
-// Rows of more than 32768 values spill about 400 bytes a thread (eight chunks in 64 registers).
+// sum in binary32, issued 302 instructions a chunk and was bound by them (43.9 and 57.7 us).  One row: 2.4 us.
+// Rows of more than 32768 values spill 100 to 244 bytes a thread (eight chunks in 64 registers).  What the sums' second
+// look costs, without it in brackets: 16384 x 2048 39.1 us (38.7), 8192 x 1024 11.2 (11.0), 64 x 7168 FP8 4.1 (3.9).
 #include "norm.cuh"
 
 namespace w8a8 {
@@ -67,9 +70,10 @@ __device__ __forceinline__ void two_sum2(uint64_t& s, uint64_t& c, uint64_t p) {
   c = add2(c, add2(sub2(s, sub2(t, b)), sub2(p, b)));
   s = t;
 }
-__device__ __forceinline__ void two_sum(float& s, float& c, float p) {
-  const float t = __fadd_rn(s, p), b = __fsub_rn(t, s);
-  c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(p, b)));
+// (s, e) + (so, eo).  The same bits with the two exchanged, so all lanes of a butterfly end with the same.
+__device__ __forceinline__ void two_sum(float& s, float& e, float so, float eo) {
+  const float t = __fadd_rn(s, so), b = __fsub_rn(t, s);
+  e = __fadd_rn(__fadd_rn(e, eo), __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(so, b)));
   s = t;
 }
 
@@ -97,10 +101,11 @@ __device__ __forceinline__ uint64_t wide2(uint32_t w) {
   return pk(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// The sum of the squares of a thread's values as s + e.  The sum starts at B, a power of two above the largest square,
-// and B is taken off at the end (exact: s - B is a smaller multiple of what s's last place holds).  A sum that is never
-// smaller than what is added gives its rounding error in two operations (Dekker, "A floating-point technique for
-// extending the available precision", 1971), the second an fma since squares are exact; any order of magnitudes takes six.
+// The sum of the squares of a thread's values as s + e.  The sum starts at B, the power of two of the largest square,
+// and B is taken off at the end (exact: s - B is a smaller multiple of what s's last place holds).  A sum whose exponent
+// is never below that of what is added gives its rounding error in two operations (Dekker, "A floating-point technique
+// for extending the available precision", 1971), the second an fma since squares are exact; any order of magnitudes
+// takes six.
 template <int CH>
 __device__ __forceinline__ void sum_squares(const uint4 (&v)[CH], float& s, float& e) {
   uint32_t top = 0u;
@@ -111,8 +116,7 @@ __device__ __forceinline__ void sum_squares(const uint4 (&v)[CH], float& s, floa
     for (int i = 0; i < 4; ++i) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(q[i]));
   }
   const float m = max_nan(__uint_as_float((top << 16) & 0x7fff0000u), __uint_as_float(top & 0x7fff0000u));
-  const float above = __uint_as_float((__float_as_uint(m) & 0x7f800000u) + 0x00800000u);  // 2^k > m
-  const float B = __fmul_rn(above, above);
+  const float B = __uint_as_float(__float_as_uint(__fmul_rn(m, m)) & 0x7f800000u);
   if (m < 0x1p59f) {
     uint64_t s2 = pk(B, B), c2 = 0ull;
 #pragma unroll
@@ -130,8 +134,7 @@ __device__ __forceinline__ void sum_squares(const uint4 (&v)[CH], float& s, floa
     upk(c2, e, e1);
     s = __fsub_rn(s, B);
     s1 = __fsub_rn(s1, B);
-    two_sum(s, e, s1);
-    e = __fadd_rn(e, e1);
+    two_sum(s, e, s1, e1);
   } else {  // squares near the top of binary32 or above it, infinities and NaNs
     uint64_t s2 = 0ull, c2 = 0ull;
 #pragma unroll
@@ -143,9 +146,107 @@ __device__ __forceinline__ void sum_squares(const uint4 (&v)[CH], float& s, floa
     float s1, e1;
     upk(s2, s, s1);
     upk(c2, e, e1);
-    two_sum(s, e, s1);
-    e = __fadd_rn(e, e1);
+    two_sum(s, e, s1, e1);
   }
+}
+
+// How far s + e may be from the exact sum S, relative to it.  With u = 2^-24 and n = 4 CH additions to each half of a
+// thread's pair, whose running sums, B among them, come to no more than X: every error is at most u X, the j-th addition
+// to e rounds by at most j u^2 X, and over a row the X come to at most 3 S (the B of a thread are no larger than its
+// largest square): 1.5 n (n + 1) u^2 S.  Joining the halves rounds e twice, by (6 n + 2) u^2 S at most, and each of up to
+// ten steps of the reductions twice, together by (60 n + 110) u^2 S.  Squares below 2^-126 may lose 2^-149 each, with S
+// above 2^-90 a relative 2^-43 in all.  n = 4: 406 u^2 < 2^-39; n = 16: 1576 u^2 < 2^-37; n = 32: 3808 u^2 < 2^-36.
+template <int CH>
+constexpr float slack() {
+  static_assert(CH <= 8, "the bounds above");
+  return CH == 1 ? 0x1p-39f : CH <= 4 ? 0x1p-37f : 0x1p-36f;
+}
+
+template <int G>
+__device__ __forceinline__ void meet(int grp);
+
+// The exact sum of a row's squares, rounded once to binary32; s is that sum as it was before, within a few of its last
+// places, or infinite.  A value is an integer m < 256 times 2^(E - 134), E its exponent field.  Its square is cut into
+// what is a multiple of 2^top, top 57 below s's exponent, and digits of 40 bits below that; the first parts are added up
+// as integers, which no order changes.  They decide the rounding unless they come to less than 65536 units below the
+// middle (a unit for each value that has digits left); then the next digits are added up, and so on.
+// row: K / 8 = nchunk chunks, which this thread wrote itself as far as it reads them (t, t + threads, ...).  words: two
+// a warp.
+template <int G>
+__device__ __noinline__ float exact_sum(const uint4* row, int nchunk, int t, int warp, int grp, unsigned long long* words, float s) {
+  constexpr unsigned long long kRest = 1ull << 63, kHuge = 1ull << 62;
+  const int lane = t & 31;
+  const int top = (s <= 3.4028234663852886e38f ? static_cast<int>(__float_as_uint(s) >> 23) - 127 : 145) - 57;
+  // the sum of the parts of one level; kRest: there is something below them; kHuge: squares of 2^128 and more
+  const auto level_sum = [&](int level) {
+    const int at = 268 + top - 40 * level;  // a square's m^2 stands 2 E - at places above the level's unit
+    unsigned long long sum = 0ull;
+    bool rest = false, huge = false;
+#pragma unroll 2
+    for (int c = t; c < nchunk; c += 32 * G) {
+      const uint4 v = row[c];
+      const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t b = (q[i >> 1] >> (16 * (i & 1))) & 0x7fffu;
+        const uint32_t m = b >= 128u ? (b & 127u) | 128u : b;
+        const int sh = 2 * max(static_cast<int>(b >> 7), 1) - at;
+        huge = huge || b >= 191u << 7;  // 2^64
+        if (sh >= 0) {
+          const unsigned long long part = static_cast<unsigned long long>(m * m) << min(sh, 63);
+          sum += level == 0 ? part : sh < 40 ? part & ((1ull << 40) - 1) : 0ull;
+        } else {
+          const int r = min(-sh, 31);
+          sum += (m * m) >> r;
+          rest = rest || ((m * m) & ((1u << r) - 1u)) != 0u;
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (__any_sync(0xffffffffu, rest)) sum |= kRest;
+    if (__any_sync(0xffffffffu, huge)) sum |= kHuge;
+    if constexpr (G > 1) {
+      unsigned long long* w = words + (level & 1) * G;  // (the other half is read until the next level's barrier)
+      if (lane == 0) w[warp] = sum;
+      meet<G>(grp);
+      unsigned long long all = 0ull, flags = 0ull;
+      for (int i = 0; i < G; ++i) {
+        all += w[i] & (kHuge - 1);
+        flags |= w[i] & (kRest | kHuge);
+      }
+      sum = all | flags;
+    }
+    return sum;
+  };
+  unsigned long long w = level_sum(0);
+  if ((w & kHuge) != 0ull) return s;
+  bool rest = (w & kRest) != 0ull;
+  w &= kHuge - 1;
+  // exponent of the result's last place; 32 to 36 bits of w lie below it
+  const int lsb = max(64 - __clzll(static_cast<long long>(w)) - 24 + top, -149);
+  const int shift = lsb - top;
+  unsigned long long q = w >> shift;
+  const unsigned long long below = w & ((1ull << shift) - 1), half = 1ull << (shift - 1);
+  if (below >= half) {
+    q += below > half || rest || (q & 1ull) != 0ull ? 1ull : 0ull;
+  } else {
+    unsigned long long gap = half - below;
+    for (int level = 1; rest && gap < 65536ull; ++level) {
+      gap <<= 40;
+      w = level_sum(level);
+      rest = (w & kRest) != 0ull;
+      w &= kHuge - 1;
+      if (w >= gap) {
+        q += w > gap || rest || (q & 1ull) != 0ull ? 1ull : 0ull;
+        break;
+      }
+      gap -= w;
+    }
+  }
+  // (with lsb = -149 q may be below 2^23, a number without the leading bit: the same bits)
+  const long long bits = (static_cast<long long>(lsb + 150) << 23) + static_cast<long long>(q) - (1ll << 23);
+  return __uint_as_float(static_cast<uint32_t>(min(bits, 0x7f800000ll)));
 }
 
 // 16 bytes read once.  Not the read-only path: residual_out may be x or residual itself.
@@ -272,11 +373,17 @@ __device__ __forceinline__ float group_max(float m, float* red, int grp, int w, 
 template <int G>
 constexpr int kCtaWarps = G > 4 ? G : 4;
 
+// CTAs a SM that the registers have to allow: all 64 warps with a chunk a thread, 36 with four (CTAs of four warps; larger
+// ones 32).  exact_sum() alone would take more registers, and spills its own in that case.
+template <int CH, int G>
+constexpr int kCtas = CH == 1 ? 64 / kCtaWarps<G> : G <= 4 ? 9 : 32 / G;
+
 template <int FORM, int CH, int G>
-__global__ void __launch_bounds__(32 * kCtaWarps<G>) norm_quant_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(32 * kCtaWarps<G>, kCtas<CH, G>) norm_quant_kernel(const NormArgs a) {
   constexpr int kWarps = kCtaWarps<G>;
   constexpr int NG = kWarps / G;
   __shared__ float red_s[kWarps], red_c[kWarps], red_m[kWarps], red_n[kWarps];
+  __shared__ unsigned long long words[2 * kWarps];
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int warp = static_cast<int>(threadIdx.x >> 5);
@@ -318,8 +425,7 @@ __global__ void __launch_bounds__(32 * kCtaWarps<G>) norm_quant_kernel(const Nor
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float so = __shfl_xor_sync(0xffffffffu, s, o), eo = __shfl_xor_sync(0xffffffffu, e, o);
-    two_sum(s, e, so);
-    e = __fadd_rn(e, eo);
+    two_sum(s, e, so, eo);
   }
   if constexpr (G > 1) {
     if (lane == 0) {
@@ -332,12 +438,21 @@ __global__ void __launch_bounds__(32 * kCtaWarps<G>) norm_quant_kernel(const Nor
 #pragma unroll
     for (int o = G / 2; o > 0; o >>= 1) {
       const float so = __shfl_xor_sync(0xffffffffu, s, o), eo = __shfl_xor_sync(0xffffffffu, e, o);
-      two_sum(s, e, so);
-      e = __fadd_rn(e, eo);
+      two_sum(s, e, so, eo);
     }
   }
-  // (a sum past the largest binary32 value is infinite, and what it lost is no number)
-  const float sum = fabsf(s) <= 3.4028234663852886e38f ? __fadd_rn(s, e) : s;
+  // S: s + e rounded where what e lost cannot change it, else the exact sum.  Below 2^-88 a sum counts only beside an eps
+  // that is as small.  (All threads of a group have the same s and e, and go the same way.)
+  float sum = s;
+  bool sure = a.eps >= 0x1p-60f || s != s;
+  if (s >= 0x1p-89f) {
+    const float lost = __fmul_ru(s, slack<CH>());
+    sum = __fadd_rn(s, __fsub_rd(e, lost));
+    sure = sum == __fadd_rn(s, __fadd_ru(e, lost));
+  }
+  if (!sure)
+    sum = exact_sum<G>(reinterpret_cast<const uint4*>((a.residual != nullptr ? a.residual_out : a.x) + at), nchunk, t, w, grp,
+                       words + 2 * G * grp, s);
   const float g = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(a.K)), a.eps));
 
   // -v = (r * -g) * w
