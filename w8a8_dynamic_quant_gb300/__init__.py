@@ -784,7 +784,7 @@ def _rms_norm(name, x, weight, eps, residual, want_y, q, scale, residual_out, y,
     dev, device = x.get_device(), x.device
     if not (dev >= 0 and x.dtype is _BF16 and x.is_contiguous()):
         _check(x, "x", _BF16, (M, K), dev)
-    f32 = type(weight) is _Tensor and weight.dtype is _F32
+    f32 = isinstance(weight, _Tensor) and weight.dtype is _F32  # (a Parameter too)
     _check(weight, "weight", _F32 if f32 else _BF16, (K,), dev)
     r_ptr = out_ptr = y_ptr = None
     if residual is not None:
