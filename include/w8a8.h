@@ -390,8 +390,10 @@ W8A8_API w8a8_status moe_gate_topk(const void* logits, int64_t T, int64_t E, con
 /* be shorter: ceil(K/128) scales a row, ceil(N/128) x ceil(K/128) a weight. */
 /* Weights are used as they lie in a checkpoint; there is nothing to pack.   */
 /* One workspace may serve FP8 calls of different sizes in turn, but not the */
-/* other calls as well (they lay theirs out differently).  After a device    */
-/* timeout zero-fill it again.  w8a8_last_engine() is W8A8_ENGINE_TC.        */
+/* other calls as well (they lay theirs out differently).  What they ask for */
+/* does not grow in step with the rows (the most is in the middle): it has   */
+/* the size of the largest of theirs.  After a device timeout zero-fill it   */
+/* again.  w8a8_last_engine() is W8A8_ENGINE_TC.                             */
 /* ------------------------------------------------------------------------ */
 
 /* x [M,K] bf16 -> q [M,K] E4M3 bytes, scale [M, ceil(K/128)] fp32: per block
@@ -525,7 +527,9 @@ W8A8_API w8a8_status w8a8_mx_rms_norm_quant(const uint16_t* x, const uint16_t* r
 /* K % 16 == 0; x and w 16-byte aligned; any N (rows of y that start on      */
 /* 16-byte boundaries are stored faster).  residual may be y itself (bf16),  */
 /* no other tensors may overlap.  One workspace may serve bf16 products of   */
-/* different sizes in turn; after a device timeout zero-fill it again.       */
+/* different sizes in turn, but not the other calls as well (they lay theirs */
+/* out differently).  Only its first W8A8_BF16_ZERO_BYTES need to be zero;   */
+/* after a device timeout zero them again.                                   */
 /* w8a8_last_engine() is W8A8_ENGINE_TC.                                     */
 /* ------------------------------------------------------------------------ */
 
@@ -539,7 +543,14 @@ enum {
 };
 #define W8A8_MM_F32 1u /* y is fp32 */
 
+#define W8A8_BF16_ZERO_BYTES 5120 /* of a workspace: the status word and the arrival counters */
+
+/* A workspace of this size serves every dense product of at most M rows to at most N channels, plain or gated, whatever
+ * its K. */
 W8A8_API size_t w8a8_bf16_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* The least that one product of exactly these sizes takes: W8A8_STATUS_BYTES for most. */
+W8A8_API size_t w8a8_bf16_matmul_call_bytes(int64_t M, int64_t N, int64_t K, int act);
 
 /* x [M,K] bf16, w [N,K] bf16 ([2N,K] for SWIGLU), bias [rows of w] bf16 or NULL, residual [M,N] bf16 or NULL
  * -> y [M,N] bf16 or fp32. */

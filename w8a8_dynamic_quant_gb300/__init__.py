@@ -7,7 +7,8 @@ the library's CUDA kernels; nothing here computes, and there is no fallback.
 
 BF16 tensors are torch.bfloat16; INT8 tensors torch.int8; scales float32;
 group lists int64 (on the device).  Workspaces are zero-filled uint8 device
-tensors that can be reused across calls on one stream.
+tensors that can be reused across calls of one kind on one stream: the int8
+products and layers of one shape, the FP8 calls, or the bf16 products.
 """
 from __future__ import annotations
 
@@ -868,6 +869,7 @@ def _out_dtype(dtype, y):
 
 
 def bf16_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
+    """The bytes of a workspace for every w8a8_bf16_matmul of at most M rows to at most N channels, whatever its K."""
     return _size("w8a8_bf16_matmul_workspace_bytes", M, N, K)
 
 
@@ -879,7 +881,7 @@ def w8a8_bf16_matmul(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tens
     activation: "none", "relu", "silu", "gelu", "gelu_tanh", or "swiglu" with w [2N,K] (the gate's rows, then the up
     projection's; bias [2N]): silu(gate) * up.  bias bf16 [rows of w], residual bf16 [M,N] (y itself is allowed).  The
     layers that a quantised model keeps in bf16; with out_dtype float32 the router's logits.  Keep a workspace (`ws`)
-    over calls: without one every call zero-fills its own."""
+    over calls, one for the largest batch serves the smaller ones: without one every call zeroes its own."""
     M, K = _dims(x, "x", 2)
     rows = _dims(w, "w", 2)[0]
     dev, act = x.get_device(), _activation(activation)
@@ -896,7 +898,11 @@ def w8a8_bf16_matmul(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tens
         _check(bias, "bias", _BF16, (rows,), dev)
     if residual is not None:
         _check(residual, "residual", _BF16, (M, N), dev)
-    ws = _check_ws(ws, lambda: bf16_matmul_workspace_bytes(M, N, K), dev)
+    if ws is None:  # what this call needs, of which only the status word and the counters have to be zero
+        ws = _empty(max(_size("w8a8_bf16_matmul_call_bytes", M, N, K, act), 256), dtype=torch.uint8, device=x.device)
+        (ws[:_capi.BF16_ZERO_BYTES] if ws.numel() > _capi.BF16_ZERO_BYTES else ws).zero_()
+    else:
+        _check_ws(ws, None, dev)
     out_dtype = _out_dtype(out_dtype, y)
     if y is None:
         y = _empty((M, N), dtype=out_dtype, device=x.device)

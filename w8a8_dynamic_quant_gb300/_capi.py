@@ -60,6 +60,7 @@ SIGNATURES = {
     **{n: (_int, [_vp, _vp, _vp, _i64, _i64, ctypes.c_float, _u32, _vp, _vp, _vp, _vp, _vp])
        for n in ("w8a8_rms_norm_quant", "w8a8_fp8_rms_norm_quant", "w8a8_mx_rms_norm_quant")},
     "w8a8_bf16_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "w8a8_bf16_matmul_call_bytes": (_sz, [_i64, _i64, _i64, _int]),
     "w8a8_bf16_matmul": (_int, [_vp, _i64, _i64, _vp, _i64, _vp, _int, _vp, _u32, _vp, _vp, _sz, _vp]),
     "w8a8_bf16_grouped_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
     "w8a8_bf16_grouped_matmul": (_int, [_vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _int, _u32, _vp, _vp, _sz, _vp]),
@@ -81,6 +82,7 @@ PACK_F16 = 2
 NORM_WEIGHT_F32 = 1
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5}
 MM_F32 = 1
+BF16_ZERO_BYTES = 5120
 
 _lib = None
 _lock = threading.Lock()

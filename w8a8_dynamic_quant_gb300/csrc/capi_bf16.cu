@@ -38,9 +38,11 @@ w8a8_status norm_common(int form, const uint16_t* x, const uint16_t* residual, c
   return cuda_status(launch_norm_quant(a, form, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// (a tile's last rows lie up to 255 past the tensor's: their coordinates are 32-bit integers)
+constexpr int64_t kMaxRows = INT32_MAX - 256;
+static_assert(kStatusBytes + kBf16CounterBytes == W8A8_BF16_ZERO_BYTES, "what of a workspace has to be zero");
+
 w8a8_status matmul_common(Bf16GemmArgs& a, uint32_t flags, void* ws, size_t ws_bytes, w8a8_stream_t stream) {
-  // (a tile's last rows lie up to 255 past the tensor's: their coordinates are 32-bit integers)
-  constexpr int64_t kMaxRows = INT32_MAX - 256;
   if (a.E <= 0 || a.E > kMaxE || a.R < 0 || a.R > kMaxRows || a.act < W8A8_ACT_NONE || a.act > W8A8_ACT_SWIGLU ||
       (flags & ~W8A8_MM_F32) != 0u)
     return W8A8_ERR_SHAPE;
@@ -82,7 +84,19 @@ w8a8_status w8a8_mx_rms_norm_quant(const uint16_t* x, const uint16_t* residual, 
 }
 
 size_t w8a8_bf16_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return M < 0 || N <= 0 || K <= 0 ? 0 : kStatusBytes + bf16_gemm_ws_bytes(M, N, K);
+  return M < 0 || N <= 0 || K <= 0 ? 0 : kStatusBytes + bf16_gemm_ws_bytes(M, N);
+}
+
+size_t w8a8_bf16_matmul_call_bytes(int64_t M, int64_t N, int64_t K, int act) {
+  if (M < 0 || M > kMaxRows || N <= 0 || N > kMaxRows || K <= 0 || K > W8A8_MAX_K || act < W8A8_ACT_NONE ||
+      act > W8A8_ACT_SWIGLU)
+    return 0;
+  Bf16GemmArgs a;
+  a.R = M;
+  a.N = N;
+  a.K = K;
+  a.act = act;
+  return kStatusBytes + (M == 0 ? 0 : plan_bf16_gemm(a));
 }
 
 size_t w8a8_bf16_grouped_matmul_workspace_bytes(int64_t E, int64_t R, int64_t N, int64_t K) {

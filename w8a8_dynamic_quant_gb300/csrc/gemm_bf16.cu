@@ -924,6 +924,13 @@ constexpr int round16(int64_t n) { return static_cast<int>((n + 15) & ~int64_t(1
 // 128 weight rows and n / 2 token rows of 128 bytes to a SM at about 58 bytes a cycle.
 constexpr int64_t block_cost(int n) { return std::max(2 * n, (128 + n / 2) * 128 / 58); }
 
+// The accumulator's columns for blocks of `per` tokens.
+constexpr int tile_of(int per) { return per <= 32 ? 32 : per <= 64 ? 64 : per <= 128 ? 128 : 256; }
+
+// Scratch of cut units: the counters, and two pieces a pair, [2 CTAs][128 channels][tile tokens] binary32 each.
+constexpr size_t cut_bytes(int pairs, int nt) { return kBf16CounterBytes + static_cast<size_t>(pairs) * 4 * B_HALF * nt * 4; }
+static_assert(kBf16CounterBytes == kCounterBytes, "[pairs][2 CTAs][epilogue warps]");
+
 BPlan make_plan(int64_t E, int64_t R, int64_t channel_blocks, int64_t K, bool grouped) {
   BPlan p{256, 0, 0, 1, F_MAX_CLUSTERS, 0};
   if (grouped) {
@@ -947,7 +954,7 @@ BPlan make_plan(int64_t E, int64_t R, int64_t channel_blocks, int64_t K, bool gr
       p.split = ks;
       p.cut = cut;
       p.pairs = static_cast<int>(ks > 1 ? units * ks : std::min<int64_t>(units, F_MAX_CLUSTERS));
-      p.nt = per <= 32 ? 32 : per <= 64 ? 64 : per <= 128 ? 128 : 256;
+      p.nt = tile_of(per);
     };
     const int64_t waves = (units + F_MAX_CLUSTERS - 1) / F_MAX_CLUSTERS;
     take(waves * (KB * block_cost(per) + 300) + 8 * per, 1, 0);
@@ -998,18 +1005,19 @@ cudaError_t launch_gated(int nt, const Bf16GemmArgs& g, const BArgs& a, int pair
 size_t plan_bf16_gemm(Bf16GemmArgs& a) {
   const int64_t width = a.act == W8A8_ACT_SWIGLU ? 128 : 256;  // channels of a tile
   a.plan = make_plan(a.E, a.R, (a.N + width - 1) / width, a.K, a.group_list != nullptr);
-  // two pieces a pair, [2 CTAs][128 channels][tile tokens] binary32 each
-  return a.plan.cut ? kCounterBytes + static_cast<size_t>(a.plan.pairs) * 4 * B_HALF * a.plan.nt * 4 : 0;
+  return a.plan.cut ? cut_bytes(a.plan.pairs, a.plan.nt) : 0;
 }
 
-size_t bf16_gemm_ws_bytes(int64_t R, int64_t N, int64_t K) {
-  Bf16GemmArgs a;
-  a.R = R;
-  a.N = N;
-  a.K = K;
-  const size_t plain = plan_bf16_gemm(a);
-  a.act = W8A8_ACT_SWIGLU;
-  return std::max(plain, plan_bf16_gemm(a));
+size_t bf16_gemm_ws_bytes(int64_t R, int64_t N) {
+  // make_plan() cuts only between F_MAX_CLUSTERS and 4 F_MAX_CLUSTERS units: what the widest tile that R rows (fewer, with
+  // fewer channels, no wider one) can be cut into so many with takes, be that plan chosen or not
+  const int64_t channel_blocks = std::min<int64_t>((std::min<int64_t>(N, INT32_MAX) + 127) / 128, 4 * F_MAX_CLUSTERS - 1);
+  const int64_t least = F_MAX_CLUSTERS / channel_blocks + 1;  // token blocks
+  const int64_t rows = std::min<int64_t>(R, 4 * F_MAX_CLUSTERS * 256);
+  int64_t per = std::min<int64_t>(256, round16(rows));
+  if (least > 1) per = std::min(per, (rows - 1) / (least - 1) & ~int64_t(15));
+  if (rows == 0 || per < 16) return 0;
+  return cut_bytes(F_MAX_CLUSTERS, tile_of(static_cast<int>(per)));
 }
 
 cudaError_t launch_bf16_gemm(const Bf16GemmArgs& g, void* ws, cudaStream_t stream) {

@@ -21,10 +21,11 @@ struct Bf16GemmArgs {
     int nt, blocks, per, split, pairs, cut;
   } plan = {};                          // plan_bf16_gemm's
 };
-// Chooses the tiles and returns the scratch that they need (zero-filled once; grouped products need none).
+// Chooses the tiles and returns the scratch that they need (its counters zero-filled once; grouped products need none).
 size_t plan_bf16_gemm(Bf16GemmArgs& a);
-// The most that a dense product of R rows to N channels asks for, gated or not.
-size_t bf16_gemm_ws_bytes(int64_t R, int64_t N, int64_t K);
+constexpr size_t kBf16CounterBytes = 4864;  // at the scratch's start
+// The most that a dense product of up to R rows to up to N channels asks for, gated or not, whatever its K.
+size_t bf16_gemm_ws_bytes(int64_t R, int64_t N);
 cudaError_t launch_bf16_gemm(const Bf16GemmArgs& a, void* ws, cudaStream_t stream);
 
 }  // namespace w8a8
