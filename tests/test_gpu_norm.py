@@ -66,7 +66,8 @@ def check(form, x, weight, eps=1e-6, residual=None, want_y=False):
         assert y is None
 
 
-# one chunk; groups of 1, 2, 4, 8 and 32 warps; two, four and eight chunks a thread; rows that end inside a group of each
+# groups of 1 to 32 warps with one chunk a thread, above 8192 values four and eight; rows that end inside a group of each
+# (four chunks of shorter rows take more of them: test_gpu_norm_arms.py)
 SIZES = [(1, 32), (3, 160), (5, 256), (7, 288), (9, 512), (130, 1024), (33, 1504), (400, 2016), (5, 2080), (400, 4096),
          (700, 2176), (310, 7168), (64, 7168), (400, 8192), (3, 8224), (11, 16384), (2, 17408), (3, 32768), (2, 65536)]
 
