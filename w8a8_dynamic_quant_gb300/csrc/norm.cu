@@ -556,12 +556,10 @@ __global__ void __launch_bounds__(32 * kCtaWarps<G>, kCtas<CH, G>) norm_quant_ke
         }
       } else {
         nan = (__ballot_sync(0xffffffffu, nan) >> (lane & ~3) & 15u) != 0u;
-        // floor(log2 m) - 8 of the largest magnitude, within E8M0's range (subnormal m: far below it)
-        const uint32_t bits = __float_as_uint(m);
-        const int field = static_cast<int>(bits >> 23);
-        const int shared = max(-127, field - 127 - 8);  // field <= 254, or 255 for an infinity
-        const int sh = min(127, shared);
-        const float inv = sh < 127 ? __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) : __uint_as_float(0x00400000u);
+        // floor(log2 m) - 8 of the largest magnitude: at most 120, an infinity's, and no less than E8M0's lowest (m below
+        // 2^-119)
+        const int sh = max(-127, static_cast<int>(__float_as_uint(m) >> 23) - 127 - 8);
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
         const uint64_t inv2 = pk(-inv, -inv);
         uint32_t k[4];
 #pragma unroll
