@@ -781,7 +781,9 @@ bf16_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
         for (int i = 0; i < 16; ++i) other[i] = __ldcg(from + i * 32);
       };
       if (joined) fetch_other(0);
-      const uint32_t sum_at = lane_addr + C::kSumCol + c0;
+      // The sums over chunks of K: columns of its own for each half (c0 = 0 is the first), whatever n is.  The other half may
+      // be at a unit of another n, whose halves meet elsewhere.
+      const uint32_t sum_at = lane_addr + (c0 != 0 ? C::kSumCol + C::kCols : C::kSumCol);
       bool ok = true;
       for (int k0 = kb0; k0 < kb1; k0 += chunk) {
         ok = wait_for(smem_u32(&bar_accf[buf]), bphase, &s_abort, a.status, 4u);
