@@ -537,7 +537,7 @@ enum {
   W8A8_ACT_NONE = 0,
   W8A8_ACT_RELU = 1,
   W8A8_ACT_SILU = 2,      /* v / (1 + exp(-v)) */
-  W8A8_ACT_GELU = 3,      /* v * Phi(v) */
+  W8A8_ACT_GELU = 3,      /* v * Phi(v); 0 for -infinity, where the others but RELU give NaN */
   W8A8_ACT_GELU_TANH = 4, /* v / (1 + exp(-2u)), u = sqrt(2/pi) (v + 0.044715 v^3) */
   W8A8_ACT_SWIGLU = 5     /* silu(gate) * up */
 };

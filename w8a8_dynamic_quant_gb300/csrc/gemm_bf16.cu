@@ -32,14 +32,14 @@
 // sizes alone, from the costs at make_plan().
 //
 // What bounds it.  Many tokens: the tensor cores, under the power cap when called without a pause (8192 x 14336 x 4096
-// with gelu_tanh 556 us at 1.5 GHz, 490 in a burst; the library's product alone 557 and 478).  Tiles of fewer than about
+// with gelu_tanh 563 to 569 us at 1.5 GHz, 485 to 493 in a burst; the library's product alone 557 and 478 to 497).  Tiles of fewer than about
 // 230 tokens: bringing 128 weight rows and half the token rows of a block to each SM, about 58 bytes a cycle, where the
 // MMAs would take twice that at 128 tokens (1141 x 4096 x 4096: 32.5 us).  Few tokens: the weight stream (128 tokens to
 // 8 of 64 experts of 4096 x 7168: 541 us, 7.0 TB/s) or, for one small layer, latency: of the 10.7 us of 64 x 2048 x 7168
 // the stream takes 4.3, the way of the first tiles 1.5, the parts' meeting and the epilogue 2, launch and end 2.
 // Small K: the epilogue, 3.7 us a tile of 256 tokens (5.8 with a residual).
 //
-// Registers: 147 to 168 of the 168 that 320 threads may have, none spilled.
+// Registers: 145 to 168 of the 168 that 320 threads may have, none spilled.
 //
 // Every mbarrier wait is bounded (2 s): on expiry the CTA sets W8A8_ERR_DEVICE_TIMEOUT, lets in-flight copies land,
 // frees TMEM and returns.
@@ -923,7 +923,8 @@ using BPlan = decltype(Bf16GemmArgs::plan);
 constexpr int round16(int64_t n) { return static_cast<int>((n + 15) & ~int64_t(15)); }
 
 // Cycles of one 64-deep block of a tile of n tokens: the tensor core's (four MMAs of n / 2, at least 40), or bringing
-// 128 weight rows and n / 2 token rows of 128 bytes to a SM at about 58 bytes a cycle.
+// 128 weight rows and n / 2 token rows of 128 bytes to a SM at about 58 bytes a cycle.  (The memory's rate is not in it: it
+// bounds few tokens' products alike whichever way they are tiled.)
 constexpr int64_t block_cost(int n) { return std::max(2 * n, (128 + n / 2) * 128 / 58); }
 
 // The accumulator's columns for blocks of `per` tokens.
@@ -936,7 +937,12 @@ static_assert(kBf16CounterBytes == kCounterBytes, "[pairs][2 CTAs][epilogue warp
 BPlan make_plan(int64_t E, int64_t R, int64_t channel_blocks, int64_t K, bool grouped) {
   BPlan p{256, 0, 0, 1, F_MAX_CLUSTERS, 0};
   if (grouped) {
-    const int64_t want = 2 * ((R + E - 1) / E);  // twice the mean rows of a group
+    // Twice the mean rows of a group: the host knows no more of the list.  Each group's weights are read once a tile of its
+    // rows.  64 experts of 2 x 2048 x 4096, top-8 by a zipf rule, tiles of 32 / 64 / 128 / 256 in us: 256 tokens (mean 32,
+    // most 243) 382 / 337 / 326 / 328, 1024 tokens (128, 963) 913 / 575 / 420 / 359, 4096 (512, 3814) 3309 / 1781 / 1046 /
+    // 741.  128 tokens alike (mean 16), 2 x 2048 x 7168: 541 / 544 / 550 / 566.  It is wrong where one expert has nearly all
+    // rows: 1024 of 1024 in one of 64, 4096 x 4096: 100 / 60 / 34 / 27.
+    const int64_t want = 2 * ((R + E - 1) / E);
     p.nt = want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
     return p;
   }

@@ -22,7 +22,7 @@
 // loads hide.  8192 x 4096 with residual: INT8 39.2 us, FP8 39.8, MXFP8 38.7, 5.9 to 6.1 TB/s, 0.87 to 0.90 of the copy
 // rate; 16384 x 2048 the same.  The first form, one chunk or two a thread, six operations a square and the residual's
 // sum in binary32, issued 302 instructions a chunk and was bound by them (43.9 and 57.7 us).  One row: 2.4 us.
-// Rows of more than 32768 values spill 100 to 244 bytes a thread (eight chunks in 64 registers).  What the sums' second
+// Rows of more than 32768 values spill 108 to 244 bytes a thread (eight chunks in 64 registers).  What the sums' second
 // look costs, without it in brackets: 16384 x 2048 39.1 us (38.7), 8192 x 1024 11.2 (11.0), 64 x 7168 FP8 4.1 (3.9).
 #include "norm.cuh"
 
@@ -412,7 +412,9 @@ __global__ void __launch_bounds__(32 * kCtaWarps<G>, kCtas<CH, G>) norm_quant_ke
         uint32_t* p0 = &v[c].x;
         const uint32_t q0[4] = {res[c].x, res[c].y, res[c].z, res[c].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // one rounding, as of the binary32 sum, which is exact or far from a tie (all 2^32 pairs: the same)
+        for (int i = 0; i < 4; ++i)
+          // One rounding, the bits of the binary32 sum rounded to bf16: rounding to p bits by way of 2 p + 2 or more changes
+          // no sum (Figueroa, "When is double rounding innocuous?", 1995), here 8 by way of 24.
           asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(p0[i]) : "r"(q0[i]));
         if (t + 32 * G * c < nchunk) reinterpret_cast<uint4*>(a.residual_out + at)[t + 32 * G * c] = v[c];
       }
