@@ -63,3 +63,27 @@ def test_smaller_products_on_a_large_workspace():
             del junk
             assert torch.equal(W.w8a8_bf16_matmul(x, w[:rows], activation=act), want)
     assert W.read_device_status(ws) == 0 and not bool(ws[:5120].any())
+
+
+@pytest.mark.gpu
+def test_graphs_of_calls_without_a_workspace():
+    """A captured call without a workspace zeroes its own at every replay; two such graphs share the capture's memory."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    pool, graphs = None, []
+    for M, N, K, act in ((64, 20480, 1024, "none"), (33, 10200, 1040, "swiglu")):
+        x = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+        w = (torch.randn(2 * N if act == "swiglu" else N, K, generator=g, device="cuda") * K ** -0.5).to(torch.bfloat16)
+        y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        W.w8a8_bf16_matmul(x, w, activation=act, y=y)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, pool=pool):
+            W.w8a8_bf16_matmul(x, w, activation=act, y=y)
+            W.w8a8_bf16_matmul(x, w, activation=act, y=y)
+        pool = pool or graph.pool()
+        graphs.append((graph, x, w, act, y))
+    for _ in range(5):
+        for graph, x, w, act, y in graphs:
+            x.mul_(1.25)
+            y.zero_()
+            graph.replay()
+            assert torch.equal(y, W.w8a8_bf16_matmul(x, w, activation=act))
